@@ -181,7 +181,7 @@ def _mxfp4(x, rule):
     e = e.clamp(min=-127)
     a = b.abs() * _pow2(-e).unsqueeze(-1)
     c = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0)
-         + 8 * torch.signbit(b)).view(x.shape)
+         + 8 * torch.signbit(b).to(torch.uint8)).view(x.shape)
     return c[:, 0::2] | (c[:, 1::2] << 4), (e + 127).to(torch.uint8)
 
 
