@@ -47,7 +47,7 @@ const char* mxq_status_string(int status)
     case MXQ_ERR_WORKSPACE: return "MXQ_ERR_WORKSPACE: workspace missing or too small";
     case MXQ_ERR_HIP: return "MXQ_ERR_HIP: a HIP runtime call failed";
     case MXQ_ERR_NOT_IMPLEMENTED: return "MXQ_ERR_NOT_IMPLEMENTED";
-    case MXQ_ERR_DTYPE: return "MXQ_ERR_DTYPE: unknown output data type";
+    case MXQ_ERR_DTYPE: return "MXQ_ERR_DTYPE: unknown data type or format";
     case MXQ_ERR_RULE: return "MXQ_ERR_RULE: unknown scale rule or flag";
     default: return "unknown mxq_status";
     }
@@ -313,6 +313,190 @@ mxq_status mxq_scaled_grouped_mm_packed(const void* packed, const void* wq_e4m3,
     return hip_status(mxq::launch_grouped_mm_strided(base, base + K, ldp, ldp, wq_e4m3, ws_e8m0, group_end_offs,
                                                      (int)M, (int)N, (int)K, (int)G, y, out_dtype == MXQ_OUT_F32,
                                                      workspace, (hipStream_t)stream));
+}
+
+// ------------------------------------------------------------------ MXFP4 ---
+static mxq_status check_mxfp4(const void* a, const void* q, const void* s, int64_t M, int64_t K)
+{
+    mxq_status st = check_2d(M, K);
+    if (st != MXQ_OK) return st;
+    if (K % 32 != 0) return MXQ_ERR_SHAPE;
+    if (M == 0 || K == 0) return MXQ_OK;
+    if (!a || !q || !s) return MXQ_ERR_NULL;
+    if (!aligned16(a) || !aligned16(q) || !aligned16(s)) return MXQ_ERR_ALIGN;
+    return MXQ_OK;
+}
+
+mxq_status mxq_quantize_mxfp4(const void* x_bf16, int64_t M, int64_t K, int rule, void* q_e2m1, void* s_e8m0,
+                              void* stream)
+{
+    const mxq_status st = check_mxfp4(x_bf16, q_e2m1, s_e8m0, M, K);
+    if (st == MXQ_ERR_SHAPE) return st;
+    if (rule != MXQ_SCALE_FLOOR && rule != MXQ_SCALE_RCEIL) return MXQ_ERR_RULE;
+    if (st != MXQ_OK || M == 0 || K == 0) return st;
+    return hip_status(mxq::launch_mxfp4_quantize(x_bf16, M, K, q_e2m1, s_e8m0, rule == MXQ_SCALE_RCEIL,
+                                                 (hipStream_t)stream));
+}
+
+mxq_status mxq_dequantize_mxfp4(const void* q_e2m1, const void* s_e8m0, int64_t M, int64_t K, void* y_bf16,
+                                void* stream)
+{
+    const mxq_status st = check_mxfp4(y_bf16, q_e2m1, s_e8m0, M, K);
+    if (st != MXQ_OK || M == 0 || K == 0) return st;
+    return hip_status(mxq::launch_mxfp4_dequantize(q_e2m1, s_e8m0, M, K, y_bf16, (hipStream_t)stream));
+}
+
+static mxq_status check_mxfp4_mm_sizes(int64_t M, int64_t N, int64_t K, int64_t G)
+{
+    if (M < 0 || N < 0 || K <= 0) return MXQ_ERR_SHAPE;
+    return mxq::mxfp4_mm_sizes_ok(M, N, K, G) ? MXQ_OK : MXQ_ERR_SHAPE;
+}
+
+size_t mxq_mxfp4_grouped_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t G)
+{
+    if (check_mxfp4_mm_sizes(M, N, K, G) != MXQ_OK) return 0;
+    return mxq::mxfp4_mm_workspace_bytes(M, N, G);
+}
+
+mxq_status mxq_mxfp4_grouped_mm(const void* xq, const void* xs_e8m0, int x_format, const void* wq_e2m1,
+                                const void* ws_e8m0, const int32_t* group_end_offs, int64_t M, int64_t N, int64_t K,
+                                int32_t G, int out_dtype, void* y, void* workspace, size_t workspace_bytes,
+                                void* stream)
+{
+    const mxq_status st = check_mxfp4_mm_sizes(M, N, K, G);
+    if (st != MXQ_OK) return st;
+    if (x_format != MXQ_FMT_E4M3 && x_format != MXQ_FMT_E2M1) return MXQ_ERR_DTYPE;
+    if (out_dtype != MXQ_OUT_BF16 && out_dtype != MXQ_OUT_F32) return MXQ_ERR_DTYPE;
+    if (M == 0 || N == 0) return MXQ_OK;
+    if (!xq || !xs_e8m0 || !wq_e2m1 || !ws_e8m0 || !group_end_offs || !y) return MXQ_ERR_NULL;
+    if (!aligned16(xq) || !aligned16(xs_e8m0) || !aligned16(wq_e2m1) || !aligned16(ws_e8m0) || !aligned16(y))
+        return MXQ_ERR_ALIGN;
+    if (((uintptr_t)group_end_offs & 3u) != 0) return MXQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes < mxq::mxfp4_mm_workspace_bytes(M, N, G)) return MXQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
+    const bool x8 = x_format == MXQ_FMT_E4M3;
+    return hip_status(mxq::launch_mxfp4_mm(xq, xs_e8m0, x8, x8 ? K : K / 2, K / 32, wq_e2m1, ws_e8m0, group_end_offs,
+                                           (int)M, (int)N, (int)K, (int)G, y, out_dtype == MXQ_OUT_F32, workspace,
+                                           (hipStream_t)stream));
+}
+
+mxq_status mxq_mxfp4_grouped_mm_packed(const void* packed, const void* wq_e2m1, const void* ws_e8m0,
+                                       const int32_t* group_end_offs, int64_t M, int64_t N, int64_t K, int32_t G,
+                                       int out_dtype, void* y, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const mxq_status st = check_mxfp4_mm_sizes(M, N, K, G);
+    if (st != MXQ_OK) return st;
+    if (K % 512 != 0) return MXQ_ERR_SHAPE;        // 16-byte aligned packed rows
+    if (out_dtype != MXQ_OUT_BF16 && out_dtype != MXQ_OUT_F32) return MXQ_ERR_DTYPE;
+    if (M == 0 || N == 0) return MXQ_OK;
+    if (!packed || !wq_e2m1 || !ws_e8m0 || !group_end_offs || !y) return MXQ_ERR_NULL;
+    if (!aligned16(packed) || !aligned16(wq_e2m1) || !aligned16(ws_e8m0) || !aligned16(y)) return MXQ_ERR_ALIGN;
+    if (((uintptr_t)group_end_offs & 3u) != 0) return MXQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes < mxq::mxfp4_mm_workspace_bytes(M, N, G)) return MXQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
+    const int64_t ldp = K + K / 32;
+    const uint8_t* base = static_cast<const uint8_t*>(packed);
+    return hip_status(mxq::launch_mxfp4_mm(base, base + K, true, ldp, ldp, wq_e2m1, ws_e8m0, group_end_offs, (int)M,
+                                           (int)N, (int)K, (int)G, y, out_dtype == MXQ_OUT_F32, workspace,
+                                           (hipStream_t)stream));
+}
+
+// ------------------------------------------------------------------- norm ---
+static mxq_status check_norm(int64_t M, int64_t K, int dtype, bool mx)
+{
+    const mxq_status st = check_2d(M, K);
+    if (st != MXQ_OK) return st;
+    if (K % (mx ? 32 : 8) != 0 || K > mxq::norm_max_k()) return MXQ_ERR_SHAPE;
+    if (dtype != MXQ_OUT_BF16 && dtype != MXQ_OUT_F32) return MXQ_ERR_DTYPE;
+    return MXQ_OK;
+}
+
+mxq_status mxq_add_rmsnorm(const void* x, const void* residual, const void* weight, int dtype, int64_t M, int64_t K,
+                           float eps, void* h, void* y, void* q_e4m3, void* s_e8m0, float* rstd, void* stream)
+{
+    const mxq_status st = check_norm(M, K, dtype, q_e4m3 != nullptr || s_e8m0 != nullptr);
+    if (st != MXQ_OK) return st;
+    if (!(eps >= 0.0f)) return MXQ_ERR_RULE;
+    if (M == 0 || K == 0) return MXQ_OK;
+    if (!x || !weight || (!y && !q_e4m3) || (q_e4m3 == nullptr) != (s_e8m0 == nullptr)) return MXQ_ERR_NULL;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(h) || !aligned16(y) ||
+        !aligned16(q_e4m3) || !aligned16(s_e8m0) || ((uintptr_t)rstd & 3u) != 0)
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_add_rmsnorm(x, residual, weight, dtype == MXQ_OUT_F32, M, K, eps, h, y, q_e4m3,
+                                              s_e8m0, rstd, (hipStream_t)stream));
+}
+
+size_t mxq_add_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K)
+{
+    if (check_norm(M, K, MXQ_OUT_BF16, false) != MXQ_OK) return 0;
+    return mxq::add_rmsnorm_bwd_workspace_bytes(M, K);
+}
+
+mxq_status mxq_add_rmsnorm_bwd(const void* h, const void* weight, const float* rstd, const void* dy, const void* dh,
+                               int dtype, int64_t M, int64_t K, void* dx, float* dweight, void* workspace,
+                               size_t workspace_bytes, void* stream)
+{
+    const mxq_status st = check_norm(M, K, dtype, false);
+    if (st != MXQ_OK) return st;
+    if (K == 0) return MXQ_OK;
+    if (!dweight || (M > 0 && (!h || !weight || !rstd || !dy || !dx))) return MXQ_ERR_NULL;
+    if (!aligned16(dweight) || (M > 0 && (!aligned16(h) || !aligned16(weight) || !aligned16(dy) || !aligned16(dh) ||
+                                          !aligned16(dx) || ((uintptr_t)rstd & 3u) != 0)))
+        return MXQ_ERR_ALIGN;
+    if (M > 0 && (!workspace || workspace_bytes < mxq::add_rmsnorm_bwd_workspace_bytes(M, K)))
+        return MXQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_add_rmsnorm_bwd(h, weight, rstd, dy, dh, dtype == MXQ_OUT_F32, M, K, dx, dweight,
+                                                  workspace, (hipStream_t)stream));
+}
+
+// ---------------------------------------------------------------- routing ---
+static mxq_status check_route(int dtype, int64_t M, int64_t E, int64_t topk, int score, int flags, int allowed)
+{
+    const mxq_status st = check_2d(M, E);
+    if (st != MXQ_OK) return st;
+    if (E < 1 || E > mxq::route_max_experts() || topk < 1 || topk > mxq::route_max_topk() || topk > E)
+        return MXQ_ERR_SHAPE;
+    if (dtype != MXQ_OUT_BF16 && dtype != MXQ_OUT_F32) return MXQ_ERR_DTYPE;
+    if (score != MXQ_SCORE_SOFTMAX && score != MXQ_SCORE_SIGMOID) return MXQ_ERR_RULE;
+    if ((flags & ~allowed) != 0) return MXQ_ERR_RULE;
+    return MXQ_OK;
+}
+
+mxq_status mxq_route_topk(const void* logits, int dtype, int64_t M, int32_t E, const float* bias, int score,
+                          int32_t n_groups, int32_t topk_groups, int32_t topk, int flags, float scale,
+                          int32_t* expert_ids, float* weights, void* stream)
+{
+    const mxq_status st = check_route(dtype, M, E, topk, score, flags, MXQ_ROUTE_RENORM | MXQ_ROUTE_GROUP_TOP2);
+    if (st != MXQ_OK) return st;
+    if (n_groups < 1 || E % n_groups != 0 || topk_groups < 1 || topk_groups > n_groups ||
+        (int64_t)topk_groups * (E / n_groups) < topk)
+        return MXQ_ERR_SHAPE;
+    if (M == 0) return MXQ_OK;
+    if (!logits || !expert_ids || !weights) return MXQ_ERR_NULL;
+    if (!aligned16(logits) || ((uintptr_t)bias & 3u) != 0 || ((uintptr_t)expert_ids & 3u) != 0 ||
+        ((uintptr_t)weights & 3u) != 0)
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_route_topk(logits, dtype == MXQ_OUT_F32, M, E, bias, score == MXQ_SCORE_SIGMOID,
+                                             n_groups, topk_groups, topk, (flags & MXQ_ROUTE_RENORM) != 0,
+                                             (flags & MXQ_ROUTE_GROUP_TOP2) != 0, scale, expert_ids, weights,
+                                             (hipStream_t)stream));
+}
+
+mxq_status mxq_route_topk_bwd(const void* logits, int dtype, int64_t M, int32_t E, int score,
+                              const int32_t* expert_ids, int32_t topk, int flags, float scale, const float* dweights,
+                              void* dlogits, void* stream)
+{
+    const mxq_status st = check_route(dtype, M, E, topk, score, flags, MXQ_ROUTE_RENORM);
+    if (st != MXQ_OK) return st;
+    if (M == 0) return MXQ_OK;
+    if (!logits || !expert_ids || !dweights || !dlogits) return MXQ_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(dlogits) || ((uintptr_t)expert_ids & 3u) != 0 ||
+        ((uintptr_t)dweights & 3u) != 0)
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_route_topk_bwd(logits, dtype == MXQ_OUT_F32, M, E, score == MXQ_SCORE_SIGMOID,
+                                                 expert_ids, topk, (flags & MXQ_ROUTE_RENORM) != 0, scale, dweights,
+                                                 dlogits, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -90,6 +90,118 @@ __device__ __forceinline__ uint32_t quad_max_u32(uint32_t v)
     return v > t ? v : t;
 }
 
+// ------------------------------------------------- reductions across lanes --
+// One DPP move of all 64 lanes (every lane must be active).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;               // quad permutations
+constexpr int kDppHalfMirror = 0x141, kDppMirror = 0x140;     // reversed within 8 and within 16 lanes
+
+// Reduction over each aligned run of L lanes (L = 16 or 64), the result in all
+// of them.  A fixed order, so floating sums are reproducible; no LDS.
+template <int L, class F>
+__device__ __forceinline__ uint32_t lanes_reduce(uint32_t v, F op)
+{
+    static_assert(L == 16 || L == 64, "");
+    v = op(v, dpp_move<kDppXor1>(v));
+    v = op(v, dpp_move<kDppXor2>(v));
+    v = op(v, dpp_move<kDppHalfMirror>(v));
+    v = op(v, dpp_move<kDppMirror>(v));
+    if constexpr (L == 64) {
+        const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
+        const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
+        const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32);
+        const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+        v = op(op(a, b), op(c, d));
+    }
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    return __uint_as_float(lanes_reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
+{
+    return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v)
+{
+    return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+
+// --------------------------------------------- 8 values of bf16 or fp32 --
+// kBytes of one value; load8 / store8 move values 8i .. 8i+7 of a row.
+__device__ __forceinline__ uint32_t f32_pair_to_bf16(float lo, float hi)
+{
+    const v2bf16 t = {(__bf16)lo, (__bf16)hi};        // nearest even
+    return __builtin_bit_cast(uint32_t, t);
+}
+struct Bf16 {
+    static constexpr int kBytes = 2;
+    struct Raw { uint4 a; };
+    static __device__ __forceinline__ Raw load8(const void* row, int64_t i) { return {((const uint4*)row)[i]}; }
+    static __device__ __forceinline__ Raw load8_nt(const void* row, int64_t i) { return {load_nt((const uint4*)row + i)}; }
+    static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[8])
+    {
+        const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_lo_to_f32(w[i]);
+            v[2 * i + 1] = bf16_hi_to_f32(w[i]);
+        }
+    }
+    static __device__ __forceinline__ Raw pack(const float (&v)[8])
+    {
+        return {make_uint4(f32_pair_to_bf16(v[0], v[1]), f32_pair_to_bf16(v[2], v[3]), f32_pair_to_bf16(v[4], v[5]),
+                           f32_pair_to_bf16(v[6], v[7]))};
+    }
+    static __device__ __forceinline__ void store8(void* row, int64_t i, const Raw& r) { store_nt(r.a, (uint4*)row + i); }
+    // the bf16 values of a packed chunk
+    static __device__ __forceinline__ uint4 bf16_bits(const Raw& r) { return r.a; }
+};
+struct F32 {
+    static constexpr int kBytes = 4;
+    struct Raw { uint4 a, b; };
+    static __device__ __forceinline__ Raw load8(const void* row, int64_t i)
+    {
+        return {((const uint4*)row)[2 * i], ((const uint4*)row)[2 * i + 1]};
+    }
+    static __device__ __forceinline__ Raw load8_nt(const void* row, int64_t i)
+    {
+        return {load_nt((const uint4*)row + 2 * i), load_nt((const uint4*)row + 2 * i + 1)};
+    }
+    static __device__ __forceinline__ void unpack(const Raw& r, float (&v)[8])
+    {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    }
+    static __device__ __forceinline__ Raw pack(const float (&v)[8])
+    {
+        return {make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])),
+                make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]))};
+    }
+    static __device__ __forceinline__ void store8(void* row, int64_t i, const Raw& r)
+    {
+        store_nt(r.a, (uint4*)row + 2 * i);
+        store_nt(r.b, (uint4*)row + 2 * i + 1);
+    }
+    static __device__ __forceinline__ uint4 bf16_bits(const Raw& r)
+    {
+        float v[8];
+        unpack(r, v);
+        return Bf16::pack(v).a;
+    }
+};
+
 // Non-zero in each byte lane of the result whose input byte is 0x7F or 0xFF.
 __device__ __forceinline__ uint32_t nan_code_bytes(uint32_t q)
 {

@@ -52,6 +52,36 @@ hipError_t launch_grouped_mm_strided(const void* xq, const void* xs, uint32_t ld
                                      const void* ws, const int32_t* offs, int M, int N, int K, int G, void* y,
                                      bool f32_out, void* workspace, hipStream_t stream);
 
+// MXFP4: codec and grouped product.
+hipError_t launch_mxfp4_quantize(const void* x, int64_t M, int64_t K, void* q, void* s, bool rceil,
+                                 hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(const void* q, const void* s, int64_t M, int64_t K, void* y, hipStream_t stream);
+bool mxfp4_mm_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t G);
+size_t mxfp4_mm_workspace_bytes(int64_t M, int64_t N, int32_t G);
+// ldx, ldxs: row strides in bytes of the token codes (a multiple of 16) and scales (of 4).
+hipError_t launch_mxfp4_mm(const void* xq, const void* xs, bool x8, int64_t ldx, int64_t ldxs, const void* wq,
+                           const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
+                           void* workspace, hipStream_t stream);
+
+// Norm: K at most norm_max_k(), a multiple of 8 (of 32 with q).
+int norm_max_k();
+hipError_t launch_add_rmsnorm(const void* x, const void* r, const void* w, bool f32, int64_t M, int64_t K, float eps,
+                              void* h, void* y, void* q, void* s, float* rstd, hipStream_t stream);
+size_t add_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
+hipError_t launch_add_rmsnorm_bwd(const void* h, const void* w, const float* rstd, const void* dy, const void* dh,
+                                  bool f32, int64_t M, int64_t K, void* dx, float* dw, void* workspace,
+                                  hipStream_t stream);
+
+// Routing.
+int route_max_experts();
+int route_max_topk();
+hipError_t launch_route_topk(const void* logits, bool f32, int64_t M, int E, const float* bias, bool sigmoid,
+                             int n_groups, int topk_groups, int topk, bool renorm, bool top2, float scale,
+                             int32_t* ids, float* weights, hipStream_t stream);
+hipError_t launch_route_topk_bwd(const void* logits, bool f32, int64_t M, int E, bool sigmoid, const int32_t* ids,
+                                 int topk, bool renorm, float scale, const float* dweights, void* dlogits,
+                                 hipStream_t stream);
+
 hipError_t launch_transpose_u8(const void* in, int64_t R, int64_t C, void* out, hipStream_t stream);
 
 }  // namespace mxq

@@ -35,13 +35,22 @@ MXQ_SCALE_FLOOR = 0
 MXQ_SCALE_RCEIL = 1
 MXQ_GROUP_POW2_SCALE = 1
 MXQ_GROUP_INVERSE_SCALE = 2
+MXQ_FMT_E4M3 = 0
+MXQ_FMT_E2M1 = 1
+MXQ_SCORE_SOFTMAX = 0
+MXQ_SCORE_SIGMOID = 1
+MXQ_ROUTE_RENORM = 1
+MXQ_ROUTE_GROUP_TOP2 = 2
 
 EXPORTED = ("mxq_abi_version", "mxq_status_string", "mxq_last_hip_error", "mxq_quantize_mx",
             "mxq_dequantize_mx", "mxq_group_scale_workspace_bytes", "mxq_group_scale_fp8",
             "mxq_transpose_u8", "mxq_grouped_mm_workspace_bytes", "mxq_scaled_grouped_mm",
             "mxq_quantize_mx_ex", "mxq_dequantize_mx_ex", "mxq_group_scale_fp8_ex",
             "mxq_dispatch_pack_workspace_bytes", "mxq_dispatch_pack_mx", "mxq_scaled_grouped_mm_packed",
-            "mxq_set_group_scale_knobs", "mxq_group_scale_fp8_noalloc", "mxq_group_scale_route_counters")
+            "mxq_set_group_scale_knobs", "mxq_group_scale_fp8_noalloc", "mxq_group_scale_route_counters",
+            "mxq_add_rmsnorm", "mxq_add_rmsnorm_bwd_workspace_bytes", "mxq_add_rmsnorm_bwd", "mxq_route_topk",
+            "mxq_route_topk_bwd", "mxq_quantize_mxfp4", "mxq_dequantize_mxfp4",
+            "mxq_mxfp4_grouped_mm_workspace_bytes", "mxq_mxfp4_grouped_mm", "mxq_mxfp4_grouped_mm_packed")
 
 GROUP_METHODS = {"auto": 0, "hold": 1, "twopass": 2, "split": 3}
 
@@ -105,6 +114,27 @@ def lib() -> ctypes.CDLL:
         L.mxq_group_scale_route_counters.argtypes = [P, sz, i64, i64, i32, ctypes.c_int, P, P]
         L.mxq_scaled_grouped_mm.restype = ctypes.c_int
         L.mxq_scaled_grouped_mm.argtypes = [P, P, P, P, P, i64, i64, i64, i32, ctypes.c_int, P, P, sz, P]
+        f32, ci = ctypes.c_float, ctypes.c_int
+        L.mxq_add_rmsnorm.restype = ci
+        L.mxq_add_rmsnorm.argtypes = [P, P, P, ci, i64, i64, f32, P, P, P, P, P, P]
+        L.mxq_add_rmsnorm_bwd_workspace_bytes.restype = sz
+        L.mxq_add_rmsnorm_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.mxq_add_rmsnorm_bwd.restype = ci
+        L.mxq_add_rmsnorm_bwd.argtypes = [P, P, P, P, P, ci, i64, i64, P, P, P, sz, P]
+        L.mxq_route_topk.restype = ci
+        L.mxq_route_topk.argtypes = [P, ci, i64, i32, P, ci, i32, i32, i32, ci, f32, P, P, P]
+        L.mxq_route_topk_bwd.restype = ci
+        L.mxq_route_topk_bwd.argtypes = [P, ci, i64, i32, ci, P, i32, ci, f32, P, P, P]
+        L.mxq_quantize_mxfp4.restype = ci
+        L.mxq_quantize_mxfp4.argtypes = [P, i64, i64, ci, P, P, P]
+        L.mxq_dequantize_mxfp4.restype = ci
+        L.mxq_dequantize_mxfp4.argtypes = [P, P, i64, i64, P, P]
+        L.mxq_mxfp4_grouped_mm_workspace_bytes.restype = sz
+        L.mxq_mxfp4_grouped_mm_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.mxq_mxfp4_grouped_mm.restype = ci
+        L.mxq_mxfp4_grouped_mm.argtypes = [P, P, ci, P, P, P, i64, i64, i64, i32, ci, P, P, sz, P]
+        L.mxq_mxfp4_grouped_mm_packed.restype = ci
+        L.mxq_mxfp4_grouped_mm_packed.argtypes = [P, P, P, P, i64, i64, i64, i32, ci, P, P, sz, P]
         _lib = L
     return _lib
 
@@ -418,3 +448,241 @@ def mxq_scaled_grouped_mm_packed(packed: torch.Tensor, wq: torch.Tensor, ws: tor
     wbytes = workspace.numel() * workspace.element_size()
     _check(lib().mxq_scaled_grouped_mm_packed(pp, pwq, pws, po, M, N, K, G, dt, py, pw, wbytes, _stream(stream)),
            "mxq_scaled_grouped_mm_packed")
+
+
+# ------------------------------------------------------------------- norm ---
+def _float_code(t: torch.Tensor, name: str) -> int:
+    """mxq_out_dtype of a bf16 or float32 tensor."""
+    if t.dtype == torch.bfloat16:
+        return MXQ_OUT_BF16
+    if t.dtype == torch.float32:
+        return MXQ_OUT_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _opt(t, name: str, dtype=None, numel=None) -> int:
+    """_dev of a tensor that may be None (a NULL pointer)."""
+    return 0 if t is None else _dev(t, name, dtype, numel)
+
+
+def mxq_add_rmsnorm(x: torch.Tensor, residual, weight: torch.Tensor, eps: float, h=None, y=None, q=None, s=None,
+                    rstd=None, stream=None) -> None:
+    """x (+ residual) (M, K) and weight (K), bf16 or float32 -> h = x + residual, y = rmsnorm(h) * weight
+    (their type), q (M, K) / s (M, K/32) uint8 = MXFP8 of y, rstd (M) float32; outputs may be None."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D (M, K)")
+    M, K = x.shape
+    code, dt, n = _float_code(x, "x"), x.dtype, M * K
+    px = _dev(x, "x")
+    pr = _opt(residual, "residual", dt, n)
+    pw = _dev(weight, "weight", dt, K)
+    ph = _opt(h, "h", dt, n)
+    py = _opt(y, "y", dt, n)
+    pq = _opt(q, "q", torch.uint8, n)
+    ps = _opt(s, "s", torch.uint8, M * (K // 32) if K % 32 == 0 else None)
+    pd = _opt(rstd, "rstd", torch.float32, M)
+    _check(lib().mxq_add_rmsnorm(px, pr, pw, code, M, K, float(eps), ph, py, pq, ps, pd, _stream(stream)),
+           "mxq_add_rmsnorm")
+
+
+def mxq_add_rmsnorm_bwd_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().mxq_add_rmsnorm_bwd_workspace_bytes(int(M), int(K)))
+
+
+def mxq_add_rmsnorm_bwd(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dh,
+                        dx: torch.Tensor, dweight: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """h, rstd of mxq_add_rmsnorm and the gradients dy, dh (or None) -> dx (M, K) and dweight (K) float32."""
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D (M, K)")
+    M, K = h.shape
+    code, dt, n = _float_code(h, "h"), h.dtype, M * K
+    ph = _dev(h, "h")
+    pw = _dev(weight, "weight", dt, K)
+    pr = _dev(rstd, "rstd", torch.float32, M)
+    pg = _dev(dy, "dy", dt, n)
+    pd = _opt(dh, "dh", dt, n)
+    px = _dev(dx, "dx", dt, n)
+    pk = _dev(dweight, "dweight", torch.float32, K)
+    pws = _dev(workspace, "workspace")
+    wbytes = workspace.numel() * workspace.element_size()
+    _check(lib().mxq_add_rmsnorm_bwd(ph, pw, pr, pg, pd, code, M, K, px, pk, pws, wbytes, _stream(stream)),
+           "mxq_add_rmsnorm_bwd")
+
+
+def add_rmsnorm(x: torch.Tensor, residual, weight: torch.Tensor, eps: float, stream=None):
+    """(h, y, q, s, rstd) of mxq_add_rmsnorm; h is x itself when there is no residual."""
+    M, K = x.shape
+    h = x if residual is None else torch.empty_like(x)
+    y = torch.empty_like(x)
+    q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    s = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    mxq_add_rmsnorm(x, residual, weight, eps, None if residual is None else h, y, q, s, rstd, stream)
+    return h, y, q, s, rstd
+
+
+def add_rmsnorm_bwd(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dh=None, stream=None):
+    """(dx, dweight) of mxq_add_rmsnorm_bwd."""
+    M, K = h.shape
+    dx = torch.empty_like(h)
+    dweight = torch.empty(K, dtype=torch.float32, device=h.device)
+    ws = torch.empty(max(mxq_add_rmsnorm_bwd_workspace_bytes(M, K), 16), dtype=torch.uint8, device=h.device)
+    mxq_add_rmsnorm_bwd(h, weight, rstd, dy, dh, dx, dweight, ws, stream)
+    return dx, dweight
+
+
+# ---------------------------------------------------------------- routing ---
+SCORES = {"softmax": MXQ_SCORE_SOFTMAX, "sigmoid": MXQ_SCORE_SIGMOID}
+
+
+def mxq_route_topk(logits: torch.Tensor, bias, score: int, n_groups: int, topk_groups: int, flags: int, scale: float,
+                   expert_ids: torch.Tensor, weights: torch.Tensor, stream=None) -> None:
+    """logits (M, E) bf16 or float32, bias float32 (E) or None -> expert_ids int32 and weights float32, (M, topk)."""
+    if logits.dim() != 2 or expert_ids.dim() != 2 or expert_ids.shape[0] != logits.shape[0]:
+        raise ValueError("logits must be (M, E) and expert_ids (M, topk)")
+    M, E = logits.shape
+    topk = expert_ids.shape[1]
+    code = _float_code(logits, "logits")
+    pl = _dev(logits, "logits")
+    pb = _opt(bias, "bias", torch.float32, E)
+    pi = _dev(expert_ids, "expert_ids", torch.int32)
+    pw = _dev(weights, "weights", torch.float32, M * topk)
+    _check(lib().mxq_route_topk(pl, code, M, E, pb, int(score), int(n_groups), int(topk_groups), topk, int(flags),
+                                float(scale), pi, pw, _stream(stream)), "mxq_route_topk")
+
+
+def mxq_route_topk_bwd(logits: torch.Tensor, score: int, expert_ids: torch.Tensor, flags: int, scale: float,
+                       dweights: torch.Tensor, dlogits: torch.Tensor, stream=None) -> None:
+    """logits (M, E), expert_ids and dweights (M, topk) -> dlogits (M, E), the type of logits."""
+    if logits.dim() != 2 or expert_ids.dim() != 2 or expert_ids.shape[0] != logits.shape[0]:
+        raise ValueError("logits must be (M, E) and expert_ids (M, topk)")
+    M, E = logits.shape
+    topk = expert_ids.shape[1]
+    code = _float_code(logits, "logits")
+    pl = _dev(logits, "logits")
+    pi = _dev(expert_ids, "expert_ids", torch.int32)
+    pw = _dev(dweights, "dweights", torch.float32, M * topk)
+    pd = _dev(dlogits, "dlogits", logits.dtype, M * E)
+    _check(lib().mxq_route_topk_bwd(pl, code, M, E, int(score), pi, topk, int(flags), float(scale), pw, pd,
+                                    _stream(stream)), "mxq_route_topk_bwd")
+
+
+def route_topk(logits: torch.Tensor, topk: int, bias=None, score: str = "softmax", n_groups: int = 1,
+               topk_groups: int = 1, renormalize: bool = False, group_top2: bool = False, scale: float = 1.0,
+               stream=None):
+    """(expert_ids, weights), each (M, topk), of mxq_route_topk."""
+    M = logits.shape[0]
+    ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
+    flags = (MXQ_ROUTE_RENORM if renormalize else 0) | (MXQ_ROUTE_GROUP_TOP2 if group_top2 else 0)
+    mxq_route_topk(logits, bias, SCORES[score], n_groups, topk_groups, flags, scale, ids, weights, stream)
+    return ids, weights
+
+
+def route_topk_bwd(logits: torch.Tensor, expert_ids: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
+                   renormalize: bool = False, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """dlogits of mxq_route_topk_bwd."""
+    dlogits = torch.empty_like(logits)
+    mxq_route_topk_bwd(logits, SCORES[score], expert_ids, MXQ_ROUTE_RENORM if renormalize else 0, scale, dweights,
+                       dlogits, stream)
+    return dlogits
+
+
+# ------------------------------------------------------------------ MXFP4 ---
+def mxq_quantize_mxfp4(x: torch.Tensor, rule: int, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
+    """x (M, K) bf16 -> q (M, K/2) uint8 pairs of E2M1 codes, s (M, K/32) uint8 E8M0 codes."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D (M, K)")
+    M, K = x.shape
+    px = _dev(x, "x", torch.bfloat16)
+    pq = _dev(q, "q", torch.uint8, M * (K // 2) if K % 32 == 0 else None)
+    ps = _dev(s, "s", torch.uint8, M * (K // 32) if K % 32 == 0 else None)
+    _check(lib().mxq_quantize_mxfp4(px, M, K, int(rule), pq, ps, _stream(stream)), "mxq_quantize_mxfp4")
+
+
+def mxq_dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, y: torch.Tensor, stream=None) -> None:
+    """q (M, K/2) uint8 + s (M, K/32) uint8 -> y (M, K) bf16."""
+    if y.dim() != 2:
+        raise ValueError("y must be 2-D (M, K)")
+    M, K = y.shape
+    pq = _dev(q, "q", torch.uint8, M * (K // 2) if K % 32 == 0 else None)
+    ps = _dev(s, "s", torch.uint8, M * (K // 32) if K % 32 == 0 else None)
+    py = _dev(y, "y", torch.bfloat16)
+    _check(lib().mxq_dequantize_mxfp4(pq, ps, M, K, py, _stream(stream)), "mxq_dequantize_mxfp4")
+
+
+def quantize_mxfp4(x: torch.Tensor, rule: int = MXQ_SCALE_FLOOR, stream=None):
+    M, K = x.shape
+    q = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+    s = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    mxq_quantize_mxfp4(x, rule, q, s, stream)
+    return q, s
+
+
+def dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, stream=None) -> torch.Tensor:
+    y = torch.empty((q.shape[0], 2 * q.shape[1]), dtype=torch.bfloat16, device=q.device)
+    mxq_dequantize_mxfp4(q, s, y, stream)
+    return y
+
+
+def mxq_mxfp4_grouped_mm_workspace_bytes(M: int, N: int, K: int, G: int) -> int:
+    return int(lib().mxq_mxfp4_grouped_mm_workspace_bytes(int(M), int(N), int(K), int(G)))
+
+
+def mxq_mxfp4_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, x_format: int, wq: torch.Tensor, ws: torch.Tensor,
+                         group_end_offs: torch.Tensor, y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """xq (M, K) E4M3 or (M, K/2) E2M1 by x_format, xs (M, K/32), wq (G, N, K/2) E2M1, ws (G, N, K/32),
+    group_end_offs int32[G] (device) -> y (M, N) bf16 or float32."""
+    if xq.dim() != 2 or wq.dim() != 3 or y.dim() != 2:
+        raise ValueError("xq must be 2-D, wq (G, N, K/2) and y (M, N)")
+    M = xq.shape[0]
+    G, N, half = wq.shape
+    K = 2 * half
+    if xq.shape[1] != (half if x_format == MXQ_FMT_E2M1 else K) or tuple(y.shape) != (M, N):
+        raise ValueError("operand shapes do not match")
+    kb = K // 32 if K % 32 == 0 else None
+    pxq = _dev(xq, "xq", torch.uint8)
+    pxs = _dev(xs, "xs", torch.uint8, M * kb if kb is not None else None)
+    pwq = _dev(wq, "wq", torch.uint8)
+    pws = _dev(ws, "ws", torch.uint8, G * N * kb if kb is not None else None)
+    po = _dev(group_end_offs, "group_end_offs", torch.int32, G)
+    code = _float_code(y, "y")
+    py = _dev(y, "y")
+    pw = _dev(workspace, "workspace")
+    wbytes = workspace.numel() * workspace.element_size()
+    _check(lib().mxq_mxfp4_grouped_mm(pxq, pxs, int(x_format), pwq, pws, po, M, N, K, G, code, py, pw, wbytes,
+                                      _stream(stream)), "mxq_mxfp4_grouped_mm")
+
+
+def mxq_mxfp4_grouped_mm_packed(packed: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                                group_end_offs: torch.Tensor, y: torch.Tensor, workspace: torch.Tensor,
+                                stream=None) -> None:
+    """packed (M, K + K/32) uint8 MXFP8 token rows, wq (G, N, K/2) / ws (G, N, K/32) -> y (M, N) bf16 or float32."""
+    if packed.dim() != 2 or wq.dim() != 3 or y.dim() != 2:
+        raise ValueError("packed must be 2-D, wq 3-D (G, N, K/2), y 2-D (M, N)")
+    G, N, half = wq.shape
+    K, M = 2 * half, packed.shape[0]
+    if packed.shape[1] != K + K // 32 or tuple(y.shape) != (M, N):
+        raise ValueError("shapes do not match")
+    pp = _dev(packed, "packed", torch.uint8)
+    pwq = _dev(wq, "wq", torch.uint8)
+    pws = _dev(ws, "ws", torch.uint8, G * N * (K // 32))
+    po = _dev(group_end_offs, "group_end_offs", torch.int32, G)
+    code = _float_code(y, "y")
+    py = _dev(y, "y")
+    pw = _dev(workspace, "workspace")
+    wbytes = workspace.numel() * workspace.element_size()
+    _check(lib().mxq_mxfp4_grouped_mm_packed(pp, pwq, pws, po, M, N, K, G, code, py, pw, wbytes, _stream(stream)),
+           "mxq_mxfp4_grouped_mm_packed")
+
+
+def mxfp4_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                     group_end_offs: torch.Tensor, x_format: int = MXQ_FMT_E4M3, out_dtype=torch.bfloat16,
+                     stream=None) -> torch.Tensor:
+    M = xq.shape[0]
+    G, N, half = wq.shape
+    y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
+    wsp = torch.empty(max(mxq_mxfp4_grouped_mm_workspace_bytes(M, N, 2 * half, G), 16), dtype=torch.uint8,
+                      device=xq.device)
+    mxq_mxfp4_grouped_mm(xq, xs, x_format, wq, ws, group_end_offs, y, wsp, stream)
+    return y

@@ -36,7 +36,8 @@
  *     and returned as an mxq_status; the output buffers are then untouched.
  *     A failed launch returns MXQ_ERR_HIP (see mxq_last_hip_error).  Faults
  *     inside kernels surface, HIP-style, at the caller's next synchronisation.
- *   - Results are bitwise deterministic: every reduction is a max.
+ *   - Results are bitwise deterministic: every reduction is a max, or a sum of
+ *     fp32 values in a fixed order.
  */
 #ifndef MXQ_H
 #define MXQ_H
@@ -59,8 +60,9 @@ typedef enum mxq_status {
     MXQ_ERR_WORKSPACE = 5,   /* workspace missing or smaller than required          */
     MXQ_ERR_HIP = 6,         /* a HIP runtime call failed (launch, device query)    */
     MXQ_ERR_NOT_IMPLEMENTED = 7,
-    MXQ_ERR_DTYPE = 8,       /* unknown mxq_out_dtype value                         */
-    MXQ_ERR_RULE = 9         /* unknown mxq_scale_rule value or group flag          */
+    MXQ_ERR_DTYPE = 8,       /* unknown mxq_out_dtype or mxq_format value           */
+    MXQ_ERR_RULE = 9         /* unknown mxq_scale_rule or mxq_score value, unknown
+                                flag, or an eps that is negative or NaN             */
 } mxq_status;
 
 typedef enum mxq_layout {
@@ -86,6 +88,21 @@ typedef enum mxq_out_dtype {
     MXQ_OUT_BF16 = 0,        /* bfloat16, rounded to nearest even from the fp32 sum  */
     MXQ_OUT_F32 = 1          /* the fp32 sum itself                                  */
 } mxq_out_dtype;
+
+typedef enum mxq_format {
+    MXQ_FMT_E4M3 = 0,        /* MXFP8: one E4M3 code a byte, rows of K bytes         */
+    MXQ_FMT_E2M1 = 1         /* MXFP4: two E2M1 codes a byte, rows of K/2 bytes      */
+} mxq_format;
+
+typedef enum mxq_score {
+    MXQ_SCORE_SOFTMAX = 0,   /* softmax over a row's logits                          */
+    MXQ_SCORE_SIGMOID = 1    /* 1 / (1 + exp(-l)) of each logit                      */
+} mxq_score;
+
+typedef enum mxq_route_flags {
+    MXQ_ROUTE_RENORM = 1,    /* divide the selected scores by their sum              */
+    MXQ_ROUTE_GROUP_TOP2 = 2 /* a group's value is the sum of its two largest        */
+} mxq_route_flags;
 
 /* MXQ_ABI_VERSION of the built library. */
 int mxq_abi_version(void);
@@ -422,6 +439,155 @@ mxq_status mxq_scaled_grouped_mm_packed(const void* packed, const void* wq_e4m3,
                                         const int32_t* group_end_offs, int64_t M, int64_t N, int64_t K,
                                         int32_t G, int out_dtype, void* y, void* workspace,
                                         size_t workspace_bytes, void* stream);
+
+/*
+ * Residual addition and root-mean-square norm of token rows, with the MXFP8
+ * encoding of the normalised rows: what stands before an MXFP8 dispatch or
+ * product, in one pass over the rows.
+ *
+ *   dtype    MXQ_OUT_BF16 or MXQ_OUT_F32: the type of x, residual, weight, h, y.
+ *   x        (M, K) input rows; residual (M, K) or NULL (then h's values are x's).
+ *   weight   (K).
+ *   h        (M, K) output x + residual, added in fp32 and rounded once; or NULL.
+ *   y        (M, K) output h * rstd * weight, rounded once; or NULL (with q).
+ *   q_e4m3, s_e8m0  (M, K) and (M, K/32) uint8 outputs: exactly the bytes that
+ *            mxq_quantize_mx writes for y rounded to bf16; or both NULL (with y).
+ *   rstd     (M) fp32 output 1 / sqrt(mean(h^2) + eps); or NULL.
+ *
+ * The norm is that of the stored (rounded) h, so mxq_add_rmsnorm_bwd needs only h
+ * and rstd.  Squares are summed in fp32: a row whose sum of squares passes the
+ * largest fp32 value comes out as zeros.  A NaN or Inf in a row makes the row NaN
+ * (scales 0xFF).  h and y may each be x or residual themselves (in place), not
+ * one another, and overlap nothing else.
+ *
+ * Requires K % 8 == 0 (K % 32 == 0 with q), K <= 16384, M*K <= 2^40
+ * (MXQ_ERR_SHAPE); eps >= 0 (MXQ_ERR_RULE).  Tensors 16-byte aligned, rstd 4-byte.
+ * MXQ_ERR_NULL when both y and q are missing, or one of q and s.  M == 0 or
+ * K == 0 is a no-op.
+ */
+mxq_status mxq_add_rmsnorm(const void* x, const void* residual, const void* weight, int dtype, int64_t M,
+                           int64_t K, float eps, void* h, void* y, void* q_e4m3, void* s_e8m0, float* rstd,
+                           void* stream);
+
+/*
+ * Gradients of mxq_add_rmsnorm, given h and rstd as it wrote them, dy (the
+ * gradient of y; the rounding to MXFP8 counts as the identity) and dh (the
+ * gradient that reaches h along the residual stream, or NULL):
+ *   g = dy * weight;  dx = rstd * (g - h * mean(g * h) * rstd^2) + dh, the
+ *   gradient of x and of residual alike, rounded once;
+ *   dweight (K) fp32 = sum over the rows of dy * h * rstd.
+ * dx may be dy or dh itself (in place).  Sizes and errors as mxq_add_rmsnorm
+ * without q; M == 0 writes a zero dweight.  The workspace holds the rows' parts
+ * of dweight; it needs no initialisation, and two calls in flight must not share it.
+ */
+size_t mxq_add_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
+mxq_status mxq_add_rmsnorm_bwd(const void* h, const void* weight, const float* rstd, const void* dy,
+                               const void* dh, int dtype, int64_t M, int64_t K, void* dx, float* dweight,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Routing of tokens to experts: the expert ids that mxq_dispatch_pack_mx takes,
+ * and the weights of the selected experts' outputs.
+ *
+ *   logits      (M, E) of dtype (MXQ_OUT_BF16 or MXQ_OUT_F32).
+ *   bias        fp32 (E) or NULL: added to the scores for the selection only.
+ *   score       MXQ_SCORE_SOFTMAX or MXQ_SCORE_SIGMOID (MXQ_ERR_RULE otherwise).
+ *   n_groups    the experts form n_groups runs of E / n_groups; only experts of
+ *               the topk_groups best groups are selected (1, 1: no groups).
+ *   flags       a bitwise OR of mxq_route_flags.
+ *   expert_ids  int32 (M, topk) output, best first; weights fp32 (M, topk) output.
+ *
+ * All in fp32.  s = the scores of a row.  The selection goes by s + bias, or by
+ * the logits themselves without a bias (the same order, free of rounding).  A
+ * group's value is the largest s + bias in it, or with MXQ_ROUTE_GROUP_TOP2 the
+ * sum of its two largest (without a bias: of exp(l - max l), or of the sigmoid).
+ * Ties go to the lowest index.  weights = scale * s of the selected, with
+ * MXQ_ROUTE_RENORM scale * s / (sum of the row's selected s + 1e-20).
+ * An expert whose logit is -inf or NaN, or whose key is -inf or NaN, is masked:
+ * it is never selected.  Slots with no expert left get id -1 (which
+ * mxq_dispatch_pack_mx drops) and weight 0, so a row of -inf routes nowhere.  A
+ * row that holds a NaN (or, with softmax, +inf) has NaN in all its weights; its
+ * ids are still valid or -1.
+ *
+ * Requires 1 <= E <= 1024, 1 <= topk <= 64, E % n_groups == 0,
+ * 1 <= topk_groups <= n_groups, topk <= topk_groups * E / n_groups
+ * (MXQ_ERR_SHAPE).  logits 16-byte aligned, the other arrays 4-byte.  M == 0 is a
+ * no-op.
+ */
+mxq_status mxq_route_topk(const void* logits, int dtype, int64_t M, int32_t E, const float* bias, int score,
+                          int32_t n_groups, int32_t topk_groups, int32_t topk, int flags, float scale,
+                          int32_t* expert_ids, float* weights, void* stream);
+
+/*
+ * Gradient of mxq_route_topk's weights: dlogits (M, E) of dtype from dweights
+ * fp32 (M, topk), for the expert_ids that the forward selected (distinct in a
+ * row; ids outside [0, E) count as empty slots).  flags: MXQ_ROUTE_RENORM or 0, as
+ * in the forward.  The selection itself and the bias have no gradient.  With
+ * sigmoid, or with softmax and MXQ_ROUTE_RENORM (then the weights are a softmax
+ * over the selected logits), only the selected logits get one; every other value
+ * of dlogits is written as zero.  logits and dlogits 16-byte aligned; sizes and
+ * errors as mxq_route_topk.
+ */
+mxq_status mxq_route_topk_bwd(const void* logits, int dtype, int64_t M, int32_t E, int score,
+                              const int32_t* expert_ids, int32_t topk, int flags, float scale,
+                              const float* dweights, void* dlogits, void* stream);
+
+/*
+ * MXFP4 quantization (OCP Microscaling v1.0: blocks of 32 along the rows, one
+ * E8M0 scale a block, E2M1 elements 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives), in the layout of the MXFP8 buffers.
+ *
+ *   x_bf16  (M, K) bf16 input; q_e2m1 (M, K/2) uint8 output, element 2i of a row
+ *           in the low nibble of byte i and 2i + 1 in the high; s_e8m0 (M, K/32).
+ *   rule    MXQ_SCALE_FLOOR: scale code floor(log2 amax) - 2 + 127 (elements above
+ *           6 once scaled saturate); MXQ_SCALE_RCEIL: the smallest scale with
+ *           amax <= 6 * scale.  Both clamped at 0.
+ *
+ * Elements are divided by the scale (exact) and rounded to the nearest E2M1
+ * value, ties to even, saturating at +-6, sign kept.  A block holding Inf or NaN
+ * gets scale 0xFF and every code 0.  Requires K % 32 == 0; sizes, alignment and
+ * errors as mxq_quantize_mx; M == 0 or K == 0 is a no-op.
+ */
+mxq_status mxq_quantize_mxfp4(const void* x_bf16, int64_t M, int64_t K, int rule, void* q_e2m1, void* s_e8m0,
+                              void* stream);
+
+/* The inverse: y = e2m1(q) * 2^(s-127) as bf16 (exact; past the largest bf16
+ * Inf); scale 0xFF gives NaN 0x7FC0. */
+mxq_status mxq_dequantize_mxfp4(const void* q_e2m1, const void* s_e8m0, int64_t M, int64_t K, void* y_bf16,
+                                void* stream);
+
+/*
+ * Grouped product with MXFP4 weights: Y[m, :] = X[m, :] W_g^T for every token
+ * row m of group g, as mxq_scaled_grouped_mm with
+ *   xq       (M, K) E4M3 codes (x_format MXQ_FMT_E4M3, as mxq_quantize_mx writes)
+ *            or (M, K/2) E2M1 codes (MXQ_FMT_E2M1, as mxq_quantize_mxfp4 writes);
+ *            any other x_format: MXQ_ERR_DTYPE;
+ *   wq_e2m1  (G, N, K/2) E2M1 codes and ws_e8m0 (G, N, K/32) scales
+ *            (mxq_quantize_mxfp4 of the (G*N, K) weight).
+ * Offsets, clamping, zero rows past the last end, out_dtype, alignment and
+ * errors as mxq_scaled_grouped_mm.  The matrix cores sum the exact products of a
+ * block; with E4M3 tokens products far below a block's largest (2^-14 and less of
+ * it) are cut off there, with E2M1 tokens a block's sum is exact; blocks are added
+ * in fp32 and the result is rounded once.  NaN codes and scale 0xFF are outside
+ * the contract.  Weights are constants of a serving program: there is no backward.
+ *
+ * Requires K > 0, K % 128 == 0, K <= 2^23, N % 8 == 0, 0 <= M, N <= 2^31 - 1024,
+ * 1 <= G <= 4095 and a tile list of fewer than 2^30 entries (MXQ_ERR_SHAPE);
+ * M == 0 or N == 0 is a no-op.
+ */
+size_t mxq_mxfp4_grouped_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t G);
+mxq_status mxq_mxfp4_grouped_mm(const void* xq, const void* xs_e8m0, int x_format, const void* wq_e2m1,
+                                const void* ws_e8m0, const int32_t* group_end_offs, int64_t M, int64_t N,
+                                int64_t K, int32_t G, int out_dtype, void* y, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* The same on MXFP8 token rows as mxq_dispatch_pack_mx packs them (K e4m3 codes
+ * then K/32 e8m0 scales); K % 512 == 0.  Bit-identical to mxq_mxfp4_grouped_mm on
+ * the unpacked codes and scales. */
+mxq_status mxq_mxfp4_grouped_mm_packed(const void* packed, const void* wq_e2m1, const void* ws_e8m0,
+                                       const int32_t* group_end_offs, int64_t M, int64_t N, int64_t K,
+                                       int32_t G, int out_dtype, void* y, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
