@@ -18,6 +18,7 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kStepK = 128;           // k of one 16x16 MFMA: four scale blocks
+constexpr int64_t kManyRows = 48;      // rows a group, on average, from which the tile kernel takes the call
 constexpr int kFewThreads = 256;
 constexpr int kFewCols = 64;          // output columns of a workgroup (16 a wave)
 
@@ -105,6 +106,8 @@ hipError_t launch_mxfp4_mm(const void* xq, const void* xs, bool x8, int64_t ldx,
                            const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
                            void* workspace, hipStream_t stream)
 {
+    if (K >= mxfp4_mm_tile_min_k() && M >= kManyRows * G)
+        return launch_mxfp4_mm_tile(xq, xs, x8, ldx, ldxs, wq, wsc, offs, M, N, K, G, y, f32_out, stream);
     const dim3 grid((unsigned)((N + kFewCols - 1) / kFewCols), (unsigned)(G + 1));
 #define MXQ_LAUNCH(X8, F)                                                                                            \
     hipLaunchKernelGGL((mxfp4_mm_few_kernel<X8, F>), grid, dim3(kFewThreads), 0, stream, (const uint8_t*)xq,         \
