@@ -62,8 +62,7 @@ size_t mxfp4_mm_workspace_bytes(int64_t M, int64_t N, int32_t G);
 hipError_t launch_mxfp4_mm(const void* xq, const void* xs, bool x8, int64_t ldx, int64_t ldxs, const void* wq,
                            const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
                            void* workspace, hipStream_t stream);
-// Its part for groups of many rows: K at least mxfp4_mm_tile_min_k().
-int mxfp4_mm_tile_min_k();
+// Its part for groups of many rows.
 hipError_t launch_mxfp4_mm_tile(const void* xq, const void* xs, bool x8, int64_t ldx, int64_t ldxs, const void* wq,
                                 const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
                                 hipStream_t stream);

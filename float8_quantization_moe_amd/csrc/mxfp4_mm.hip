@@ -106,7 +106,7 @@ hipError_t launch_mxfp4_mm(const void* xq, const void* xs, bool x8, int64_t ldx,
                            const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
                            void* workspace, hipStream_t stream)
 {
-    if (K >= mxfp4_mm_tile_min_k() && M >= kManyRows * G)
+    if (M >= kManyRows * G)
         return launch_mxfp4_mm_tile(xq, xs, x8, ldx, ldxs, wq, wsc, offs, M, N, K, G, y, f32_out, stream);
     const dim3 grid((unsigned)((N + kFewCols - 1) / kFewCols), (unsigned)(G + 1));
 #define MXQ_LAUNCH(X8, F)                                                                                            \

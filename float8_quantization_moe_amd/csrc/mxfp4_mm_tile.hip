@@ -8,9 +8,10 @@
 // shape for both.  K advances 256 values a slot through a 2-slot LDS ring of 32 KB
 // of W and 32 KB of X codes and 16 bytes of scales a row, filled by
 // buffer-load-to-LDS in whole 128-byte lines.  A slot is four MFMA steps of 64 k; a
-// step's operands are read from LDS during the step before it, and the loads of the
-// slot after next go out between the MFMAs of a slot's last step, right after the
-// one barrier that a slot needs.
+// step's operands are read from LDS during the step before it.  The one barrier that
+// a slot needs comes before its last step, when all its operands are in registers:
+// the loads of the slot after next go into its place from there on, spread between
+// the MFMAs of three steps.
 //
 // The slots of successive tiles form one stream: the loads run ahead of the
 // products across the end of a tile, so the next tile's operands arrive while this
@@ -190,7 +191,7 @@ struct Loader {
     uint32_t off_w[8], off_x[8], off_ws, off_xs;         // lane offsets of the wave's loads
     uint32_t lds_data, lds_ws, lds_xs;                   // LDS addresses of the wave's part of ring slot 0
     uint32_t upper;                                      // bit 31: this lane's chunk of load 0 is in the second half of a row's slot
-    int left;                                            // slots of the tile from the next one on
+    int entry, left;                                     // the tile's place in the list; its slots from the next one on
     static constexpr int kXStep = X8 ? 256 : 128;        // bytes of an X row in a slot
 
     __device__ __forceinline__ void set_lanes(const MmArgs& a, const uint8_t* lds, int wave, int lane)
@@ -219,12 +220,12 @@ struct Loader {
     }
 
     // The first slot of tile `entry` of the list; past its end, loads of nothing.
-    __device__ __forceinline__ void set_tile(const MmArgs& a, const Tile* list, int entry, int count, int nslots)
+    __device__ __forceinline__ void set_tile(const MmArgs& a, const Tile* list, int e, int count, int nslots)
     {
         left = nslots;
         const uint32_t half = (uint32_t)a.K / 2u, kb = (uint32_t)a.K / 32u;
-        const bool some = entry < count;
-        const Tile t = list[some ? entry : 0];
+        const bool some = e < count;
+        const Tile t = list[some ? e : 0];
         const int g = some ? uniform(t.g) : 0, r0 = some ? uniform(t.r0) : 0;
         const uint32_t nx = some ? (uint32_t)(uniform(t.r1) - r0) : 1u;
         const int n0 = some ? uniform(t.c) * kCols : 0;
@@ -236,34 +237,38 @@ struct Loader {
         xs = resource(a.xs + (int64_t)r0 * a.ldxs, some ? (nx - 1u) * a.ldxs + kb : 0u);
     }
 
-    static __device__ __forceinline__ void step(v4i& r, uint32_t bytes, bool nothing)
+    static __device__ __forceinline__ void step(v4i& r, uint32_t bytes)
     {
         const uint64_t base = (((uint64_t)(uint32_t)r.y << 32) | (uint32_t)r.x) + bytes;
         const uint32_t left = (uint32_t)r.z;
         r.x = uniform((int)(uint32_t)base);              // (resources stay in scalar registers)
         r.y = uniform((int)(uint32_t)(base >> 32));
-        r.z = uniform((int)(nothing || left < bytes ? 0u : left - bytes));
+        r.z = uniform((int)(left < bytes ? 0u : left - bytes));
     }
-    // Where K ends half way through a tile's last slot, that slot's X codes past K
-    // are zeros: their lanes' offsets leave the resource (bit 31) for its loads.
+    // On to the next slot of the stream.  Where K ends half way through a tile's last
+    // slot, that slot's X codes past K are to be zeros: for its loads their lanes'
+    // offsets leave the resource (bit 31).
+    __device__ __forceinline__ void advance(const MmArgs& a, const Tile* list, int count, int nslots)
+    {
+        const bool was_last = left == 1;
+        if (was_last) {
+            set_tile(a, list, ++entry, count, nslots);
+        } else {
+            --left;
+            step(w, 128u);
+            step(x, kXStep);
+            step(ws, 8u);
+            step(xs, 8u);
+        }
+        if (a.K % kSlotK != 0 && was_last != (left == 1)) toggle_half();
+    }
     __device__ __forceinline__ void toggle_half()
     {
 #pragma unroll
         for (int i = 0; i < 8; ++i) off_x[i] ^= (i & (X8 ? 2 : 1)) ? upper ^ 0x80000000u : upper;
     }
-    // On to the next slot of the tile (`nothing`: K has no other, its loads are zeros).
-    __device__ __forceinline__ void next_slot(const MmArgs& a, bool nothing)
-    {
-        --left;
-        if (a.K % kSlotK != 0 && left <= 1) toggle_half();
-        step(w, 128u, nothing);
-        step(x, kXStep, nothing);
-        step(ws, 8u, nothing);
-        step(xs, 8u, nothing);
-    }
 
-    static constexpr int kLoads = 18;
-    // Load I of the slot into ring slot b.
+    // Load I (0 .. 17) of the slot into ring slot b.
     template <int I>
     __device__ __forceinline__ void issue(uint32_t b)
     {
@@ -360,40 +365,56 @@ __device__ __forceinline__ void mfma(v16f (&acc)[4][TM], const Operands<X8, TM>&
                                                                 2 * (T & 1), sx);
 }
 
-// Step T's MFMAs; LOADS: with the next slot's loads into ring slot b between them.
-template <bool X8, int TM, int T, bool ZERO, bool LOADS, int I = 0>
+// Step T's MFMAs, with loads A .. B - 1 of the next slot of the stream into ring
+// slot b spread between them.
+template <bool X8, int TM, int T, bool ZERO, int A, int B, int I = 0>
 __device__ __forceinline__ void mfmas(v16f (&acc)[4][TM], const Operands<X8, TM>& f, const Scales<TM>& s, Loader<X8>& ld,
                                       uint32_t b)
 {
     constexpr int n = 4 * TM;
     if constexpr (I < n) {
         mfma<X8, TM, T, ZERO, I>(acc, f, s);
-        if constexpr (LOADS) {
-            ld.template issue_some<I * Loader<X8>::kLoads / n, (I + 1) * Loader<X8>::kLoads / n>(b);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        mfmas<X8, TM, T, ZERO, LOADS, I + 1>(acc, f, s, ld, b);
+        ld.template issue_some<A + I * (B - A) / n, A + (I + 1) * (B - A) / n>(b);
+        if constexpr (A < B) __builtin_amdgcn_sched_barrier(0);
+        mfmas<X8, TM, T, ZERO, A, B, I + 1>(acc, f, s, ld, b);
     }
 }
 
-// One slot.  On entry f[0] and s hold (or are being read from LDS with) its first
-// step and scales; on exit the next slot's, unless it is the tile's LAST.
-template <bool X8, int TM, bool FIRST, bool LAST>
-__device__ __forceinline__ void slot_products(v16f (&acc)[4][TM], Operands<X8, TM> (&f)[2], Scales<TM>& s, Loader<X8>& ld,
-                                              const uint8_t* lds, const Lane& l, uint32_t& b)
+// How a slot's loads are spread: the first kLoadsA in the last step of the slot two
+// before it, up to kLoadsB in the first step of the slot before it, the rest in the
+// second.  All 18 at once fill the memory pipe's queue and hold up the MFMAs behind
+// them: 16640 x 8192 x 5120 over 16 groups 723 / 481 us (E4M3 / E2M1 tokens) against
+// 658 / 451 in thirds (9 + 9: 662 / 450; 12 + 6: 687 / 466).
+constexpr int kLoadsA = 6, kLoadsB = 12, kLoadsC = 18;
+
+// Steps 0 and 1 of the slot in ring slot b, with the second part of the loads of
+// the slot after it.  f[0] and s hold (or are being read with) its first step and
+// scales; f[1] is left with step 1's successor: f[0] holds step 2.
+template <bool X8, int TM, bool FIRST>
+__device__ __forceinline__ void steps01(v16f (&acc)[4][TM], Operands<X8, TM> (&f)[2], Scales<TM>& s, Loader<X8>& ld,
+                                        const uint8_t* lds, const Lane& l, uint32_t b)
 {
     shift_scales<TM>(s, l);
     read_step<X8, TM, 1>(f[1], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
-    mfmas<X8, TM, 0, FIRST, false>(acc, f[0], s, ld, b);
+    mfmas<X8, TM, 0, FIRST, kLoadsA, kLoadsB>(acc, f[0], s, ld, b ^ 1u);
     __builtin_amdgcn_sched_barrier(0);
     read_step<X8, TM, 2>(f[0], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
-    mfmas<X8, TM, 1, false, false>(acc, f[1], s, ld, b);
+    mfmas<X8, TM, 1, false, kLoadsB, kLoadsC>(acc, f[1], s, ld, b ^ 1u);
     __builtin_amdgcn_sched_barrier(0);
+}
+
+// Steps 2 and 3, with the barrier between them and the first part of the loads into
+// this ring slot; on exit f[0] and s hold the next slot's, unless this is the
+// tile's LAST.
+template <bool X8, int TM, bool LAST>
+__device__ __forceinline__ void steps23(v16f (&acc)[4][TM], Operands<X8, TM> (&f)[2], Scales<TM>& s, Loader<X8>& ld,
+                                        const uint8_t* lds, const Lane& l, uint32_t b)
+{
     read_step<X8, TM, 3>(f[1], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
-    mfmas<X8, TM, 2, false, false>(acc, f[0], s, ld, b);
+    mfmas<X8, TM, 2, false, 0, 0>(acc, f[0], s, ld, b);
     slot_barrier();
     const Scales<TM> now = s;
     if constexpr (!LAST) {
@@ -401,14 +422,20 @@ __device__ __forceinline__ void slot_products(v16f (&acc)[4][TM], Operands<X8, T
         read_scales<TM>(s, lds, b ^ 1u, l);
         __builtin_amdgcn_sched_barrier(0);
     }
-    mfmas<X8, TM, 3, false, true>(acc, f[1], now, ld, b);
-    // (the sums are needed here: otherwise the compiler moves a whole slot's MFMAs past its loads into the next block)
+    mfmas<X8, TM, 3, false, 0, kLoadsA>(acc, f[1], now, ld, b);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The sums are needed here: without this the compiler moves MFMAs past the loads
+// that are meant to run under them, into the next basic block.
+template <int TM>
+__device__ __forceinline__ void pin(v16f (&acc)[4][TM])
+{
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) asm volatile("" : "+a"(acc[i][j]));
     __builtin_amdgcn_sched_barrier(0);
-    b ^= 1u;
 }
 
 // Stores: lane (r, h) holds, of row r of each 32 x 32 part, columns 8 q + 4 h .. + 3
@@ -450,34 +477,36 @@ __device__ __forceinline__ void store_tile(const v16f (&acc)[4][TM], const MmArg
     }
 }
 
-// Tile e of the list: its slots are the next of the stream, the first of them in
-// ring slot b.  The loads move to the next tile at the last slot but one.
+// One tile: its slots are the next to come out of the stream, the first of them in
+// ring slot b; the loads are part way into the slot after it.
 template <bool X8, int TM, bool F32OUT>
 __device__ __forceinline__ void tile_product(Loader<X8>& ld, const MmArgs& a, const uint8_t* lds, const Tile* list, int count,
-                                             int e, const Tile& t, const Lane& l, int nslots, uint32_t& b)
+                                             const Tile& t, const Lane& l, int nslots, uint32_t& b)
 {
-    const bool pad = a.K <= kSlotK;
     v16f acc[4][TM];
     Operands<X8, TM> f[2];
     Scales<TM> s;
     read_scales<TM>(s, lds, b, l);
     read_step<X8, TM, 0>(f[0], lds, b, l);
-    if (nslots == 2) ld.set_tile(a, list, e + 1, count, nslots);
-    slot_products<X8, TM, true, false>(acc, f, s, ld, lds, l, b);
-    ld.next_slot(a, pad);
-    for (int i = 1; i < nslots - 1; ++i) {
-        if (i == nslots - 2) ld.set_tile(a, list, e + 1, count, nslots);
-        slot_products<X8, TM, false, false>(acc, f, s, ld, lds, l, b);
-        ld.next_slot(a, false);
+    steps01<X8, TM, true>(acc, f, s, ld, lds, l, b);
+    pin<TM>(acc);
+    ld.advance(a, list, count, nslots);
+    for (int i = 1; i < nslots; ++i) {
+        steps23<X8, TM, false>(acc, f, s, ld, lds, l, b);
+        b ^= 1u;
+        steps01<X8, TM, false>(acc, f, s, ld, lds, l, b);
+        pin<TM>(acc);
+        ld.advance(a, list, count, nslots);
     }
-    if (a.K % kSlotK != 0) {                             // (the scales past K, too)
+    if (a.K % kSlotK != 0) {                             // (no scales past K)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s.w[i].y = 0;
 #pragma unroll
         for (int j = 0; j < TM; ++j) s.x[j].y = 0;
     }
-    slot_products<X8, TM, false, true>(acc, f, s, ld, lds, l, b);
-    ld.next_slot(a, false);
+    steps23<X8, TM, true>(acc, f, s, ld, lds, l, b);
+    pin<TM>(acc);
+    b ^= 1u;
     store_tile<TM, F32OUT>(acc, a, t, l);
 }
 
@@ -503,15 +532,15 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
     if (count > 0) {
         const Lane l = {(uint32_t)(lane & 31), (uint32_t)(lane >> 5), (uint32_t)((lane >> 1) & 7), (uint32_t)(lane & 15),
                         (uint32_t)(wave >> 1), (uint32_t)(wave & 1)};
-        // two slots at least: the second of a K of one slot is zeros
-        const int nslots = a.K <= kSlotK ? 2 : (a.K + kSlotK - 1) / kSlotK;
+        const int nslots = (a.K + kSlotK - 1) / kSlotK;
         Loader<X8> ld;
         ld.set_lanes(a, lds, wave, lane);
+        ld.entry = 0;
         ld.set_tile(a, list, 0, count, nslots);
-        ld.template issue_some<0, Loader<X8>::kLoads>(0);
-        ld.next_slot(a, a.K <= kSlotK);
-        ld.template issue_some<0, Loader<X8>::kLoads>(1);
-        ld.next_slot(a, false);
+        if (a.K < kSlotK) ld.toggle_half();
+        ld.template issue_some<0, kLoadsC>(0);
+        ld.advance(a, list, count, nslots);
+        ld.template issue_some<0, kLoadsA>(1);
         slot_barrier();
         uint32_t b = 0;
         for (int e = 0; e < count; ++e) {
@@ -522,9 +551,9 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
             t.c = uniform(t.c);
             // a group's last tile runs at the smallest of its heights that holds its rows
             const int rows = t.r1 - t.r0;
-            if (rows > R / 2) tile_product<X8, R / 64, F32OUT>(ld, a, lds, list, count, e, t, l, nslots, b);
-            else if (X8 || rows > R / 4) tile_product<X8, R / 128, F32OUT>(ld, a, lds, list, count, e, t, l, nslots, b);
-            else tile_product<X8, 1, F32OUT>(ld, a, lds, list, count, e, t, l, nslots, b);
+            if (rows > R / 2) tile_product<X8, R / 64, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
+            else if (X8 || rows > R / 4) tile_product<X8, R / 128, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
+            else tile_product<X8, 1, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
         }
         slot_barrier();                                  // the loads past the end land before the LDS goes away
     }
@@ -538,9 +567,6 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
 }
 
 }  // namespace
-
-// A K below one slot would need its first slot cut short, which only the last can be.
-int mxfp4_mm_tile_min_k() { return kSlotK; }
 
 hipError_t launch_mxfp4_mm_tile(const void* xq, const void* xs, bool x8, int64_t ldx, int64_t ldxs, const void* wq,
                                 const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
