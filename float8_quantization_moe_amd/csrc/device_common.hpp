@@ -234,6 +234,19 @@ __device__ __forceinline__ int wave_incl_sum(int v)
     return v;
 }
 
+// wave_incl_max of non-negative values with DPP alone (no LDS round trips).
+__device__ __forceinline__ int wave_incl_max_dpp(int v)
+{
+    auto up = [](int x, int moved) { return moved > x ? moved : x; };      // (lanes with no source get 0)
+    v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
+    v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+    v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+    v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+    v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));   // lane 15 of rows 0, 2 to rows 1, 3
+    v = up(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));   // lane 31 to rows 2 and 3
+    return v;
+}
+
 __device__ __forceinline__ int readlane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 }  // namespace mxq
