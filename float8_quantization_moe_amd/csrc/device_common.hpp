@@ -100,16 +100,16 @@ __device__ __forceinline__ uint32_t dpp_move(uint32_t v)
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E;               // quad permutations
 constexpr int kDppHalfMirror = 0x141, kDppMirror = 0x140;     // reversed within 8 and within 16 lanes
 
-// Reduction over each aligned run of L lanes (L = 16 or 64), the result in all
+// Reduction over each aligned run of L lanes (L = 8, 16 or 64), the result in all
 // of them.  A fixed order, so floating sums are reproducible; no LDS.
 template <int L, class F>
 __device__ __forceinline__ uint32_t lanes_reduce(uint32_t v, F op)
 {
-    static_assert(L == 16 || L == 64, "");
+    static_assert(L == 8 || L == 16 || L == 64, "");
     v = op(v, dpp_move<kDppXor1>(v));
     v = op(v, dpp_move<kDppXor2>(v));
     v = op(v, dpp_move<kDppHalfMirror>(v));
-    v = op(v, dpp_move<kDppMirror>(v));
+    if constexpr (L > 8) v = op(v, dpp_move<kDppMirror>(v));
     if constexpr (L == 64) {
         const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
         const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);

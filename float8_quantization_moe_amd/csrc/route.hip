@@ -13,17 +13,22 @@
 // Ties go to the lowest index, of groups and of experts.  A logit of -inf or NaN
 // (or a key of -inf or NaN) is never selected; slots that nothing is left for
 // get id -1 and weight 0.
-// All arithmetic is fp32 with the correctly rounded divide: the selection must
-// not depend on how a row is spread over lanes, so the keys use nothing but
-// operations on one value (and, for softmax with a bias, the row's sum).
+// All arithmetic is fp32.  The selection must not depend on how a row is spread over
+// lanes, so a key uses nothing but correctly rounded operations on its own value
+// and expf (and, for softmax with a bias, the row's sum).
 //
-// Forward layout: L lanes a row (16 lanes for E <= 256, so that a wave works on
-// four rows and each cross-lane step serves all four; 64 beyond), each with
-// 4 C values in registers: lane i holds experts 4 (i + L j) .. + 3.  A round of
-// the selection is an integer maximum over the row (the keys mapped to integers
-// of the same order, 0 for "not eligible"), then the lowest index that holds it;
-// both finish across the lanes with DPP.  Reading the logits is the floor; the
-// rounds' VALU work is what bounds it.
+// Forward layout: L lanes a row (8 lanes for E <= 64, so that a wave works on
+// eight rows and each cross-lane step serves all eight; 16 up to 256; 64 beyond), each with
+// 4 C values in registers: lane i holds experts 4 (i + L j) .. + 3.  A key and its
+// index become one 64-bit number, ordered as the keys and then by falling index (a
+// key of -inf: not eligible).  Each lane sorts its numbers once (a fixed network of f64 minima
+// and maxima: the bit patterns compare as doubles) and keeps the list in LDS; a
+// round of the selection is then the maximum of the lists' heads over the row's
+// lanes, with DPP, and the winner steps to its next.  Reading the logits is the
+// floor; VALU work is what bounds it (scores 17 and keys 10 instructions a value,
+// the sort 5, a round 20 for four rows).
+// 65536 x 128, sigmoid, bias, 4 of 8 groups, top-8: 24.1 us (8 lanes a row 26.2 at
+// its best; rounds that searched the registers instead of sorted lists 33).
 #include "device_common.hpp"
 #include "internal.hpp"
 
@@ -45,12 +50,75 @@ __device__ __forceinline__ uint32_t order_key(float f)
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
+// 1 / x for x >= 1, correctly rounded: one Newton step from the hardware's
+// reciprocal is exact for every float from 1 to 2^126 (checked one by one); past
+// that the quotient is subnormal and takes the divide, and 1 / inf is 0.
+__device__ __forceinline__ float reciprocal_step(float x)
+{
+    const float y = __builtin_amdgcn_rcpf(x);
+    return __builtin_fmaf(__builtin_fmaf(-x, y, 1.0f), y, y);
+}
+__device__ __forceinline__ float sigmoid_of(float l)
+{
+    const float x = 1.0f + expf(-l);
+    return x < 0x1p126f ? reciprocal_step(x) : 1.0f / x;
+}
+// The same for N values, with one branch.
+template <int N>
+__device__ __forceinline__ void sigmoids_of(const float (&l)[N], float (&s)[N])
+{
+    float x[N], most = 1.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = 1.0f + expf(-l[i]);
+        most = fmaxf(most, x[i]);
+        s[i] = reciprocal_step(x[i]);
+    }
+    if (most >= 0x1p126f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (x[i] >= 0x1p126f) s[i] = 1.0f / x[i];
+    }
+}
+
+// Key and index as one number; doubles of these bits are finite and in their order.
+__device__ __forceinline__ double ranked(uint32_t key, uint32_t id)
+{
+    return __hiloint2double((int)(key >> 1), (int)((key << 31) | (1023u - id)));
+}
+
+constexpr uint32_t kNoKey = 0x007FFFFFu >> 1;             // the high word of -inf: not eligible
+
+// Sorts v in falling order (odd-even merge network).
+template <int N>
+__device__ __forceinline__ void sort_falling(double (&v)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const double a = v[i + j], b = v[i + j + k];
+                        v[i + j] = __builtin_fmax(a, b);
+                        v[i + j + k] = __builtin_fmin(a, b);
+                    }
+}
+
+// The LDS operations of one wave run in order: this keeps the compiler's order too.
+__device__ __forceinline__ void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 // The 4 logits of experts e0 .. e0+3 of a row; -inf past E.  `vec`: rows are
 // aligned to 4 values (E % 4 == 0).
 template <bool F32L>
-__device__ __forceinline__ void load4(const void* row, int e0, int E, bool vec, float (&v)[4])
+__device__ __forceinline__ void load4(const void* row, int e0, int E, bool vec, float* v)
 {
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = MXQ_NEG_INF;
@@ -91,159 +159,189 @@ struct RouteArgs {
     bool renorm, top2;
 };
 
-// LDS of one workgroup, per row: E values (groups only), n_groups values, topk
-// ids and scores.
+// Rows are the work of single waves: no workgroup barrier.  A wave's LDS holds the
+// groups' values first, then the lanes' sorted lists.
 template <bool F32L, bool SIGMOID, int L, int C>
-__global__ __launch_bounds__(kRouteThreads)
+__global__ __launch_bounds__(kRouteThreads, C == 4 ? 3 : 6)      // (workgroups a CU; 4 would spill)
 void route_topk_kernel(const void* __restrict__ logits, const float* __restrict__ bias, int64_t M, RouteArgs a,
                        int32_t* __restrict__ ids, float* __restrict__ weights)
 {
     constexpr int kRows = kRouteThreads / L;
-    constexpr int kMaxE = 4 * L * C;
-    __shared__ float values[kRows][kMaxE + 4];
-    __shared__ float gvalues[kRows][kMaxE + 4];
-    __shared__ int32_t out_id[kRows][kRouteMaxTopk];
-    __shared__ float out_s[kRows][kRouteMaxTopk];
+    constexpr int NE = 4 * C, kMaxE = L * NE;
+    constexpr int kSlots = (kRouteMaxTopk + L - 1) / L;          // slots a lane finishes at most
+    __shared__ double lds[kRouteThreads * (NE + 1)];
     const int lane = (int)threadIdx.x % L, sub = (int)threadIdx.x / L;
+    double* list = lds + threadIdx.x * (NE + 1);
+    float* values = (float*)(lds + sub * L * (NE + 1));          // kMaxE values of the row, then of its groups
+    float* gvalues = values + kMaxE;
     const int E = a.E;
-    const bool vec = E % 4 == 0;
+    const bool vec = E % 4 == 0, bias_vec = ((uintptr_t)bias & 15u) == 0;
+    const bool groups = a.n_groups > 1;
+    // what all values of a row are needed for; the selected ones' scores are made again at the end
+    const bool all_scores = bias != nullptr || groups, total_needed = !SIGMOID && (all_scores || !a.renorm);
     for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < M; m0 += (int64_t)gridDim.x * kRows) {
         const int64_t m = m0 + sub;
         const bool live = m < M;
         const uint8_t* row = (const uint8_t*)logits + (live ? m : M - 1) * E * (F32L ? 4 : 2);
 
-        // scores s, and the row's poison: a NaN anywhere, or +inf under softmax
-        float l[C][4], s[C][4], v[C][4];
-        bool bad = false;
+        float l[NE], v[NE];
+        bool bad = false;                                        // a NaN anywhere, or +inf under softmax
         float top = MXQ_NEG_INF;
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-            load4<F32L>(row, 4 * (lane + L * j), E, vec, l[j]);
+        for (int j = 0; j < C; ++j) load4<F32L>(row, 4 * (lane + L * j), E, vec, l + 4 * j);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                bad |= l[j][c] != l[j][c] || (!SIGMOID && l[j][c] == -MXQ_NEG_INF);
-                top = fmaxf(top, l[j][c]);
-            }
+        for (int i = 0; i < NE; ++i) {
+            bad |= l[i] != l[i] || (!SIGMOID && l[i] == -MXQ_NEG_INF);
+            if constexpr (!SIGMOID) top = fmaxf(top, l[i]);
         }
+        bad = lanes_max<L>(bad ? 1u : 0u) != 0;
         float total = 1.0f;
         if constexpr (SIGMOID) {
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) v[j][c] = s[j][c] = sigmoid_of(l[j][c]);
+            if (all_scores) sigmoids_of<NE>(l, v);
         } else {
             top = lanes_max_f<L>(top);
             top = top > MXQ_NEG_INF ? top : 0.0f;
-            float sum = 0.0f;
+            if (total_needed) {
+                float sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < C; ++j)
+                for (int i = 0; i < NE; ++i) {
+                    v[i] = expf(l[i] - top);
+                    sum += v[i];
+                }
+                total = lanes_sum<L>(sum);
+                total = total > 0.0f ? total : 1.0f;
+            }
+        }
+
+        float key[NE];                                           // -inf: not eligible
+#pragma unroll
+        for (int i = 0; i < NE; ++i) key[i] = l[i];
+        if (bias) {                                              // (uniform)
+            const float unit = SIGMOID ? 1.0f : 1.0f / total;
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float b4[4];
+                load4<true>(bias, 4 * (lane + L * j), E, vec && bias_vec, b4);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    v[j][c] = expf(l[j][c] - top);
-                    sum += v[j][c];
+                    const int i = 4 * j + c;
+                    v[i] = (SIGMOID ? v[i] : v[i] * unit) + b4[c];
+                    key[i] = v[i];
                 }
-            total = lanes_sum<L>(sum);
-            total = total > 0.0f ? total : 1.0f;
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) s[j][c] = v[j][c] / total;
-        }
-        bad = lanes_max<L>(bad ? 1u : 0u) != 0;
-
-        // keys
-        uint32_t key[C][4];
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int e = 4 * (lane + L * j) + c;
-                float k = l[j][c];
-                if (bias) k = v[j][c] = s[j][c] + (e < E ? bias[e] : 0.0f);
-                const bool ok = l[j][c] > MXQ_NEG_INF && k > MXQ_NEG_INF;      // (false for NaN)
-                key[j][c] = ok ? order_key(k) : 0u;
-                if (a.n_groups > 1 && e < E) values[sub][e] = ok ? v[j][c] : MXQ_NEG_INF;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < NE; ++i) key[i] = l[i] > MXQ_NEG_INF && key[i] > MXQ_NEG_INF ? key[i] : MXQ_NEG_INF;   // (NaN too)
 
-        if (a.n_groups > 1) {                                     // (uniform)
-            __syncthreads();
+        if (groups) {                                            // (uniform)
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float4 w;
+                w.x = key[4 * j] > MXQ_NEG_INF ? v[4 * j] : MXQ_NEG_INF;
+                w.y = key[4 * j + 1] > MXQ_NEG_INF ? v[4 * j + 1] : MXQ_NEG_INF;
+                w.z = key[4 * j + 2] > MXQ_NEG_INF ? v[4 * j + 2] : MXQ_NEG_INF;
+                w.w = key[4 * j + 3] > MXQ_NEG_INF ? v[4 * j + 3] : MXQ_NEG_INF;
+                float* dst = values + 4 * (lane + L * j);
+                dst[0] = w.x, dst[1] = w.y, dst[2] = w.z, dst[3] = w.w;
+            }
+            wave_order();
             for (int g = lane; g < a.n_groups; g += L) {
                 float v1 = MXQ_NEG_INF, v2 = MXQ_NEG_INF;
+#pragma unroll 4
                 for (int i = 0; i < a.group_size; ++i) {
-                    const float t = values[sub][g * a.group_size + i];
+                    const float t = values[g * a.group_size + i];
                     v2 = fmaxf(v2, fminf(v1, t));
                     v1 = fmaxf(v1, t);
                 }
-                gvalues[sub][g] = a.top2 && v2 > MXQ_NEG_INF ? v1 + v2 : v1;
+                gvalues[g] = a.top2 && v2 > MXQ_NEG_INF ? v1 + v2 : v1;
             }
-            __syncthreads();
+            wave_order();
             // a group stays if fewer than topk_groups precede it; `values` becomes the flag
             for (int g = lane; g < a.n_groups; g += L) {
-                const float t = gvalues[sub][g];
+                const float t = gvalues[g];
                 int before = 0;
+#pragma unroll 4
                 for (int i = 0; i < a.n_groups; ++i) {
-                    const float u = gvalues[sub][i];
+                    const float u = gvalues[i];
                     before += u > t || (u == t && i < g) ? 1 : 0;
                 }
-                values[sub][g] = before < a.topk_groups ? 1.0f : 0.0f;
+                values[g] = before < a.topk_groups ? 1.0f : 0.0f;
             }
-            __syncthreads();
+            wave_order();
+            // (experts past E look at a group past the last: they are not eligible anyway)
+            if (a.group_size % 4 == 0) {                         // four neighbours are of one group
 #pragma unroll
-            for (int j = 0; j < C; ++j)
+                for (int j = 0; j < C; ++j) {
+                    const bool out = values[__umulhi((uint32_t)(4 * (lane + L * j)), a.group_magic)] == 0.0f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int e = 4 * (lane + L * j) + c;
-                    const int g = a.group_size > 1 ? (int)__umulhi((uint32_t)e, a.group_magic) : e;
-                    if (e < E && values[sub][g] == 0.0f) key[j][c] = 0u;
+                    for (int c = 0; c < 4; ++c) key[4 * j + c] = out ? MXQ_NEG_INF : key[4 * j + c];
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NE; ++i) {
+                    const uint32_t e = (uint32_t)(4 * (lane + L * (i / 4)) + i % 4);
+                    const uint32_t g = a.group_size > 1 ? __umulhi(e, a.group_magic) : e;
+                    key[i] = values[g] == 0.0f ? MXQ_NEG_INF : key[i];
+                }
+            }
+            wave_order();
         }
 
-        // topk rounds
-        float picked = 0.0f;                                      // this lane's part of the selected scores' sum
-        for (int t = 0; t < a.topk; ++t) {
-            uint32_t best = 0;
+        double r[NE];
 #pragma unroll
-            for (int j = 0; j < C; ++j)
+        for (int i = 0; i < NE; ++i) r[i] = ranked(order_key(key[i]), (uint32_t)(4 * (lane + L * (i / 4)) + i % 4));
+        sort_falling<NE>(r);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) best = key[j][c] > best ? key[j][c] : best;
-            best = lanes_max<L>(best);
-            uint32_t id = 0xFFFFFFFFu;
+        for (int i = 1; i < NE; ++i) list[i] = r[i];
+        list[NE] = 0.0;
+        wave_order();
+
+        int slot[kSlots];
+        uint32_t hi = (uint32_t)__double2hiint(r[0]), lo = (uint32_t)__double2loint(r[0]);
+        int at = 0;
 #pragma unroll
-            for (int j = C - 1; j >= 0; --j)
-#pragma unroll
-                for (int c = 3; c >= 0; --c)
-                    if (key[j][c] == best) id = (uint32_t)(4 * (lane + L * j) + c);
-            id = lanes_min<L>(id);
-#pragma unroll
-            for (int j = 0; j < C; ++j)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if ((uint32_t)(4 * (lane + L * j) + c) == id) {
-                        if (best != 0) {
-                            out_id[sub][t] = (int32_t)id;
-                            out_s[sub][t] = s[j][c];
-                            picked += s[j][c];
-                        }
-                        key[j][c] = 0u;
-                    }
-            if (best == 0 && lane == 0) {
-                out_id[sub][t] = -1;
-                out_s[sub][t] = 0.0f;
+        for (int tb = 0; tb < kSlots; ++tb) {
+            slot[tb] = -1;
+            const int n = a.topk - tb * L < L ? a.topk - tb * L : L;
+            for (int t = 0; t < n; ++t) {
+                const uint32_t best = lanes_max<L>(hi);
+                const uint32_t which = lanes_max<L>(hi == best ? lo : 0u);
+                if (lane == t && best > kNoKey) slot[tb] = (int)(1023u - (which & 1023u));
+                if (hi == best && lo == which) {             // (the list's end is 0, and 0 wins over nothing)
+                    ++at;
+                    const double next = list[at];
+                    hi = (uint32_t)__double2hiint(next);
+                    lo = (uint32_t)__double2loint(next);
+                }
             }
         }
-        const float sum = lanes_sum<L>(picked) + kTiny;
-        __syncthreads();
-        for (int t = lane; t < a.topk; t += L) {
-            float w = out_s[sub][t];
+
+        float s[kSlots], sum = 0.0f;
+#pragma unroll
+        for (int tb = 0; tb < kSlots; ++tb) {
+            s[tb] = 0.0f;
+            if (slot[tb] >= 0) {
+                float x;
+                if constexpr (F32L) x = ((const float*)row)[slot[tb]];
+                else x = bf16_lo_to_f32(((const uint16_t*)row)[slot[tb]]);
+                s[tb] = SIGMOID ? sigmoid_of(x) : expf(x - top) / total;
+            }
+            sum += s[tb];
+        }
+        sum = lanes_sum<L>(sum) + kTiny;
+#pragma unroll
+        for (int tb = 0; tb < kSlots; ++tb) {
+            const int t = lane + L * tb;
+            float w = s[tb];
             if (a.renorm) w /= sum;
             w *= a.scale;
             if (bad) w = __builtin_nanf("");
-            if (live) {
-                ids[m * a.topk + t] = out_id[sub][t];
+            if (live && t < a.topk) {
+                ids[m * a.topk + t] = slot[tb];
                 weights[m * a.topk + t] = w;
             }
         }
-        __syncthreads();
+        wave_order();
     }
 }
 
@@ -383,7 +481,8 @@ constexpr int64_t kRouteMaxGrid = 1 << 22;
 // Lanes a row and values a lane for E experts.
 #define MXQ_ROUTE_SHAPE(E, CALL)         \
     do {                                 \
-        if ((E) <= 64) CALL(16, 1);      \
+        if ((E) <= 32) CALL(8, 1);       \
+        else if ((E) <= 64) CALL(8, 2);  \
         else if ((E) <= 128) CALL(16, 2);\
         else if ((E) <= 256) CALL(16, 4);\
         else if ((E) <= 512) CALL(64, 2);\

@@ -168,8 +168,15 @@ def group_scale_knobs(**kw):
         mxq_set_group_scale_knobs()
 
 
+# The current stream's handle without building a torch.cuda.Stream object (0.1 us
+# instead of 2.9 us a call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
