@@ -264,7 +264,8 @@ void mxfp4_mm_few_kernel(const FewArgs a)
 
 bool mxfp4_mm_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t G)
 {
-    if (M > ((int64_t)1 << 31) - 1024 || N > ((int64_t)1 << 31) - 1024) return false;
+    // (K: the 256 rows of a tile stay within a buffer resource of 2^31 bytes)
+    if (M > ((int64_t)1 << 31) - 1024 || N > ((int64_t)1 << 31) - 1024 || K > ((int64_t)1 << 22)) return false;
     return grouped_mm_sizes_ok(M, N, K, G);
 }
 

@@ -3,15 +3,14 @@
 // calls with few rows).
 //
 // Persistent workgroups (one a CU, 4 waves in 2 x 2) walk over output tiles of 256
-// columns x R rows: R = 256 for E2M1 tokens, 128 for E4M3 tokens, whose codes take
-// twice the space and whose MFMA takes twice the time, so that the K loop has one
-// shape for both.  K advances 256 values a slot through a 2-slot LDS ring of 32 KB
-// of W and 32 KB of X codes and 16 bytes of scales a row, filled by
+// columns x 256 rows (128 where that leaves CUs idle).  K advances 256 values a slot through a 2-slot LDS ring of 32 KB
+// of W codes, 32 KB of X codes (of E4M3 tokens, with twice the bytes and MFMAs of twice
+// the time, half a slot's) and 16 bytes of scales a row, filled by
 // buffer-load-to-LDS in whole 128-byte lines.  A slot is four MFMA steps of 64 k; a
 // step's operands are read from LDS during the step before it.  The one barrier that
 // a slot needs comes before its last step, when all its operands are in registers:
 // the loads of the slot after next go into its place from there on, spread between
-// the MFMAs of three steps.
+// the MFMAs of three steps.  (E4M3: a second barrier half way, for the X codes.)
 //
 // The slots of successive tiles form one stream: the loads run ahead of the
 // products across the end of a tile, so the next tile's operands arrive while this
@@ -45,7 +44,14 @@ constexpr uint32_t kEntryBase = kScaleBase + 2 * 2 * kScaleOperand;
 constexpr int kMaxEntries = 1024;                        // tiles of one workgroup
 constexpr uint32_t kLdsBytes = kEntryBase + kMaxEntries * 16;
 static_assert(kLdsBytes <= 160 * 1024, "LDS of a CU");
-constexpr int kColBlock = 4;                             // column tiles of a block of the tile order
+// Tiles of 128 rows while there is less than one of 256 rows for each CU: 777 ragged
+// rows x 1736 x 1408 over 16 groups (126 tiles of 256 rows) 16.2 / 13.4 us (E4M3 /
+// E2M1) against 23.6 / 17.8; 2048 x 8192 x 5120 over 4 groups (384) 114 / 87 against
+// 119 / 78; one group of 16384 rows 632 / 486 against 538 / 379.
+constexpr int kManyTiles = 1;
+// Column tiles of a block of the tile order; one group of 16384 x 8192 x 5120, E4M3: 2
+// 521 us, 3 533, 4 580, 8 575 (1 measured slower before); 16 groups 625 / 642 / 643 / 691.
+constexpr int kColBlock = 2;                             // column tiles of a block of the tile order
 constexpr int kXcds = 8;
 constexpr int kMaxGroups = 4095;
 static_assert((2 * (kMaxGroups + 2) + kThreads) * 4 <= (int)kScaleBase, "the scan's arrays fit the ring");
@@ -65,10 +71,8 @@ struct MmArgs {
     void* y;
     uint32_t ldx, ldxs;
     int M, N, K, G;
+    int rows;                                            // token rows of a tile, at most: 128 or 256
 };
-
-template <bool X8>
-constexpr int tile_rows() { return X8 ? 128 : 256; }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -89,12 +93,13 @@ __device__ __forceinline__ void load_to_lds(const v4i& srd, uint32_t lds, uint32
                  : "memory");
 }
 
-// Every load of this wave has landed and its LDS reads are done; then meet the
-// other waves.
+// At most N of this wave's loads are still under way (the last ones issued) and its
+// LDS reads are done; then meet the other waves.
+template <int N>
 __device__ __forceinline__ void slot_barrier()
 {
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -116,10 +121,9 @@ __device__ int block_scan(int v, int* sh)
 // Fills `list` with this workgroup's tiles and returns their number; *rows_end is
 // the last group's clamped end.  end_sh: the groups' clamped ends; first_sh: each
 // group's first row tile.
-template <int R>
 __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_sh, Tile* list, int* rows_end)
 {
-    const int t = (int)threadIdx.x;
+    const int t = (int)threadIdx.x, R = a.rows;
     const int per = (a.G + kThreads - 1) / kThreads;
     const int ga = t * per < a.G ? t * per : a.G, gb = ga + per < a.G ? ga + per : a.G;
     int top = 0;
@@ -180,111 +184,153 @@ __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_
 }
 
 // ------------------------------------------------------------------ loads ---
-// The stream of slots to load: the current tile's resources and its next slot.
-// LDS rows of 128 bytes hold their eight 16-byte chunks at c ^ ((row >> 1) & 7),
-// rows of 256 bytes (E4M3) their sixteen at c ^ (row & 15): the 16 lanes that a
-// 128-bit LDS read serves at a time then meet 16 different bank groups.  The
-// swizzle is applied to the source offsets (the LDS side is linear in the lane).
+// The stream of slots to load.  E2M1 tokens: a slot's X codes (128 bytes a row)
+// travel with its W codes and scales.  E4M3 tokens: 256 bytes a row, in two halves
+// that each have one place in LDS; they run a slot behind the W codes, half by half.
+//
+// LDS rows of 128 bytes hold their eight 16-byte chunks at c ^ ((row >> 1) & 7): the
+// 16 lanes that a 128-bit LDS read serves at a time then meet 16 different bank
+// groups.  The swizzle is applied to the source offsets (the LDS side is linear in
+// the lane).
 template <bool X8>
 struct Loader {
-    v4i w, x, ws, xs;                                    // resources that start at the next slot
-    uint32_t off_w[8], off_x[8], off_ws, off_xs;         // lane offsets of the wave's loads
-    uint32_t lds_data, lds_ws, lds_xs;                   // LDS addresses of the wave's part of ring slot 0
-    uint32_t upper;                                      // bit 31: this lane's chunk of load 0 is in the second half of a row's slot
+    v4i w, ws, xs;                                       // resources that start at the next slot
+    v4i x, xb;                                           // X8: at its first half's and the running slot's second half
     int entry, left;                                     // the tile's place in the list; its slots from the next one on
-    static constexpr int kXStep = X8 ? 256 : 128;        // bytes of an X row in a slot
+    int xentry, xleft;                                   // X8: the same of the X codes
+    uint32_t off_w[8], off_x[8], off_ws, off_xs;         // lane offsets of the wave's loads, 8 rows each
+    uint32_t lds_data, lds_scale;                        // LDS addresses of the wave's part of ring slot 0
+    uint32_t upper;                                      // bit 31: this lane's chunk of load 0 is in the second half of a row's slot
 
     __device__ __forceinline__ void set_lanes(const MmArgs& a, const uint8_t* lds, int wave, int lane)
     {
         const uint32_t half = (uint32_t)a.K / 2u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t row = (uint32_t)(64 * wave + 8 * i + (lane >> 3));        // 8 rows of 128 bytes a load
+            const uint32_t row = (uint32_t)(64 * wave + 8 * i + (lane >> 3));
             const uint32_t chunk = ((uint32_t)lane & 7u) ^ ((row >> 1) & 7u);
             off_w[i] = row * half + 16u * chunk;
-            if constexpr (X8) {
-                const uint32_t xrow = (uint32_t)(32 * wave + 4 * i + (lane >> 4));   // 4 rows of 256 bytes a load
-                off_x[i] = xrow * a.ldx + 16u * (((uint32_t)lane & 15u) ^ (xrow & 15u));
-            } else {
-                off_x[i] = row * a.ldx + 16u * chunk;
-            }
+            off_x[i] = row * a.ldx + 16u * chunk;
         }
-        const int xw = X8 ? wave & 1 : wave;             // 128 rows: two waves bring the same scales
-        upper = ((uint32_t)lane >> (X8 ? 3 : 2)) << 31;
+        upper = ((uint32_t)lane >> 2) << 31;
         off_ws = (uint32_t)(64 * wave + lane) * ((uint32_t)a.K / 32u);
-        off_xs = (uint32_t)(64 * xw + lane) * a.ldxs;
+        off_xs = (uint32_t)(64 * wave + lane) * a.ldxs;
         const uint32_t base = (uint32_t)uniform((int)(uint32_t)(uintptr_t)(LdsPtr)lds);
         lds_data = base + 8192u * (uint32_t)wave;
-        lds_ws = base + kScaleBase + 1024u * (uint32_t)wave;
-        lds_xs = base + kScaleBase + kScaleOperand + 1024u * (uint32_t)xw;
+        lds_scale = base + kScaleBase + 1024u * (uint32_t)wave;
     }
 
-    // The first slot of tile `entry` of the list; past its end, loads of nothing.
-    __device__ __forceinline__ void set_tile(const MmArgs& a, const Tile* list, int e, int count, int nslots)
+    // Tile e of the list; past its end, one that loads nothing.
+    struct Place {
+        int64_t wrow;
+        int r0;
+        uint32_t nw, nx;
+    };
+    static __device__ __forceinline__ Place place_of(const MmArgs& a, const Tile* list, int e, int count)
     {
-        left = nslots;
-        const uint32_t half = (uint32_t)a.K / 2u, kb = (uint32_t)a.K / 32u;
         const bool some = e < count;
         const Tile t = list[some ? e : 0];
-        const int g = some ? uniform(t.g) : 0, r0 = some ? uniform(t.r0) : 0;
-        const uint32_t nx = some ? (uint32_t)(uniform(t.r1) - r0) : 1u;
+        const int g = some ? uniform(t.g) : 0;
         const int n0 = some ? uniform(t.c) * kCols : 0;
-        const uint32_t nw = (uint32_t)(a.N - n0 < kCols ? a.N - n0 : kCols);
-        const int64_t wrow = (int64_t)g * a.N + n0;
-        w = resource(a.wq + wrow * half, some ? nw * half : 0u);
-        ws = resource(a.ws + wrow * kb, some ? nw * kb : 0u);
-        x = resource(a.xq + (int64_t)r0 * a.ldx, some ? (nx - 1u) * a.ldx + (X8 ? (uint32_t)a.K : half) : 0u);
-        xs = resource(a.xs + (int64_t)r0 * a.ldxs, some ? (nx - 1u) * a.ldxs + kb : 0u);
+        Place p;
+        p.r0 = some ? uniform(t.r0) : 0;
+        p.nx = some ? (uint32_t)(uniform(t.r1) - p.r0) : 0u;
+        p.nw = some ? (uint32_t)(a.N - n0 < kCols ? a.N - n0 : kCols) : 0u;
+        p.wrow = (int64_t)g * a.N + n0;
+        return p;
+    }
+    // The first slot of tile `entry`: W codes and both scales, and of E2M1 tokens the X codes.
+    __device__ __forceinline__ void set_tile(const MmArgs& a, const Tile* list, int count, int nslots)
+    {
+        const uint32_t half = (uint32_t)a.K / 2u, kb = (uint32_t)a.K / 32u;
+        const Place p = place_of(a, list, entry, count);
+        left = nslots;
+        w = resource(a.wq + p.wrow * half, p.nw * half);
+        ws = resource(a.ws + p.wrow * kb, p.nw * kb);
+        xs = resource(a.xs + (int64_t)p.r0 * a.ldxs, p.nx ? (p.nx - 1u) * a.ldxs + kb : 0u);
+        if constexpr (!X8) x = resource(a.xq + (int64_t)p.r0 * a.ldx, p.nx ? (p.nx - 1u) * a.ldx + half : 0u);
+    }
+    __device__ __forceinline__ void set_x_tile(const MmArgs& a, const Tile* list, int count, int nslots)
+    {
+        const Place p = place_of(a, list, xentry, count);
+        xleft = nslots;
+        x = resource(a.xq + (int64_t)p.r0 * a.ldx, p.nx ? (p.nx - 1u) * a.ldx + (uint32_t)a.K : 0u);
     }
 
-    static __device__ __forceinline__ void step(v4i& r, uint32_t bytes)
+    // (Signed, so that the bound is a scalar maximum: an unsigned saturating subtraction
+    // is vector code, and the resources have to stay in scalar registers.)
+    static __device__ __forceinline__ v4i stepped(const v4i& r, int bytes, bool nothing = false)
     {
-        const uint64_t base = (((uint64_t)(uint32_t)r.y << 32) | (uint32_t)r.x) + bytes;
-        const uint32_t left = (uint32_t)r.z;
-        r.x = uniform((int)(uint32_t)base);              // (resources stay in scalar registers)
-        r.y = uniform((int)(uint32_t)(base >> 32));
-        r.z = uniform((int)(left < bytes ? 0u : left - bytes));
+        const uint64_t base = (((uint64_t)(uint32_t)r.y << 32) | (uint32_t)r.x) + (uint32_t)bytes;
+        const int left = r.z - bytes > 0 ? r.z - bytes : 0;
+        return v4i{(int)(uint32_t)base, (int)(uint32_t)(base >> 32), nothing ? 0 : left, 0x00020000};
     }
     // On to the next slot of the stream.  Where K ends half way through a tile's last
-    // slot, that slot's X codes past K are to be zeros: for its loads their lanes'
-    // offsets leave the resource (bit 31).
+    // slot, that slot's X codes past K are to be zeros: E4M3, its second half loads
+    // nothing; E2M1, for its loads their lanes' offsets leave the resource (bit 31).
     __device__ __forceinline__ void advance(const MmArgs& a, const Tile* list, int count, int nslots)
     {
+        if constexpr (X8) {
+            xb = stepped(x, 128, xleft == 1 && a.K % kSlotK != 0);
+            if (xleft == 1) {
+                ++xentry;
+                set_x_tile(a, list, count, nslots);
+            } else {
+                --xleft;
+                x = stepped(x, 256);
+            }
+        }
         const bool was_last = left == 1;
         if (was_last) {
-            set_tile(a, list, ++entry, count, nslots);
+            ++entry;
+            set_tile(a, list, count, nslots);
         } else {
             --left;
-            step(w, 128u);
-            step(x, kXStep);
-            step(ws, 8u);
-            step(xs, 8u);
+            w = stepped(w, 128);
+            ws = stepped(ws, 8);
+            xs = stepped(xs, 8);
+            if constexpr (!X8) x = stepped(x, 128);
         }
-        if (a.K % kSlotK != 0 && was_last != (left == 1)) toggle_half();
+        if constexpr (!X8) {
+            if (a.K % kSlotK != 0 && was_last != (left == 1)) toggle_half();
+        }
     }
     __device__ __forceinline__ void toggle_half()
     {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) off_x[i] ^= (i & (X8 ? 2 : 1)) ? upper ^ 0x80000000u : upper;
+        for (int i = 0; i < 8; ++i) off_x[i] ^= (i & 1) ? upper ^ 0x80000000u : upper;
     }
 
-    // Load I (0 .. 17) of the slot into ring slot b.
+    // Load I of the slot into ring slot b: 0, 1 the scales, then W and (E2M1) X codes.
+    static constexpr int kLoads = X8 ? 10 : 18;
     template <int I>
     __device__ __forceinline__ void issue(uint32_t b)
     {
-        constexpr int i = (I - 2) / 2;
-        if constexpr (I == 0) load_to_lds(ws, lds_ws + b * 2u * kScaleOperand, off_ws);
-        else if constexpr (I == 1) load_to_lds(xs, lds_xs + b * 2u * kScaleOperand, off_xs);
-        else if constexpr (I % 2 == 0) load_to_lds(w, lds_data + b * kSlotBytes + 1024u * i, off_w[i]);
-        else load_to_lds(x, lds_data + b * kSlotBytes + kOperandBytes + 1024u * i, off_x[i]);
+        if constexpr (I == 0) {
+            load_to_lds(ws, lds_scale + b * 2u * kScaleOperand, off_ws);
+        } else if constexpr (I == 1) {
+            load_to_lds(xs, lds_scale + b * 2u * kScaleOperand + kScaleOperand, off_xs);
+        } else {
+            constexpr int i = X8 ? I - 2 : (I - 2) / 2;
+            if constexpr (X8 || I % 2 == 0) load_to_lds(w, lds_data + b * kSlotBytes + 1024u * i, off_w[i]);
+            else load_to_lds(x, lds_data + b * kSlotBytes + kOperandBytes + 1024u * i, off_x[i]);
+        }
     }
-
     template <int I, int END>
     __device__ __forceinline__ void issue_some(uint32_t b)
     {
         if constexpr (I < END) {
             issue<I>(b);
             issue_some<I + 1, END>(b);
+        }
+    }
+    // X8: loads I .. END - 1 (of 8) of X half H.
+    template <int H, int I, int END>
+    __device__ __forceinline__ void issue_x()
+    {
+        if constexpr (I < END) {
+            load_to_lds(H ? xb : x, lds_data + H * kSlotBytes + kOperandBytes + 1024u * I, off_x[I]);
+            issue_x<H, I + 1, END>();
         }
     }
 };
@@ -301,7 +347,7 @@ struct Scales {
 };
 
 struct Lane {
-    uint32_t row, h, swz, swx;                           // lane % 32, lane / 32, and its rows' swizzles
+    uint32_t row, h, swz;                                // lane % 32, lane / 32, and its rows' swizzle
     uint32_t wn, wm;                                     // the wave's place in the 2 x 2
 };
 
@@ -311,20 +357,12 @@ __device__ __forceinline__ void read_step(Operands<X8, TM>& f, const uint8_t* ld
     const uint8_t* W = lds + b * kSlotBytes + (128u * l.wn + l.row) * 128u + (((2u * T + l.h) ^ l.swz) << 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.w[i] = *(const v4i*)(W + 4096 * i);
-    if constexpr (X8) {
-        const uint8_t* X = lds + b * kSlotBytes + kOperandBytes + (32u * TM * l.wm + l.row) * 256u;
-        const uint8_t* X0 = X + (((4u * T + l.h) ^ l.swx) << 4);
-        const uint8_t* X1 = X + (((4u * T + 2u + l.h) ^ l.swx) << 4);
+    const uint8_t* X = lds + (X8 ? (uint32_t)(T / 2) : b) * kSlotBytes + kOperandBytes + (32u * TM * l.wm + l.row) * 128u;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            f.x[i][0] = *(const v4i*)(X0 + 8192 * i);
-            f.x[i][1] = *(const v4i*)(X1 + 8192 * i);
-        }
-    } else {
-        const uint8_t* X = lds + b * kSlotBytes + kOperandBytes + (32u * TM * l.wm + l.row) * 128u +
-                           (((2u * T + l.h) ^ l.swz) << 4);
+    for (int p = 0; p < (X8 ? 2 : 1); ++p) {
+        const uint8_t* P = X + ((((X8 ? 4u * (T % 2) + 2u * p : 2u * T) + l.h) ^ l.swz) << 4);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) f.x[i][0] = *(const v4i*)(X + 4096 * i);
+        for (int i = 0; i < TM; ++i) f.x[i][p] = *(const v4i*)(P + 4096 * i);
     }
 }
 
@@ -366,48 +404,57 @@ __device__ __forceinline__ void mfma(v16f (&acc)[4][TM], const Operands<X8, TM>&
 }
 
 // Step T's MFMAs, with loads A .. B - 1 of the next slot of the stream into ring
-// slot b spread between them.
-template <bool X8, int TM, int T, bool ZERO, int A, int B, int I = 0>
+// slot b and (X8) loads XA .. XB - 1 of X half H spread between them.
+template <bool X8, int TM, int T, bool ZERO, int A, int B, int H = 0, int XA = 0, int XB = 0, int I = 0>
 __device__ __forceinline__ void mfmas(v16f (&acc)[4][TM], const Operands<X8, TM>& f, const Scales<TM>& s, Loader<X8>& ld,
                                       uint32_t b)
 {
     constexpr int n = 4 * TM;
     if constexpr (I < n) {
         mfma<X8, TM, T, ZERO, I>(acc, f, s);
+        ld.template issue_x<H, XA + I * (XB - XA) / n, XA + (I + 1) * (XB - XA) / n>();
         ld.template issue_some<A + I * (B - A) / n, A + (I + 1) * (B - A) / n>(b);
-        if constexpr (A < B) __builtin_amdgcn_sched_barrier(0);
-        mfmas<X8, TM, T, ZERO, A, B, I + 1>(acc, f, s, ld, b);
+        if constexpr (A < B || XA < XB) __builtin_amdgcn_sched_barrier(0);
+        mfmas<X8, TM, T, ZERO, A, B, H, XA, XB, I + 1>(acc, f, s, ld, b);
     }
 }
 
 // How a slot's loads are spread: the first kLoadsA in the last step of the slot two
 // before it, up to kLoadsB in the first step of the slot before it, the rest in the
-// second.  All 18 at once fill the memory pipe's queue and hold up the MFMAs behind
-// them: 16640 x 8192 x 5120 over 16 groups 723 / 481 us (E4M3 / E2M1 tokens) against
-// 658 / 451 in thirds (9 + 9: 662 / 450; 12 + 6: 687 / 466).
-constexpr int kLoadsA = 6, kLoadsB = 12, kLoadsC = 18;
+// second (E2M1 only).  All 18 of E2M1 at once fill the memory pipe's queue and hold up
+// the MFMAs behind them: 16640 x 8192 x 5120 over 16 groups 481 us against 451 in
+// thirds (9 + 9: 450; 12 + 6: 466).  X8: the halves' loads go out in steps 1 and 3.
+template <bool X8>
+struct Spread {
+    static constexpr int kLoadsA = X8 ? 3 : 6, kLoadsB = X8 ? 10 : 12, kLoadsC = X8 ? 10 : 18;
+};
 
-// Steps 0 and 1 of the slot in ring slot b, with the second part of the loads of
-// the slot after it.  f[0] and s hold (or are being read with) its first step and
-// scales; f[1] is left with step 1's successor: f[0] holds step 2.
+// Steps 0 and 1 of the slot in ring slot b, with the second part of the loads of the
+// slot after it.  On entry f[0] and s hold (or are being read with) its first step
+// and scales, on exit f[0] step 2.  X8: between them the barrier after which the
+// first X half's place may be loaded anew and the second half has landed (step 0's
+// own loads may still be under way: they are the W codes of the next slot).
 template <bool X8, int TM, bool FIRST>
 __device__ __forceinline__ void steps01(v16f (&acc)[4][TM], Operands<X8, TM> (&f)[2], Scales<TM>& s, Loader<X8>& ld,
                                         const uint8_t* lds, const Lane& l, uint32_t b)
 {
+    using S = Spread<X8>;
     shift_scales<TM>(s, l);
     read_step<X8, TM, 1>(f[1], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
-    mfmas<X8, TM, 0, FIRST, kLoadsA, kLoadsB>(acc, f[0], s, ld, b ^ 1u);
-    __builtin_amdgcn_sched_barrier(0);
+    mfmas<X8, TM, 0, FIRST, S::kLoadsA, S::kLoadsB>(acc, f[0], s, ld, b ^ 1u);
+    if constexpr (X8) slot_barrier<S::kLoadsB - S::kLoadsA>();
+    else __builtin_amdgcn_sched_barrier(0);
     read_step<X8, TM, 2>(f[0], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
-    mfmas<X8, TM, 1, false, kLoadsB, kLoadsC>(acc, f[1], s, ld, b ^ 1u);
+    if constexpr (X8) mfmas<X8, TM, 1, false, 0, 0, 0, 0, 8>(acc, f[1], s, ld, b);
+    else mfmas<X8, TM, 1, false, S::kLoadsB, S::kLoadsC>(acc, f[1], s, ld, b ^ 1u);
     __builtin_amdgcn_sched_barrier(0);
 }
 
 // Steps 2 and 3, with the barrier between them and the first part of the loads into
-// this ring slot; on exit f[0] and s hold the next slot's, unless this is the
-// tile's LAST.
+// this ring slot (X8: and those of the second X half); on exit f[0] and s hold the
+// next slot's, unless this is the tile's LAST.
 template <bool X8, int TM, bool LAST>
 __device__ __forceinline__ void steps23(v16f (&acc)[4][TM], Operands<X8, TM> (&f)[2], Scales<TM>& s, Loader<X8>& ld,
                                         const uint8_t* lds, const Lane& l, uint32_t b)
@@ -415,14 +462,14 @@ __device__ __forceinline__ void steps23(v16f (&acc)[4][TM], Operands<X8, TM> (&f
     read_step<X8, TM, 3>(f[1], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
     mfmas<X8, TM, 2, false, 0, 0>(acc, f[0], s, ld, b);
-    slot_barrier();
+    slot_barrier<0>();
     const Scales<TM> now = s;
     if constexpr (!LAST) {
         read_step<X8, TM, 0>(f[0], lds, b ^ 1u, l);
         read_scales<TM>(s, lds, b ^ 1u, l);
         __builtin_amdgcn_sched_barrier(0);
     }
-    mfmas<X8, TM, 3, false, 0, kLoadsA>(acc, f[1], now, ld, b);
+    mfmas<X8, TM, 3, false, 0, Spread<X8>::kLoadsA, 1, 0, X8 ? 8 : 0>(acc, f[1], now, ld, b);
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -515,7 +562,6 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
 void mxfp4_mm_tile_kernel(const MmArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
-    constexpr int R = tile_rows<X8>();
     const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
     Tile* list = (Tile*)(lds + kEntryBase);
     int rows_end;
@@ -524,24 +570,28 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
         int* end_sh = (int*)lds;
         int* first_sh = end_sh + kMaxGroups + 1;
         int* scan_sh = first_sh + kMaxGroups + 1;
-        count = uniform(make_list<R>(a, end_sh, first_sh, scan_sh, list, &rows_end));
+        count = uniform(make_list(a, end_sh, first_sh, scan_sh, list, &rows_end));
         rows_end = uniform(rows_end);
     }
     __syncthreads();                                     // the list is complete, the scan's arrays are free
 
     if (count > 0) {
-        const Lane l = {(uint32_t)(lane & 31), (uint32_t)(lane >> 5), (uint32_t)((lane >> 1) & 7), (uint32_t)(lane & 15),
+        const Lane l = {(uint32_t)(lane & 31), (uint32_t)(lane >> 5), (uint32_t)((lane >> 1) & 7),
                         (uint32_t)(wave >> 1), (uint32_t)(wave & 1)};
         const int nslots = (a.K + kSlotK - 1) / kSlotK;
+        using S = Spread<X8>;
         Loader<X8> ld;
         ld.set_lanes(a, lds, wave, lane);
-        ld.entry = 0;
-        ld.set_tile(a, list, 0, count, nslots);
-        if (a.K < kSlotK) ld.toggle_half();
-        ld.template issue_some<0, kLoadsC>(0);
+        ld.entry = ld.xentry = 0;
+        ld.set_tile(a, list, count, nslots);
+        if constexpr (X8) ld.set_x_tile(a, list, count, nslots);
+        else if (a.K < kSlotK) ld.toggle_half();
+        ld.template issue_some<0, S::kLoadsC>(0);
+        if constexpr (X8) ld.template issue_x<0, 0, 8>();
         ld.advance(a, list, count, nslots);
-        ld.template issue_some<0, kLoadsA>(1);
-        slot_barrier();
+        if constexpr (X8) ld.template issue_x<1, 0, 8>();
+        ld.template issue_some<0, S::kLoadsA>(1);
+        slot_barrier<0>();
         uint32_t b = 0;
         for (int e = 0; e < count; ++e) {
             Tile t = list[e];
@@ -549,13 +599,13 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
             t.r0 = uniform(t.r0);
             t.r1 = uniform(t.r1);
             t.c = uniform(t.c);
-            // a group's last tile runs at the smallest of its heights that holds its rows
+            // a group's last tile runs at the smallest of three heights that holds its rows
             const int rows = t.r1 - t.r0;
-            if (rows > R / 2) tile_product<X8, R / 64, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
-            else if (X8 || rows > R / 4) tile_product<X8, R / 128, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
+            if (rows > 128) tile_product<X8, 4, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
+            else if (rows > 64) tile_product<X8, 2, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
             else tile_product<X8, 1, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
         }
-        slot_barrier();                                  // the loads past the end land before the LDS goes away
+        slot_barrier<0>();                               // the loads past the end land before the LDS goes away
     }
 
     // rows past the last end: zeros
@@ -572,20 +622,22 @@ hipError_t launch_mxfp4_mm_tile(const void* xq, const void* xs, bool x8, int64_t
                                 const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
                                 hipStream_t stream)
 {
-    const MmArgs a = {(const uint8_t*)xq, (const uint8_t*)xs, (const uint8_t*)wq, (const uint8_t*)wsc, offs, y,
-                      (uint32_t)ldx, (uint32_t)ldxs, M, N, K, G};
     int device = 0, cus = 0;
     hipError_t e = hipGetDevice(&device);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
     if (e != hipSuccess) return e;
+    const int64_t cols = (N + kCols - 1) / kCols;
+    const auto tiles = [&](int rows) { return (((int64_t)M + rows - 1) / rows + G) * cols; };   // at most
+    const int rows = tiles(256) >= kManyTiles * cus ? 256 : 128;
     // One workgroup a CU, fewer when there are not that many tiles, more (which then run one
     // after the other) when a workgroup's list would not hold its tiles.
-    const int rows = x8 ? tile_rows<true>() : tile_rows<false>();
-    const int64_t most = (((int64_t)M + rows - 1) / rows + G) * ((N + kCols - 1) / kCols);
+    const int64_t most = tiles(rows);
     int64_t grid = most < cus ? most : cus;
     const int64_t least = (most + kMaxEntries - kXcds - 1) / (kMaxEntries - kXcds);
     grid = grid < least ? least : grid;
     grid = (grid + kXcds - 1) / kXcds * kXcds;
+    const MmArgs a = {(const uint8_t*)xq, (const uint8_t*)xs, (const uint8_t*)wq, (const uint8_t*)wsc, offs, y,
+                      (uint32_t)ldx, (uint32_t)ldxs, M, N, K, G, rows};
 #define MXQ_LAUNCH(X8, F) \
     hipLaunchKernelGGL((mxfp4_mm_tile_kernel<X8, F>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a)
     if (x8 && f32_out) MXQ_LAUNCH(true, true);

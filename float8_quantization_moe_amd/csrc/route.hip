@@ -162,7 +162,7 @@ struct RouteArgs {
 // Rows are the work of single waves: no workgroup barrier.  A wave's LDS holds the
 // groups' values first, then the lanes' sorted lists.
 template <bool F32L, bool SIGMOID, int L, int C>
-__global__ __launch_bounds__(kRouteThreads, C == 4 ? 3 : 6)      // (workgroups a CU; 4 would spill)
+__global__ __launch_bounds__(kRouteThreads, C == 4 ? 3 : 5)      // (workgroups a CU; one more would spill)
 void route_topk_kernel(const void* __restrict__ logits, const float* __restrict__ bias, int64_t M, RouteArgs a,
                        int32_t* __restrict__ ids, float* __restrict__ weights)
 {

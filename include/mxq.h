@@ -571,7 +571,7 @@ mxq_status mxq_dequantize_mxfp4(const void* q_e2m1, const void* s_e8m0, int64_t 
  * in fp32 and the result is rounded once.  NaN codes and scale 0xFF are outside
  * the contract.  Weights are constants of a serving program: there is no backward.
  *
- * Requires K > 0, K % 128 == 0, K <= 2^23, N % 8 == 0, 0 <= M, N <= 2^31 - 1024,
+ * Requires K > 0, K % 128 == 0, K <= 2^22, N % 8 == 0, 0 <= M, N <= 2^31 - 1024,
  * 1 <= G <= 4095 and a tile list of fewer than 2^30 entries (MXQ_ERR_SHAPE);
  * M == 0 or N == 0 is a no-op.
  */

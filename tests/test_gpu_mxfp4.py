@@ -175,6 +175,31 @@ def test_product(case, fmt, dtype):
     check(*operands(M, N, K, len(ends), fmt, M + N + K), ends, fmt, dtype)
 
 
+# enough tiles for 256 rows each, the groups' last ones of every height; K of one slot and less, odd halves
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("fmt", FMTS, ids=["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("M,N,K,ends", [
+    (4200, 4096, 128, [4200]),
+    (4200, 4096, 256, [1030, 1300, 4190]),
+    (4300, 4104, 384, [300, 300, 1000, 4300]),
+    (4170, 4360, 640, [60, 130, 4100, 4170]),
+    (4400, 4096, 1024, [2000, 4400]),
+], ids=lambda v: str(v) if isinstance(v, int) else "")
+def test_product_many_rows(M, N, K, ends, fmt, dtype):
+    check(*operands(M, N, K, len(ends), fmt, M + N + K), ends, fmt, dtype)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_product_random_shapes(seed):
+    r = np.random.default_rng(seed)
+    G = int(r.choice([1, 2, 3, 7, 16, 40]))
+    M, N, K = int(np.exp(r.uniform(0, np.log(900)))), 8 * int(r.integers(1, 90)), 128 * int(r.integers(1, 13))
+    ends = np.sort(r.integers(0, M + 4, G)).tolist()
+    fmt, dtype = int(r.choice(FMTS)), [torch.bfloat16, torch.float32][int(r.integers(0, 2))]
+    print(M, N, K, ends, fmt, dtype, flush=True)
+    check(*operands(M, N, K, G, fmt, seed), ends, fmt, dtype)
+
+
 @pytest.mark.parametrize("fmt", FMTS, ids=["mxfp8", "mxfp4"])
 @pytest.mark.parametrize("M", [3, 300])
 def test_every_k_position_and_scale_block(M, fmt):
