@@ -17,7 +17,8 @@
 //
 // Both are HBM bound (a few operations a value): the row is read once and held in
 // registers between its reduction and its use, LANES threads a row with C chunks
-// of 8 values each.  The sum of a row is one fp32 tree in a fixed order, so
+// of 8 values each.  65536 x 5120 bf16 with every output: 507 us, 5.97 TB/s; backward of
+// 16640 x 5120 with dh: 119 us, 5.7 TB/s.  The sum of a row is one fp32 tree in a fixed order, so
 // results are reproducible.
 #include "device_common.hpp"
 #include "internal.hpp"
@@ -73,8 +74,8 @@ void add_rmsnorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __res
         for (int c = 0; c < C; ++c) {
             const int i = lane + c * LANES;
             if (i < K8) {
-                xr[c] = T::load8_nt(x + at, i);
-                if (r) rr[c] = T::load8_nt(r + at, i);
+                xr[c] = T::load8(x + at, i);
+                if (r) rr[c] = T::load8(r + at, i);
             }
         }
         float ss = 0.0f;
@@ -122,9 +123,9 @@ void add_rmsnorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __res
 }
 
 // Backward.  Each workgroup walks over rows and keeps its part of dw in fp32
-// registers; the parts (one row of `part` for each LANES threads) are summed by
+// registers; the parts (one row of `part` for each workgroup) are summed by
 // dweight_kernel in a fixed order.
-template <class T, int LANES, int C>
+template <class T, int LANES, int C, bool NT>
 __global__ __launch_bounds__(LANES < 256 ? 256 : LANES)
 void add_rmsnorm_bwd_kernel(const uint8_t* __restrict__ h, const uint8_t* __restrict__ w,
                             const float* __restrict__ rstd, const uint8_t* dy, const uint8_t* dh, int64_t M, int K,
@@ -153,9 +154,9 @@ void add_rmsnorm_bwd_kernel(const uint8_t* __restrict__ h, const uint8_t* __rest
         for (int c = 0; c < C; ++c) {
             const int i = lane + c * LANES;
             if (i < K8) {
-                hr[c] = T::load8_nt(h + at, i);
-                gr[c] = T::load8_nt(dy + at, i);
-                if (dh) dr[c] = T::load8_nt(dh + at, i);
+                hr[c] = NT ? T::load8_nt(h + at, i) : T::load8(h + at, i);
+                gr[c] = NT ? T::load8_nt(dy + at, i) : T::load8(dy + at, i);
+                if (dh) dr[c] = NT ? T::load8_nt(dh + at, i) : T::load8(dh + at, i);
             }
         }
         const float rs = rstd[m];
@@ -197,7 +198,24 @@ void add_rmsnorm_bwd_kernel(const uint8_t* __restrict__ h, const uint8_t* __rest
             }
         }
     }
-    float* dst = part + ((int64_t)blockIdx.x * kRows + sub) * K;
+    if constexpr (kRows > 1) {                                // the waves' parts become the workgroup's, in wave order
+        __shared__ float join[kRows - 1][LANES * C * 8];
+        if (sub > 0) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) join[sub - 1][(c * 8 + e) * LANES + lane] = acc[c][e];
+        }
+        __syncthreads();
+        if (sub > 0) return;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int r = 0; r < kRows - 1; ++r) acc[c][e] += join[r][(c * 8 + e) * LANES + lane];
+    }
+    float* dst = part + (int64_t)blockIdx.x * K;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = lane + c * LANES;
@@ -243,7 +261,14 @@ void dweight_kernel(const float* __restrict__ part, int rows, int K, float* __re
 }
 
 constexpr int kNormMaxGrid = 1 << 22;
-constexpr int kBwdParts = 1024;       // partial rows of dw at most
+// Workgroups of the backward pass at most, and so parts of dw: two a CU, which are
+// resident together (16640 x 5120: 256 / 512 / 768 / 1024 took 147 / 119 / 129 / 134 us;
+// 16640 x 1024: 512 / 1024 / 2048 25.4 / 27.5 / 31.0).
+constexpr int kBwdParts = 512;
+// Inputs that do not fit the 256 MB last-level cache are read as streams (16640 x 5120:
+// 119 us, plain loads 128); smaller ones may be in it, where their writer left them
+// (4096 x 8192: 47.6 us, as streams 54).  The forward pass measured no such gain.
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
 
 // Threads a row and chunks a thread for K values: a wave while 4 chunks hold the
 // row (no barrier), then 256 threads.
@@ -265,8 +290,7 @@ int64_t bwd_grid(int64_t M, int K)
 {
     const int rows = rows_per_group(K);
     const int64_t groups = (M + rows - 1) / rows;
-    const int64_t cap = kBwdParts / rows;
-    return groups < cap ? groups : cap;
+    return groups < kBwdParts ? groups : kBwdParts;
 }
 
 }  // namespace
@@ -298,7 +322,7 @@ hipError_t launch_add_rmsnorm(const void* x, const void* r, const void* w, bool 
 
 size_t add_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K)
 {
-    return (size_t)bwd_grid(M, (int)K) * (size_t)rows_per_group((int)K) * (size_t)K * 4u;
+    return (size_t)bwd_grid(M, (int)K) * (size_t)K * 4u;
 }
 
 hipError_t launch_add_rmsnorm_bwd(const void* h, const void* w, const float* rstd, const void* dy, const void* dh,
@@ -307,24 +331,25 @@ hipError_t launch_add_rmsnorm_bwd(const void* h, const void* w, const float* rst
 {
     const int64_t grid = bwd_grid(M, (int)K);
     float* part = (float*)workspace;
+    const bool nt = M * K * (f32 ? 4 : 2) * (dh ? 3 : 2) > kCacheBytes;
     if (grid > 0) {
-#define MXQ_CALL(L, C)                                                                                              \
-    do {                                                                                                            \
-        const dim3 block((L) < 256 ? 256 : (L));                                                                    \
-        if (f32)                                                                                                    \
-            hipLaunchKernelGGL((add_rmsnorm_bwd_kernel<F32, L, C>), dim3((unsigned)grid), block, 0, stream,         \
-                               (const uint8_t*)h, (const uint8_t*)w, rstd, (const uint8_t*)dy, (const uint8_t*)dh,  \
-                               M, (int)K, (uint8_t*)dx, part);                                                      \
-        else                                                                                                        \
-            hipLaunchKernelGGL((add_rmsnorm_bwd_kernel<Bf16, L, C>), dim3((unsigned)grid), block, 0, stream,        \
-                               (const uint8_t*)h, (const uint8_t*)w, rstd, (const uint8_t*)dy, (const uint8_t*)dh,  \
-                               M, (int)K, (uint8_t*)dx, part);                                                      \
+#define MXQ_LAUNCH(T, L, C, NT)                                                                                     \
+    hipLaunchKernelGGL((add_rmsnorm_bwd_kernel<T, L, C, NT>), dim3((unsigned)grid), dim3((L) < 256 ? 256 : (L)), 0, \
+                       stream, (const uint8_t*)h, (const uint8_t*)w, rstd, (const uint8_t*)dy, (const uint8_t*)dh,  \
+                       M, (int)K, (uint8_t*)dx, part)
+#define MXQ_CALL(L, C)                                   \
+    do {                                                 \
+        if (f32 && nt) MXQ_LAUNCH(F32, L, C, true);      \
+        else if (f32) MXQ_LAUNCH(F32, L, C, false);      \
+        else if (nt) MXQ_LAUNCH(Bf16, L, C, true);       \
+        else MXQ_LAUNCH(Bf16, L, C, false);              \
     } while (0)
         MXQ_NORM_SHAPE(K, MXQ_CALL);
 #undef MXQ_CALL
+#undef MXQ_LAUNCH
     }
     hipLaunchKernelGGL(dweight_kernel, dim3((unsigned)((K / 4 + 7) / 8)), dim3(256), 0, stream, part,
-                       (int)(grid * rows_per_group((int)K)), (int)K, dw);
+                       (int)grid, (int)K, dw);
     return hipGetLastError();
 }
 

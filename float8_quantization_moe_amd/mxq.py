@@ -518,13 +518,19 @@ def mxq_add_rmsnorm_bwd(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tenso
 
 def add_rmsnorm(x: torch.Tensor, residual, weight: torch.Tensor, eps: float, stream=None):
     """(h, y, q, s, rstd) of mxq_add_rmsnorm; h is x itself when there is no residual."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D (M, K)")
     M, K = x.shape
+    code, dt = _float_code(x, "x"), x.dtype
+    px, pr, pw = _dev(x, "x"), _opt(residual, "residual", dt, M * K), _dev(weight, "weight", dt, K)
+    # (outputs made here need no checks: a token's norm is host time)
     h = x if residual is None else torch.empty_like(x)
     y = torch.empty_like(x)
-    q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    s = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
-    mxq_add_rmsnorm(x, residual, weight, eps, None if residual is None else h, y, q, s, rstd, stream)
+    q = torch.empty_like(x, dtype=torch.uint8)
+    s = x.new_empty((M, K // 32), dtype=torch.uint8)
+    rstd = x.new_empty(M, dtype=torch.float32)
+    _check(lib().mxq_add_rmsnorm(px, pr, pw, code, M, K, eps, 0 if residual is None else h.data_ptr(), y.data_ptr(),
+                                 q.data_ptr(), s.data_ptr(), rstd.data_ptr(), _stream(stream)), "mxq_add_rmsnorm")
     return h, y, q, s, rstd
 
 

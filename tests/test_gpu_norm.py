@@ -6,9 +6,9 @@ a lane and 10 across lanes and waves, so the sum is good to 74 u, rstd to half o
 and its own two roundings, and a product of three factors to 2 u more: below 2^-18
 relative for an fp32 output, and half a step of bf16 more for a bf16 output.  dx
 subtracts two terms, so its bound is relative to the terms' sizes; a dot product of
-K terms in the same tree is good to 80 u of the sum of magnitudes.  dweight adds at
-most M / 256 rows in a register, then 1024 parts in 32 slices: with M <= 2000
-(8 + 64 + 3) u of the sum of magnitudes."""
+K terms in the same tree is good to 80 u of the sum of magnitudes.  dweight adds a
+few rows in a register, the waves of a workgroup, then up to 1024 parts in 32 slices
+and the slices: with M <= 2000 no more than (8 + 64 + 3) u of the sum of magnitudes."""
 import numpy as np
 import pytest
 import torch
