@@ -585,8 +585,8 @@ def route_topk(logits: torch.Tensor, topk: int, bias=None, score: str = "softmax
                stream=None):
     """(expert_ids, weights), each (M, topk), of mxq_route_topk."""
     M = logits.shape[0]
-    ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty((M, topk), dtype=torch.int32)
+    weights = logits.new_empty((M, topk), dtype=torch.float32)
     flags = (MXQ_ROUTE_RENORM if renormalize else 0) | (MXQ_ROUTE_GROUP_TOP2 if group_top2 else 0)
     mxq_route_topk(logits, bias, SCORES[score], n_groups, topk_groups, flags, scale, ids, weights, stream)
     return ids, weights
@@ -626,14 +626,14 @@ def mxq_dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, y: torch.Tensor, stre
 
 def quantize_mxfp4(x: torch.Tensor, rule: int = MXQ_SCALE_FLOOR, stream=None):
     M, K = x.shape
-    q = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-    s = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    q = x.new_empty((M, K // 2), dtype=torch.uint8)
+    s = x.new_empty((M, K // 32), dtype=torch.uint8)
     mxq_quantize_mxfp4(x, rule, q, s, stream)
     return q, s
 
 
 def dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, stream=None) -> torch.Tensor:
-    y = torch.empty((q.shape[0], 2 * q.shape[1]), dtype=torch.bfloat16, device=q.device)
+    y = q.new_empty((q.shape[0], 2 * q.shape[1]), dtype=torch.bfloat16)
     mxq_dequantize_mxfp4(q, s, y, stream)
     return y
 
