@@ -5,8 +5,8 @@
 // Persistent workgroups (one a CU, 4 waves in 2 x 2) walk over output tiles of 256
 // columns x 256 rows (128 where that leaves CUs idle).  K advances 256 values a slot through a 2-slot LDS ring of 32 KB
 // of W codes, 32 KB of X codes (of E4M3 tokens, with twice the bytes and MFMAs of twice
-// the time, half a slot's) and 16 bytes of scales a row, filled by
-// buffer-load-to-LDS in whole 128-byte lines.  A slot is four MFMA steps of 64 k; a
+// the time, half a slot's) filled by buffer-load-to-LDS in whole 128-byte lines.  Scales
+// come 16 bytes a row for two slots: every row is a line of its own, 64 of them a load.  A slot is four MFMA steps of 64 k; a
 // step's operands are read from LDS during the step before it.  The one barrier that
 // a slot needs comes before its last step, when all its operands are in registers:
 // the loads of the slot after next go into its place from there on, spread between
@@ -20,7 +20,8 @@
 // Tile list: row tiles never straddle a group.  Group by group, inside a group in
 // blocks of kColBlock column tiles with the block's row tiles consecutive, so that
 // neighbours in the list share W and X tiles; each of the 8 XCDs (workgroup index
-// mod 8) walks one contiguous stretch, its CUs side by side.  Every workgroup finds
+// mod 8) walks one contiguous stretch, its CUs side by side, the last round's tiles in
+// smaller parts where that fills CUs.  Every workgroup finds
 // its own tiles from the group offsets (a scan in LDS), so no launch comes before.
 //
 // MFMA operand A is W (output columns), B is X (token rows).  In a 64-k step, lane
@@ -45,9 +46,9 @@ constexpr int kMaxEntries = 1024;                        // tiles of one workgro
 constexpr uint32_t kLdsBytes = kEntryBase + kMaxEntries * 16;
 static_assert(kLdsBytes <= 160 * 1024, "LDS of a CU");
 // Tiles of 128 rows while there is less than one of 256 rows for each CU: 777 ragged
-// rows x 1736 x 1408 over 16 groups (126 tiles of 256 rows) 16.2 / 13.4 us (E4M3 /
-// E2M1) against 23.6 / 17.8; 2048 x 8192 x 5120 over 4 groups (384) 114 / 87 against
-// 119 / 78; one group of 16384 rows 632 / 486 against 538 / 379.
+// rows x 1736 x 1408 over 16 groups (126 tiles of 256 rows) 14.4 / 12.2 us (E4M3 /
+// E2M1) against 17.7 / 14.5; the other way round above that: one group of 16384 rows
+// 632 / 486 against 538 / 379.
 constexpr int kManyTiles = 1;
 // Column tiles of a block of the tile order; one group of 16384 x 8192 x 5120, E4M3: 2
 // 521 us, 3 533, 4 580, 8 575 (1 measured slower before); 16 groups 625 / 642 / 643 / 691.
@@ -155,12 +156,17 @@ __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_
 
     const int NC = (a.N + kCols - 1) / kCols;
     const int V = first_sh[a.G] * NC;
-    const int q = (V + kXcds - 1) / kXcds;
-    const int x = (int)blockIdx.x % kXcds, stride = (int)gridDim.x / kXcds;
-    const int lo = x * q + (int)blockIdx.x / kXcds, hi = (x + 1) * q < V ? (x + 1) * q : V;
-    const int count = lo < hi ? (hi - lo + stride - 1) / stride : 0;
+    const int x = (int)blockIdx.x % kXcds, cu = (int)blockIdx.x / kXcds, cus = (int)gridDim.x / kXcds;
+    const int lo = (int)((int64_t)V * x / kXcds), n = (int)((int64_t)V * (x + 1) / kXcds) - lo;
+    // The tiles left after the last full round are cut in row parts of 64 or more while
+    // that gives no more than one for each CU (2048 x 8192 x 5120 over 4 groups, 12 tiles
+    // for 8 CUs: 90 / 66 us E4M3 / E2M1 against 114 / 76; 8192 x 4096 x 2048 over 32: 92 /
+    // 68 against 102 / 74).
+    const int full = n / cus, over = n - full * cus;
+    const int parts = 4 * over <= cus && R == 256 ? 4 : 2 * over <= cus ? 2 : 1;
+    const int count = full + (cu < over * parts);
     for (int j = t; j < count && j < kMaxEntries; j += kThreads) {
-        const int L = lo + j * stride;
+        const int L = lo + j * cus + (j < full ? cu : cu / parts);
         int p = 0, r = a.G - 1;                          // the last group whose tiles start at or before L
         while (p < r) {
             const int mid = (p + r + 1) >> 1;
@@ -172,10 +178,12 @@ __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_
         const int cb = local / (rt * kColBlock);
         const int rem = local - cb * rt * kColBlock;
         const int width = NC - cb * kColBlock < kColBlock ? NC - cb * kColBlock : kColBlock;
+        const int height = j < full ? R : R / parts, part = j < full ? 0 : cu % parts;
         Tile tl;
         tl.g = p;
-        tl.r0 = (p ? end_sh[p - 1] : 0) + rem / width * R;
-        tl.r1 = tl.r0 + R < end_sh[p] ? tl.r0 + R : end_sh[p];
+        tl.r0 = (p ? end_sh[p - 1] : 0) + rem / width * R + part * height;
+        tl.r1 = tl.r0 + height < end_sh[p] ? tl.r0 + height : end_sh[p];
+        if (tl.r1 < tl.r0) tl.r1 = tl.r0;                // a part past the group's rows
         tl.c = cb * kColBlock + rem % width;
         list[j] = tl;
     }
@@ -197,6 +205,8 @@ struct Loader {
     v4i w, ws, xs;                                       // resources that start at the next slot
     v4i x, xb;                                           // X8: at its first half's and the running slot's second half
     int entry, left;                                     // the tile's place in the list; its slots from the next one on
+    bool new_chunk;                                      // the next slot is the first of a chunk of scales
+    uint32_t chunk;                                      // the place in LDS of the next chunk
     int xentry, xleft;                                   // X8: the same of the X codes
     uint32_t off_w[8], off_x[8], off_ws, off_xs;         // lane offsets of the wave's loads, 8 rows each
     uint32_t lds_data, lds_scale;                        // LDS addresses of the wave's part of ring slot 0
@@ -245,6 +255,7 @@ struct Loader {
         const uint32_t half = (uint32_t)a.K / 2u, kb = (uint32_t)a.K / 32u;
         const Place p = place_of(a, list, entry, count);
         left = nslots;
+        new_chunk = true;
         w = resource(a.wq + p.wrow * half, p.nw * half);
         ws = resource(a.ws + p.wrow * kb, p.nw * kb);
         xs = resource(a.xs + (int64_t)p.r0 * a.ldxs, p.nx ? (p.nx - 1u) * a.ldxs + kb : 0u);
@@ -286,6 +297,7 @@ struct Loader {
             set_tile(a, list, count, nslots);
         } else {
             --left;
+            new_chunk = !new_chunk;
             w = stepped(w, 128);
             ws = stepped(ws, 8);
             xs = stepped(xs, 8);
@@ -301,20 +313,21 @@ struct Loader {
         for (int i = 0; i < 8; ++i) off_x[i] ^= (i & 1) ? upper ^ 0x80000000u : upper;
     }
 
-    // Load I of the slot into ring slot b: 0, 1 the scales, then W and (E2M1) X codes.
-    static constexpr int kLoads = X8 ? 10 : 18;
+    // Scales travel in chunks of 16 bytes a row, two slots' worth (one group of 16384 x
+    // 8192 x 5120, E2M1: 351 us; 16 bytes for every slot, half of them unused, 374).
+    __device__ __forceinline__ void issue_scales()
+    {
+        load_to_lds(ws, lds_scale + chunk * 2u * kScaleOperand, off_ws);
+        load_to_lds(xs, lds_scale + chunk * 2u * kScaleOperand + kScaleOperand, off_xs);
+        chunk ^= 1u;
+    }
+    // Load I of the slot into ring slot b: W and (E2M1) X codes in turn.
     template <int I>
     __device__ __forceinline__ void issue(uint32_t b)
     {
-        if constexpr (I == 0) {
-            load_to_lds(ws, lds_scale + b * 2u * kScaleOperand, off_ws);
-        } else if constexpr (I == 1) {
-            load_to_lds(xs, lds_scale + b * 2u * kScaleOperand + kScaleOperand, off_xs);
-        } else {
-            constexpr int i = X8 ? I - 2 : (I - 2) / 2;
-            if constexpr (X8 || I % 2 == 0) load_to_lds(w, lds_data + b * kSlotBytes + 1024u * i, off_w[i]);
-            else load_to_lds(x, lds_data + b * kSlotBytes + kOperandBytes + 1024u * i, off_x[i]);
-        }
+        constexpr int i = X8 ? I : I / 2;
+        if constexpr (X8 || I % 2 == 0) load_to_lds(w, lds_data + b * kSlotBytes + 1024u * i, off_w[i]);
+        else load_to_lds(x, lds_data + b * kSlotBytes + kOperandBytes + 1024u * i, off_x[i]);
     }
     template <int I, int END>
     __device__ __forceinline__ void issue_some(uint32_t b)
@@ -366,16 +379,22 @@ __device__ __forceinline__ void read_step(Operands<X8, TM>& f, const uint8_t* ld
     }
 }
 
-// The scale words of ring slot b, shifted so that bytes 0 and 2 are the lane's blocks.
-template <int TM>
-__device__ __forceinline__ void read_scales(Scales<TM>& s, const uint8_t* lds, uint32_t b, const Lane& l)
+// A slot's scale words: place `at` in LDS is its chunk's, 8 bytes on its second slot's.
+__device__ __forceinline__ uint32_t next_scales(uint32_t at, bool new_tile)
 {
-    const uint8_t* p = lds + kScaleBase + b * 2u * kScaleOperand;
+    constexpr uint32_t kChunk = 2u * kScaleOperand;
+    return new_tile || (at & 8u) ? (at & kChunk) ^ kChunk : at | 8u;
+}
+template <int TM>
+__device__ __forceinline__ void read_scales(Scales<TM>& s, const uint8_t* lds, uint32_t at, const Lane& l)
+{
+    const uint8_t* p = lds + kScaleBase + at;
 #pragma unroll
     for (int i = 0; i < 4; ++i) s.w[i] = *(const uint2*)(p + (128u * l.wn + 32u * i + l.row) * 16u);
 #pragma unroll
     for (int i = 0; i < TM; ++i) s.x[i] = *(const uint2*)(p + kScaleOperand + (32u * TM * l.wm + 32u * i + l.row) * 16u);
 }
+// Shifted so that bytes 0 and 2 of a word are the lane's blocks.
 template <int TM>
 __device__ __forceinline__ void shift_scales(Scales<TM>& s, const Lane& l)
 {
@@ -419,14 +438,15 @@ __device__ __forceinline__ void mfmas(v16f (&acc)[4][TM], const Operands<X8, TM>
     }
 }
 
-// How a slot's loads are spread: the first kLoadsA in the last step of the slot two
-// before it, up to kLoadsB in the first step of the slot before it, the rest in the
-// second (E2M1 only).  All 18 of E2M1 at once fill the memory pipe's queue and hold up
-// the MFMAs behind them: 16640 x 8192 x 5120 over 16 groups 481 us against 451 in
-// thirds (9 + 9: 450; 12 + 6: 466).  X8: the halves' loads go out in steps 1 and 3.
+// How a slot's loads of codes are spread: the first kLoadsA in the last step of the slot
+// two before it, up to kLoadsB in the first step of the slot before it, the rest in the
+// second (E2M1 only).  All of E2M1's at once fill the memory pipe's queue and hold up the
+// MFMAs behind them: with the scales in every slot, 16640 x 8192 x 5120 over 16 groups took
+// 481 us against 451 in thirds.  The thirds 6 + 6 + 4 against 5 + 5 + 6: 434 against 438;
+// one group of 16384 rows 351 against 359.  X8: the halves' loads go out in steps 1 and 3.
 template <bool X8>
 struct Spread {
-    static constexpr int kLoadsA = X8 ? 3 : 6, kLoadsB = X8 ? 10 : 12, kLoadsC = X8 ? 10 : 18;
+    static constexpr int kLoadsA = X8 ? 3 : 6, kLoadsB = X8 ? 8 : 12, kLoadsC = X8 ? 8 : 16;
 };
 
 // Steps 0 and 1 of the slot in ring slot b, with the second part of the loads of the
@@ -439,6 +459,7 @@ __device__ __forceinline__ void steps01(v16f (&acc)[4][TM], Operands<X8, TM> (&f
                                         const uint8_t* lds, const Lane& l, uint32_t b)
 {
     using S = Spread<X8>;
+    if (ld.new_chunk) ld.issue_scales();
     shift_scales<TM>(s, l);
     read_step<X8, TM, 1>(f[1], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
@@ -457,7 +478,7 @@ __device__ __forceinline__ void steps01(v16f (&acc)[4][TM], Operands<X8, TM> (&f
 // next slot's, unless this is the tile's LAST.
 template <bool X8, int TM, bool LAST>
 __device__ __forceinline__ void steps23(v16f (&acc)[4][TM], Operands<X8, TM> (&f)[2], Scales<TM>& s, Loader<X8>& ld,
-                                        const uint8_t* lds, const Lane& l, uint32_t b)
+                                        const uint8_t* lds, const Lane& l, uint32_t b, uint32_t scales)
 {
     read_step<X8, TM, 3>(f[1], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
@@ -466,7 +487,7 @@ __device__ __forceinline__ void steps23(v16f (&acc)[4][TM], Operands<X8, TM> (&f
     const Scales<TM> now = s;
     if constexpr (!LAST) {
         read_step<X8, TM, 0>(f[0], lds, b ^ 1u, l);
-        read_scales<TM>(s, lds, b ^ 1u, l);
+        read_scales<TM>(s, lds, scales, l);
         __builtin_amdgcn_sched_barrier(0);
     }
     mfmas<X8, TM, 3, false, 0, Spread<X8>::kLoadsA, 1, 0, X8 ? 8 : 0>(acc, f[1], now, ld, b);
@@ -485,40 +506,74 @@ __device__ __forceinline__ void pin(v16f (&acc)[4][TM])
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Four 16-byte pieces a lane, piece s of lane (r, h) at byte 32 s + 16 h of row r of a
+// 32-row, 128-byte block, change lanes so that piece s lies in row 16 (s % 2) +
+// 8 (s / 2) + r % 8 at byte 64 (r / 8 % 2) + 32 (r / 16) + 16 h: a store then covers
+// whole lines.  (Pieces 0 and 1, 2 and 3 swap between rows of 16 lanes, then 0 and 2,
+// 1 and 3 between halves of 16.)
+__device__ __forceinline__ void join_lines(v4i (&p)[4])
+{
+    constexpr int kRor8 = 0x128;                         // lane ^ 8, within 16 lanes
+#pragma unroll
+    for (int s = 0; s < 4; s += 2)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const auto v = __builtin_amdgcn_permlane16_swap((uint32_t)p[s][k], (uint32_t)p[s + 1][k], false, false);
+            p[s][k] = (int)v[0];
+            p[s + 1][k] = (int)v[1];
+        }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int lo = p[s][k], hi = p[s + 2][k];
+            p[s][k] = __builtin_amdgcn_update_dpp(lo, hi, kRor8, 0xf, 0xc, false);
+            p[s + 2][k] = __builtin_amdgcn_update_dpp(hi, lo, kRor8, 0xf, 0x3, false);
+        }
+}
+
 // Stores: lane (r, h) holds, of row r of each 32 x 32 part, columns 8 q + 4 h .. + 3
 // for q = 0 .. 3.  bf16: the halves of the wave exchange every other 4 columns, so
-// that a lane stores 8 consecutive ones (16 bytes).
+// that a lane has 8 consecutive ones (16 bytes).  One group of 16384 x 8192 x 5120,
+// E2M1 (bf16 out): 32-byte stretches 357 us, 64-byte ones 338, whole lines 337.
 template <int TM, bool F32OUT>
 __device__ __forceinline__ void store_tile(const v16f (&acc)[4][TM], const MmArgs& a, const Tile& t, const Lane& l)
 {
+    constexpr int kSize = F32OUT ? 4 : 2, kParts = F32OUT ? 1 : 2;
+    const int n_lane = (int)(64u * (l.row >> 3 & 1u) + 32u * (l.row >> 4) + 16u * l.h) / kSize;
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-        const int m = t.r0 + (int)(32u * TM * l.wm + 32u * j + l.row);
-        const bool row_ok = m < t.r1;
-        const int64_t at = (int64_t)m * a.N;
+        const int m = t.r0 + (int)(32u * TM * l.wm + 32u * j + (l.row & 7u));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __builtin_amdgcn_sched_barrier(0);           // (one part at a time in VGPRs)
-            const int n0 = t.c * kCols + (int)(128u * l.wn) + 32 * i;
-            const v16f& v = acc[i][j];
+        for (int i = 0; i < 4; i += kParts) {
+            __builtin_amdgcn_sched_barrier(0);           // (one block at a time in VGPRs)
+            v4i p[4];
             if constexpr (F32OUT) {
+                const v16f& v = acc[i][j];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = n0 + 8 * q + 4 * (int)l.h;
-                    if (row_ok && n < a.N)
-                        *(float4*)((float*)a.y + at + n) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                }
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) p[s][k] = __float_as_int(v[4 * s + k]);
             } else {
 #pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    const uint32_t e0 = f32_pair_to_bf16(v[4 * q], v[4 * q + 1]), e1 = f32_pair_to_bf16(v[4 * q + 2], v[4 * q + 3]);
-                    const uint32_t o0 = f32_pair_to_bf16(v[4 * q + 4], v[4 * q + 5]), o1 = f32_pair_to_bf16(v[4 * q + 6], v[4 * q + 7]);
-                    const auto s0 = __builtin_amdgcn_permlane32_swap(e0, o0, false, false);
-                    const auto s1 = __builtin_amdgcn_permlane32_swap(e1, o1, false, false);
-                    const int n = n0 + 8 * q + 8 * (int)l.h;
-                    if (row_ok && n < a.N)
-                        *(uint4*)((uint16_t*)a.y + at + n) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+                for (int s = 0; s < 4; ++s) {
+                    const v16f& v = acc[i + s / 2][j];
+                    const int q = 8 * (s % 2);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const auto w = __builtin_amdgcn_permlane32_swap(f32_pair_to_bf16(v[q + 2 * k], v[q + 2 * k + 1]),
+                                                                        f32_pair_to_bf16(v[q + 2 * k + 4], v[q + 2 * k + 5]), false, false);
+                        p[s][k] = (int)w[0];
+                        p[s][k + 2] = (int)w[1];
+                    }
                 }
+            }
+            join_lines(p);
+            const int n = t.c * kCols + (int)(128u * l.wn) + 32 * i + n_lane;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int row = m + 16 * (s % 2) + 8 * (s / 2);
+                if (row < t.r1 && n < a.N) *(v4i*)((uint8_t*)a.y + ((int64_t)row * a.N + n) * kSize) = p[s];
             }
         }
     }
@@ -528,18 +583,20 @@ __device__ __forceinline__ void store_tile(const v16f (&acc)[4][TM], const MmArg
 // ring slot b; the loads are part way into the slot after it.
 template <bool X8, int TM, bool F32OUT>
 __device__ __forceinline__ void tile_product(Loader<X8>& ld, const MmArgs& a, const uint8_t* lds, const Tile* list, int count,
-                                             const Tile& t, const Lane& l, int nslots, uint32_t& b)
+                                             const Tile& t, const Lane& l, int nslots, uint32_t& b, uint32_t& scales)
 {
     v16f acc[4][TM];
     Operands<X8, TM> f[2];
     Scales<TM> s;
-    read_scales<TM>(s, lds, b, l);
+    read_scales<TM>(s, lds, scales, l);
     read_step<X8, TM, 0>(f[0], lds, b, l);
     steps01<X8, TM, true>(acc, f, s, ld, lds, l, b);
     pin<TM>(acc);
     ld.advance(a, list, count, nslots);
     for (int i = 1; i < nslots; ++i) {
-        steps23<X8, TM, false>(acc, f, s, ld, lds, l, b);
+        scales = next_scales(scales, false);
+        steps23<X8, TM, false>(acc, f, s, ld, lds, l, b, scales);
+        pin<TM>(acc);
         b ^= 1u;
         steps01<X8, TM, false>(acc, f, s, ld, lds, l, b);
         pin<TM>(acc);
@@ -551,9 +608,10 @@ __device__ __forceinline__ void tile_product(Loader<X8>& ld, const MmArgs& a, co
 #pragma unroll
         for (int j = 0; j < TM; ++j) s.x[j].y = 0;
     }
-    steps23<X8, TM, true>(acc, f, s, ld, lds, l, b);
+    steps23<X8, TM, true>(acc, f, s, ld, lds, l, b, scales);
     pin<TM>(acc);
     b ^= 1u;
+    scales = next_scales(scales, true);
     store_tile<TM, F32OUT>(acc, a, t, l);
 }
 
@@ -574,6 +632,7 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
         rows_end = uniform(rows_end);
     }
     __syncthreads();                                     // the list is complete, the scan's arrays are free
+    if (count > 0 && uniform(list[count - 1].r0) == uniform(list[count - 1].r1)) --count;
 
     if (count > 0) {
         const Lane l = {(uint32_t)(lane & 31), (uint32_t)(lane >> 5), (uint32_t)((lane >> 1) & 7),
@@ -583,16 +642,18 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
         Loader<X8> ld;
         ld.set_lanes(a, lds, wave, lane);
         ld.entry = ld.xentry = 0;
+        ld.chunk = 0;
         ld.set_tile(a, list, count, nslots);
         if constexpr (X8) ld.set_x_tile(a, list, count, nslots);
         else if (a.K < kSlotK) ld.toggle_half();
+        ld.issue_scales();
         ld.template issue_some<0, S::kLoadsC>(0);
         if constexpr (X8) ld.template issue_x<0, 0, 8>();
         ld.advance(a, list, count, nslots);
         if constexpr (X8) ld.template issue_x<1, 0, 8>();
         ld.template issue_some<0, S::kLoadsA>(1);
         slot_barrier<0>();
-        uint32_t b = 0;
+        uint32_t b = 0, scales = 0;
         for (int e = 0; e < count; ++e) {
             Tile t = list[e];
             t.g = uniform(t.g);
@@ -601,9 +662,9 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
             t.c = uniform(t.c);
             // a group's last tile runs at the smallest of three heights that holds its rows
             const int rows = t.r1 - t.r0;
-            if (rows > 128) tile_product<X8, 4, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
-            else if (rows > 64) tile_product<X8, 2, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
-            else tile_product<X8, 1, F32OUT>(ld, a, lds, list, count, t, l, nslots, b);
+            if (rows > 128) tile_product<X8, 4, F32OUT>(ld, a, lds, list, count, t, l, nslots, b, scales);
+            else if (rows > 64) tile_product<X8, 2, F32OUT>(ld, a, lds, list, count, t, l, nslots, b, scales);
+            else tile_product<X8, 1, F32OUT>(ld, a, lds, list, count, t, l, nslots, b, scales);
         }
         slot_barrier<0>();                               // the loads past the end land before the LDS goes away
     }
@@ -632,7 +693,8 @@ hipError_t launch_mxfp4_mm_tile(const void* xq, const void* xs, bool x8, int64_t
     // One workgroup a CU, fewer when there are not that many tiles, more (which then run one
     // after the other) when a workgroup's list would not hold its tiles.
     const int64_t most = tiles(rows);
-    int64_t grid = most < cus ? most : cus;
+    const int64_t parts = most * (rows / 64);
+    int64_t grid = parts < cus ? parts : cus;
     const int64_t least = (most + kMaxEntries - kXcds - 1) / (kMaxEntries - kXcds);
     grid = grid < least ? least : grid;
     grid = (grid + kXcds - 1) / kXcds * kXcds;
