@@ -3,14 +3,13 @@
 // calls with few rows).
 //
 // Persistent workgroups (one a CU, 4 waves in 2 x 2) walk over output tiles of 256
-// columns x 256 rows (128 where that leaves CUs idle).  K advances 256 values a slot through a 2-slot LDS ring of 32 KB
-// of W codes, 32 KB of X codes (of E4M3 tokens, with twice the bytes and MFMAs of twice
-// the time, half a slot's) filled by buffer-load-to-LDS in whole 128-byte lines.  Scales
-// come 16 bytes a row for two slots: every row is a line of its own, 64 of them a load.  A slot is four MFMA steps of 64 k; a
-// step's operands are read from LDS during the step before it.  The one barrier that
-// a slot needs comes before its last step, when all its operands are in registers:
-// the loads of the slot after next go into its place from there on, spread between
-// the MFMAs of three steps.  (E4M3: a second barrier half way, for the X codes.)
+// columns x 256 rows (128 where that leaves CUs idle).  K advances 256 values a slot
+// through a 2-slot LDS ring of 32 KB of W codes and 32 KB of X codes (of E4M3 tokens, with
+// twice the bytes and MFMAs of twice the time, half a slot's), filled by
+// buffer-load-to-LDS in whole 128-byte lines.  Scales come 32 bytes a row for four slots.
+// A slot is four MFMA steps of 64 k; a step's operands are read from LDS during the step
+// before it.  With one wave a SIMD nothing issues while a load or an LDS read waits for
+// its pipe, so both are spread between the MFMAs, one or two after each (`mfmas`).
 //
 // The slots of successive tiles form one stream: the loads run ahead of the
 // products across the end of a tile, so the next tile's operands arrive while this
@@ -30,6 +29,8 @@
 #include "device_common.hpp"
 #include "internal.hpp"
 
+#include <type_traits>
+
 namespace mxq {
 
 namespace {
@@ -39,11 +40,10 @@ constexpr int kCols = 256;                               // columns of a tile
 constexpr int kSlotK = 256;
 constexpr uint32_t kOperandBytes = 32 * 1024;            // codes of one operand in one slot
 constexpr uint32_t kSlotBytes = 2 * kOperandBytes;
-constexpr uint32_t kScaleOperand = 256 * 16;             // scales of one operand in one slot
+constexpr uint32_t kScaleOperand = 256 * 32;             // scales of one operand for four slots
 constexpr uint32_t kScaleBase = 2 * kSlotBytes;
-constexpr uint32_t kEntryBase = kScaleBase + 2 * 2 * kScaleOperand;
-constexpr int kMaxEntries = 1024;                        // tiles of one workgroup
-constexpr uint32_t kLdsBytes = kEntryBase + kMaxEntries * 16;
+constexpr uint32_t kLdsBytes = kScaleBase + 2 * 2 * kScaleOperand;
+constexpr int kMaxEntries = 64;                          // tiles of one workgroup: one a lane
 static_assert(kLdsBytes <= 160 * 1024, "LDS of a CU");
 // Tiles of 128 rows while there is less than one of 256 rows for each CU: 777 ragged
 // rows x 1736 x 1408 over 16 groups (126 tiles of 256 rows) 14.4 / 12.2 us (E4M3 /
@@ -53,6 +53,11 @@ constexpr int kManyTiles = 1;
 // Column tiles of a block of the tile order; one group of 16384 x 8192 x 5120, E4M3: 2
 // 521 us, 3 533, 4 580, 8 575 (1 measured slower before); 16 groups 625 / 642 / 643 / 691.
 constexpr int kColBlock = 2;                             // column tiles of a block of the tile order
+// CUs by which the order moves on each round.  The short last tiles of equal groups come at
+// one place of every round, and would come to the same CUs; with a shift of 6, 16640 x 8192
+// x 5120 over 16 ragged groups, E4M3, 622 -> 590 us, 20000 x 4096 x 4096 over 24 320 -> 300
+// (E2M1 434 -> 434, 232 -> 225; shifts of 1, 2, 3, 10 within the noise of it).
+constexpr int kShift = 6;
 constexpr int kXcds = 8;
 constexpr int kMaxGroups = 4095;
 static_assert((2 * (kMaxGroups + 2) + kThreads) * 4 <= (int)kScaleBase, "the scan's arrays fit the ring");
@@ -64,6 +69,16 @@ typedef __attribute__((address_space(3))) uint8_t* LdsPtr;
 
 struct Tile {
     int g, r0, r1, c;                                    // group, rows [r0, r1), column tile c
+};
+
+// A workgroup's list: tile e in lane e of every wave.
+struct TileList {
+    Tile mine;
+    __device__ __forceinline__ Tile at(int e) const
+    {
+        return Tile{__builtin_amdgcn_readlane(mine.g, e), __builtin_amdgcn_readlane(mine.r0, e),
+                    __builtin_amdgcn_readlane(mine.r1, e), __builtin_amdgcn_readlane(mine.c, e)};
+    }
 };
 
 struct MmArgs {
@@ -122,7 +137,7 @@ __device__ int block_scan(int v, int* sh)
 // Fills `list` with this workgroup's tiles and returns their number; *rows_end is
 // the last group's clamped end.  end_sh: the groups' clamped ends; first_sh: each
 // group's first row tile.
-__device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_sh, Tile* list, int* rows_end)
+__device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_sh, TileList& list, int* rows_end)
 {
     const int t = (int)threadIdx.x, R = a.rows;
     const int per = (a.G + kThreads - 1) / kThreads;
@@ -165,8 +180,10 @@ __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_
     const int full = n / cus, over = n - full * cus;
     const int parts = 4 * over <= cus && R == 256 ? 4 : 2 * over <= cus ? 2 : 1;
     const int count = full + (cu < over * parts);
-    for (int j = t; j < count && j < kMaxEntries; j += kThreads) {
-        const int L = lo + j * cus + (j < full ? cu : cu / parts);
+    const int j = lane_id();
+    list.mine = Tile{0, 0, 0, 0};
+    if (j < count) {
+        const int L = lo + j * cus + (j < full ? (cu + kShift * j) % cus : cu / parts);
         int p = 0, r = a.G - 1;                          // the last group whose tiles start at or before L
         while (p < r) {
             const int mid = (p + r + 1) >> 1;
@@ -185,7 +202,7 @@ __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_
         tl.r1 = tl.r0 + height < end_sh[p] ? tl.r0 + height : end_sh[p];
         if (tl.r1 < tl.r0) tl.r1 = tl.r0;                // a part past the group's rows
         tl.c = cb * kColBlock + rem % width;
-        list[j] = tl;
+        list.mine = tl;
     }
     *rows_end = end_sh[a.G - 1];
     return count < kMaxEntries ? count : kMaxEntries;
@@ -205,10 +222,10 @@ struct Loader {
     v4i w, ws, xs;                                       // resources that start at the next slot
     v4i x, xb;                                           // X8: at its first half's and the running slot's second half
     int entry, left;                                     // the tile's place in the list; its slots from the next one on
-    bool new_chunk;                                      // the next slot is the first of a chunk of scales
+    int phase;                                           // the next slot's place in its chunk of scales
     uint32_t chunk;                                      // the place in LDS of the next chunk
     int xentry, xleft;                                   // X8: the same of the X codes
-    uint32_t off_w[8], off_x[8], off_ws, off_xs;         // lane offsets of the wave's loads, 8 rows each
+    uint32_t off_w[8], off_x[8], off_ws[2], off_xs[2];   // lane offsets of the wave's loads, 8 rows each (scales: 32)
     uint32_t lds_data, lds_scale;                        // LDS addresses of the wave's part of ring slot 0
     uint32_t upper;                                      // bit 31: this lane's chunk of load 0 is in the second half of a row's slot
 
@@ -223,11 +240,16 @@ struct Loader {
             off_x[i] = row * a.ldx + 16u * chunk;
         }
         upper = ((uint32_t)lane >> 2) << 31;
-        off_ws = (uint32_t)(64 * wave + lane) * ((uint32_t)a.K / 32u);
-        off_xs = (uint32_t)(64 * wave + lane) * a.ldxs;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t row = (uint32_t)(64 * wave + 32 * i + (lane >> 1));
+            const uint32_t part = 16u * (((uint32_t)lane ^ (row >> 3)) & 1u);
+            off_ws[i] = row * ((uint32_t)a.K / 32u) + part;
+            off_xs[i] = row * a.ldxs + part;
+        }
         const uint32_t base = (uint32_t)uniform((int)(uint32_t)(uintptr_t)(LdsPtr)lds);
         lds_data = base + 8192u * (uint32_t)wave;
-        lds_scale = base + kScaleBase + 1024u * (uint32_t)wave;
+        lds_scale = base + kScaleBase + 2048u * (uint32_t)wave;
     }
 
     // Tile e of the list; past its end, one that loads nothing.
@@ -236,32 +258,31 @@ struct Loader {
         int r0;
         uint32_t nw, nx;
     };
-    static __device__ __forceinline__ Place place_of(const MmArgs& a, const Tile* list, int e, int count)
+    static __device__ __forceinline__ Place place_of(const MmArgs& a, const TileList& list, int e, int count)
     {
         const bool some = e < count;
-        const Tile t = list[some ? e : 0];
-        const int g = some ? uniform(t.g) : 0;
-        const int n0 = some ? uniform(t.c) * kCols : 0;
+        const Tile t = list.at(some ? e : 0);
+        const int n0 = t.c * kCols;
         Place p;
-        p.r0 = some ? uniform(t.r0) : 0;
-        p.nx = some ? (uint32_t)(uniform(t.r1) - p.r0) : 0u;
+        p.r0 = t.r0;
+        p.nx = some ? (uint32_t)(t.r1 - t.r0) : 0u;
         p.nw = some ? (uint32_t)(a.N - n0 < kCols ? a.N - n0 : kCols) : 0u;
-        p.wrow = (int64_t)g * a.N + n0;
+        p.wrow = (int64_t)t.g * a.N + n0;
         return p;
     }
     // The first slot of tile `entry`: W codes and both scales, and of E2M1 tokens the X codes.
-    __device__ __forceinline__ void set_tile(const MmArgs& a, const Tile* list, int count, int nslots)
+    __device__ __forceinline__ void set_tile(const MmArgs& a, const TileList& list, int count, int nslots)
     {
         const uint32_t half = (uint32_t)a.K / 2u, kb = (uint32_t)a.K / 32u;
         const Place p = place_of(a, list, entry, count);
         left = nslots;
-        new_chunk = true;
+        phase = 0;
         w = resource(a.wq + p.wrow * half, p.nw * half);
         ws = resource(a.ws + p.wrow * kb, p.nw * kb);
         xs = resource(a.xs + (int64_t)p.r0 * a.ldxs, p.nx ? (p.nx - 1u) * a.ldxs + kb : 0u);
         if constexpr (!X8) x = resource(a.xq + (int64_t)p.r0 * a.ldx, p.nx ? (p.nx - 1u) * a.ldx + half : 0u);
     }
-    __device__ __forceinline__ void set_x_tile(const MmArgs& a, const Tile* list, int count, int nslots)
+    __device__ __forceinline__ void set_x_tile(const MmArgs& a, const TileList& list, int count, int nslots)
     {
         const Place p = place_of(a, list, xentry, count);
         xleft = nslots;
@@ -279,7 +300,7 @@ struct Loader {
     // On to the next slot of the stream.  Where K ends half way through a tile's last
     // slot, that slot's X codes past K are to be zeros: E4M3, its second half loads
     // nothing; E2M1, for its loads their lanes' offsets leave the resource (bit 31).
-    __device__ __forceinline__ void advance(const MmArgs& a, const Tile* list, int count, int nslots)
+    __device__ __forceinline__ void advance(const MmArgs& a, const TileList& list, int count, int nslots)
     {
         if constexpr (X8) {
             xb = stepped(x, 128, xleft == 1 && a.K % kSlotK != 0);
@@ -297,7 +318,7 @@ struct Loader {
             set_tile(a, list, count, nslots);
         } else {
             --left;
-            new_chunk = !new_chunk;
+            phase = (phase + 1) & 3;
             w = stepped(w, 128);
             ws = stepped(ws, 8);
             xs = stepped(xs, 8);
@@ -313,20 +334,27 @@ struct Loader {
         for (int i = 0; i < 8; ++i) off_x[i] ^= (i & 1) ? upper ^ 0x80000000u : upper;
     }
 
-    // Scales travel in chunks of 16 bytes a row, two slots' worth (one group of 16384 x
-    // 8192 x 5120, E2M1: 351 us; 16 bytes for every slot, half of them unused, 374).
+    // Scales travel in chunks of 32 bytes a row, four slots' worth: a row is a line of its
+    // own, which costs the memory pipe as much as 128 bytes of codes.  (One group of 16384 x
+    // 8192 x 5120, E2M1: 16 bytes a slot, half of them unused, 374 us; 16 for two slots 351;
+    // with the later steps' gains, 16 for two 341, 32 for four 333.)  The two 16-byte parts
+    // of a row trade places in every other 8 rows, so that 16 rows' words meet 16 different
+    // pairs of banks.
     __device__ __forceinline__ void issue_scales()
     {
-        load_to_lds(ws, lds_scale + chunk * 2u * kScaleOperand, off_ws);
-        load_to_lds(xs, lds_scale + chunk * 2u * kScaleOperand + kScaleOperand, off_xs);
+        const uint32_t to = lds_scale + chunk * 2u * kScaleOperand;
+        load_to_lds(ws, to, off_ws[0]);
+        load_to_lds(ws, to + 1024u, off_ws[1]);
+        load_to_lds(xs, to + kScaleOperand, off_xs[0]);
+        load_to_lds(xs, to + kScaleOperand + 1024u, off_xs[1]);
         chunk ^= 1u;
     }
-    // Load I of the slot into ring slot b: W and (E2M1) X codes in turn.
+    // Load I of the slot's codes into ring slot b: W, then (E2M1) X.
     template <int I>
     __device__ __forceinline__ void issue(uint32_t b)
     {
-        constexpr int i = X8 ? I : I / 2;
-        if constexpr (X8 || I % 2 == 0) load_to_lds(w, lds_data + b * kSlotBytes + 1024u * i, off_w[i]);
+        constexpr int i = I % 8;
+        if constexpr (I < 8) load_to_lds(w, lds_data + b * kSlotBytes + 1024u * i, off_w[i]);
         else load_to_lds(x, lds_data + b * kSlotBytes + kOperandBytes + 1024u * i, off_x[i]);
     }
     template <int I, int END>
@@ -364,35 +392,41 @@ struct Lane {
     uint32_t wn, wm;                                     // the wave's place in the 2 x 2
 };
 
-template <bool X8, int TM, int T>
+// Pieces P .. END - 1 of a step's operands: 4 of W, then those of X.
+template <bool X8, int TM>
+constexpr int kPieces = 4 + TM * (X8 ? 2 : 1);
+template <bool X8, int TM, int T, int P, int END>
 __device__ __forceinline__ void read_step(Operands<X8, TM>& f, const uint8_t* lds, uint32_t b, const Lane& l)
 {
-    const uint8_t* W = lds + b * kSlotBytes + (128u * l.wn + l.row) * 128u + (((2u * T + l.h) ^ l.swz) << 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f.w[i] = *(const v4i*)(W + 4096 * i);
-    const uint8_t* X = lds + (X8 ? (uint32_t)(T / 2) : b) * kSlotBytes + kOperandBytes + (32u * TM * l.wm + l.row) * 128u;
-#pragma unroll
-    for (int p = 0; p < (X8 ? 2 : 1); ++p) {
-        const uint8_t* P = X + ((((X8 ? 4u * (T % 2) + 2u * p : 2u * T) + l.h) ^ l.swz) << 4);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) f.x[i][p] = *(const v4i*)(P + 4096 * i);
+    if constexpr (P < END) {
+        if constexpr (P < 4) {
+            const uint8_t* W = lds + b * kSlotBytes + (128u * l.wn + l.row) * 128u + (((2u * T + l.h) ^ l.swz) << 4);
+            f.w[P] = *(const v4i*)(W + 4096 * P);
+        } else {
+            constexpr int p = (P - 4) / TM, i = (P - 4) % TM;
+            const uint8_t* X = lds + (X8 ? (uint32_t)(T / 2) : b) * kSlotBytes + kOperandBytes + (32u * TM * l.wm + l.row) * 128u +
+                               ((((X8 ? 4u * (T % 2) + 2u * p : 2u * T) + l.h) ^ l.swz) << 4);
+            f.x[i][p] = *(const v4i*)(X + 4096 * i);
+        }
+        read_step<X8, TM, T, P + 1, END>(f, lds, b, l);
     }
 }
 
-// A slot's scale words: place `at` in LDS is its chunk's, 8 bytes on its second slot's.
+// A slot's scale words: place `at` in LDS is its chunk's and 8 bytes a slot.
 __device__ __forceinline__ uint32_t next_scales(uint32_t at, bool new_tile)
 {
     constexpr uint32_t kChunk = 2u * kScaleOperand;
-    return new_tile || (at & 8u) ? (at & kChunk) ^ kChunk : at | 8u;
+    return new_tile || (at & 24u) == 24u ? (at & kChunk) ^ kChunk : at + 8u;
 }
-template <int TM>
+template <int TM, int P, int END>
 __device__ __forceinline__ void read_scales(Scales<TM>& s, const uint8_t* lds, uint32_t at, const Lane& l)
 {
-    const uint8_t* p = lds + kScaleBase + at;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s.w[i] = *(const uint2*)(p + (128u * l.wn + 32u * i + l.row) * 16u);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) s.x[i] = *(const uint2*)(p + kScaleOperand + (32u * TM * l.wm + 32u * i + l.row) * 16u);
+    if constexpr (P < END) {
+        const uint8_t* p = lds + kScaleBase + (at ^ (2u * (l.row & 8u)));
+        if constexpr (P < 4) s.w[P] = *(const uint2*)(p + (128u * l.wn + 32u * P + l.row) * 32u);
+        else s.x[P - 4] = *(const uint2*)(p + kScaleOperand + (32u * TM * l.wm + 32u * (P - 4) + l.row) * 32u);
+        read_scales<TM, P + 1, END>(s, lds, at, l);
+    }
 }
 // Shifted so that bytes 0 and 2 of a word are the lane's blocks.
 template <int TM>
@@ -422,77 +456,107 @@ __device__ __forceinline__ void mfma(v16f (&acc)[4][TM], const Operands<X8, TM>&
                                                                 2 * (T & 1), sx);
 }
 
-// Step T's MFMAs, with loads A .. B - 1 of the next slot of the stream into ring
-// slot b and (X8) loads XA .. XB - 1 of X half H spread between them.
-template <bool X8, int TM, int T, bool ZERO, int A, int B, int H = 0, int XA = 0, int XB = 0, int I = 0>
-__device__ __forceinline__ void mfmas(v16f (&acc)[4][TM], const Operands<X8, TM>& f, const Scales<TM>& s, Loader<X8>& ld,
-                                      uint32_t b)
+// MFMAs I .. END - 1 of step T, each followed by its share of the other work of that
+// stretch: work(k, n) does part k of n.
+template <int V>
+using Int = std::integral_constant<int, V>;
+template <bool X8, int TM, int T, bool ZERO, int I, int END, int K = 0, class Work>
+__device__ __forceinline__ void mfmas(v16f (&acc)[4][TM], const Operands<X8, TM>& f, const Scales<TM>& s, const Work& work)
 {
-    constexpr int n = 4 * TM;
-    if constexpr (I < n) {
+    if constexpr (I < END) {
         mfma<X8, TM, T, ZERO, I>(acc, f, s);
-        ld.template issue_x<H, XA + I * (XB - XA) / n, XA + (I + 1) * (XB - XA) / n>();
-        ld.template issue_some<A + I * (B - A) / n, A + (I + 1) * (B - A) / n>(b);
-        if constexpr (A < B || XA < XB) __builtin_amdgcn_sched_barrier(0);
-        mfmas<X8, TM, T, ZERO, A, B, H, XA, XB, I + 1>(acc, f, s, ld, b);
+        work(Int<K>{}, Int<K + END - I>{});
+        __builtin_amdgcn_sched_barrier(0);
+        mfmas<X8, TM, T, ZERO, I + 1, END, K + 1>(acc, f, s, work);
     }
 }
+// The bounds of part k of n of a .. b.
+#define MXQ_PART(a, b) (a) + K.value * ((b) - (a)) / N.value, (a) + (K.value + 1) * ((b) - (a)) / N.value
 
-// How a slot's loads of codes are spread: the first kLoadsA in the last step of the slot
-// two before it, up to kLoadsB in the first step of the slot before it, the rest in the
-// second (E2M1 only).  All of E2M1's at once fill the memory pipe's queue and hold up the
-// MFMAs behind them: with the scales in every slot, 16640 x 8192 x 5120 over 16 groups took
-// 481 us against 451 in thirds.  The thirds 6 + 6 + 4 against 5 + 5 + 6: 434 against 438;
-// one group of 16384 rows 351 against 359.  X8: the halves' loads go out in steps 1 and 3.
-template <bool X8>
-struct Spread {
-    static constexpr int kLoadsA = X8 ? 3 : 6, kLoadsB = X8 ? 8 : 12, kLoadsC = X8 ? 8 : 16;
-};
+// The order of a slot: its four steps in halves, what is loaded under each, and the
+// barriers between them ("read": all waves' LDS reads are done; "there": all waves' loads
+// have landed).
+//
+//                 E2M1 (16 loads a slot)             E4M3 (8 of W, 8 of each X half)
+//   step 0        slot + 1: 8 .. 13                  W of slot + 1: 4 .. 7
+//                                                    X half 0 is read
+//     2nd half                                       X half 0 of slot + 1: 0 .. 3
+//   step 1        slot + 1: 14, 15                                         4 .. 7
+//                                                    X half 1 is there
+//     2nd half
+//   step 2
+//                 the slot is read                   the slot is read
+//     2nd half    slot + 2: 0, 1                     X half 1 of slot + 1: 0 .. 3
+//   step 3        slot + 2: 2 .. 4                                         4 .. 7
+//                 slot + 1 is there                  W, X half 0 of slot + 1 are there
+//     2nd half    slot + 2: 5 .. 7                   W of slot + 2: 0 .. 3
+//
+// A place in LDS is loaded anew from half a step after its last operands were asked for,
+// and waited for half a step before its first are used: a load has two steps or more to
+// arrive.  16640 x 8192 x 5120 over 16 ragged groups, E4M3 / E2M1: 602 / 423 us with one
+// barrier for both between steps 2 and 3 and a step's LDS reads ahead of its MFMAs, 586 /
+// 421 with this order, 581 / 405 with the reads between the MFMAs too.
+constexpr int kLoads2 = 2, kLoads3 = 5, kLoads3b = 8, kLoads0 = 14;   // E2M1: loads issued by the end of each stretch
 
-// Steps 0 and 1 of the slot in ring slot b, with the second part of the loads of the
-// slot after it.  On entry f[0] and s hold (or are being read with) its first step
-// and scales, on exit f[0] step 2.  X8: between them the barrier after which the
-// first X half's place may be loaded anew and the second half has landed (step 0's
-// own loads may still be under way: they are the W codes of the next slot).
 template <bool X8, int TM, bool FIRST>
 __device__ __forceinline__ void steps01(v16f (&acc)[4][TM], Operands<X8, TM> (&f)[2], Scales<TM>& s, Loader<X8>& ld,
                                         const uint8_t* lds, const Lane& l, uint32_t b)
 {
-    using S = Spread<X8>;
-    if (ld.new_chunk) ld.issue_scales();
+    constexpr int h = 2 * TM, n = 4 * TM, P = kPieces<X8, TM>;
+    if (ld.phase == 0) ld.issue_scales();
     shift_scales<TM>(s, l);
-    read_step<X8, TM, 1>(f[1], lds, b, l);
     __builtin_amdgcn_sched_barrier(0);
-    mfmas<X8, TM, 0, FIRST, S::kLoadsA, S::kLoadsB>(acc, f[0], s, ld, b ^ 1u);
-    if constexpr (X8) slot_barrier<S::kLoadsB - S::kLoadsA>();
-    else __builtin_amdgcn_sched_barrier(0);
-    read_step<X8, TM, 2>(f[0], lds, b, l);
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (X8) mfmas<X8, TM, 1, false, 0, 0, 0, 0, 8>(acc, f[1], s, ld, b);
-    else mfmas<X8, TM, 1, false, S::kLoadsB, S::kLoadsC>(acc, f[1], s, ld, b ^ 1u);
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (X8) {
+        mfmas<X8, TM, 0, FIRST, 0, h>(acc, f[0], s, [&](auto K, auto N) {
+            read_step<X8, TM, 1, MXQ_PART(0, P)>(f[1], lds, b, l);
+            ld.template issue_some<MXQ_PART(4, 8)>(b ^ 1u);
+        });
+        slot_barrier<63>();
+        mfmas<X8, TM, 0, FIRST, h, n>(acc, f[0], s, [&](auto K, auto N) { ld.template issue_x<0, MXQ_PART(0, 4)>(); });
+        mfmas<X8, TM, 1, false, 0, h>(acc, f[1], s, [&](auto K, auto N) { ld.template issue_x<0, MXQ_PART(4, 8)>(); });
+        slot_barrier<16>();                              // (newer: W and X half 0 of the next slot)
+        mfmas<X8, TM, 1, false, h, n>(acc, f[1], s, [&](auto K, auto N) { read_step<X8, TM, 2, MXQ_PART(0, P)>(f[0], lds, b, l); });
+    } else {
+        mfmas<X8, TM, 0, FIRST, 0, n>(acc, f[0], s, [&](auto K, auto N) {
+            read_step<X8, TM, 1, MXQ_PART(0, P)>(f[1], lds, b, l);
+            ld.template issue_some<MXQ_PART(kLoads3b, kLoads0)>(b ^ 1u);
+        });
+        mfmas<X8, TM, 1, false, 0, h>(acc, f[1], s, [&](auto K, auto N) {
+            ld.template issue_some<MXQ_PART(kLoads0, 16)>(b ^ 1u);
+            read_step<X8, TM, 2, MXQ_PART(0, P / 2)>(f[0], lds, b, l);
+        });
+        mfmas<X8, TM, 1, false, h, n>(acc, f[1], s, [&](auto K, auto N) { read_step<X8, TM, 2, MXQ_PART(P / 2, P)>(f[0], lds, b, l); });
+    }
 }
 
-// Steps 2 and 3, with the barrier between them and the first part of the loads into
-// this ring slot (X8: and those of the second X half); on exit f[0] and s hold the
-// next slot's, unless this is the tile's LAST.
+// On exit f[0] and s hold the next slot's first step and scales, unless this is the
+// tile's LAST.
 template <bool X8, int TM, bool LAST>
 __device__ __forceinline__ void steps23(v16f (&acc)[4][TM], Operands<X8, TM> (&f)[2], Scales<TM>& s, Loader<X8>& ld,
                                         const uint8_t* lds, const Lane& l, uint32_t b, uint32_t scales)
 {
-    read_step<X8, TM, 3>(f[1], lds, b, l);
-    __builtin_amdgcn_sched_barrier(0);
-    mfmas<X8, TM, 2, false, 0, 0>(acc, f[0], s, ld, b);
-    slot_barrier<0>();
+    constexpr int h = 2 * TM, n = 4 * TM, P = kPieces<X8, TM>;
+    mfmas<X8, TM, 2, false, 0, h>(acc, f[0], s, [&](auto K, auto N) { read_step<X8, TM, 3, MXQ_PART(0, P)>(f[1], lds, b, l); });
+    slot_barrier<63>();
+    mfmas<X8, TM, 2, false, h, n>(acc, f[0], s, [&](auto K, auto N) {
+        if constexpr (X8) ld.template issue_x<1, MXQ_PART(0, 4)>();
+        else ld.template issue_some<MXQ_PART(0, kLoads2)>(b);
+    });
+    mfmas<X8, TM, 3, false, 0, h>(acc, f[1], s, [&](auto K, auto N) {
+        if constexpr (X8) ld.template issue_x<1, MXQ_PART(4, 8)>();
+        else ld.template issue_some<MXQ_PART(kLoads2, kLoads3)>(b);
+    });
+    slot_barrier<X8 ? 8 : kLoads3>();                         // (newer: X half 1 of the next slot; the slot after it)
     const Scales<TM> now = s;
-    if constexpr (!LAST) {
-        read_step<X8, TM, 0>(f[0], lds, b ^ 1u, l);
-        read_scales<TM>(s, lds, scales, l);
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    mfmas<X8, TM, 3, false, 0, Spread<X8>::kLoadsA, 1, 0, X8 ? 8 : 0>(acc, f[1], now, ld, b);
-    __builtin_amdgcn_sched_barrier(0);
+    mfmas<X8, TM, 3, false, h, n>(acc, f[1], now, [&](auto K, auto N) {
+        if constexpr (!LAST) {
+            read_step<X8, TM, 0, MXQ_PART(0, P)>(f[0], lds, b ^ 1u, l);
+            read_scales<TM, MXQ_PART(0, 4 + TM)>(s, lds, scales, l);
+        }
+        ld.template issue_some<MXQ_PART(X8 ? 0 : kLoads3, X8 ? 4 : kLoads3b)>(b);
+    });
 }
+#undef MXQ_PART
 
 // The sums are needed here: without this the compiler moves MFMAs past the loads
 // that are meant to run under them, into the next basic block.
@@ -582,14 +646,14 @@ __device__ __forceinline__ void store_tile(const v16f (&acc)[4][TM], const MmArg
 // One tile: its slots are the next to come out of the stream, the first of them in
 // ring slot b; the loads are part way into the slot after it.
 template <bool X8, int TM, bool F32OUT>
-__device__ __forceinline__ void tile_product(Loader<X8>& ld, const MmArgs& a, const uint8_t* lds, const Tile* list, int count,
+__device__ __forceinline__ void tile_product(Loader<X8>& ld, const MmArgs& a, const uint8_t* lds, const TileList& list, int count,
                                              const Tile& t, const Lane& l, int nslots, uint32_t& b, uint32_t& scales)
 {
     v16f acc[4][TM];
     Operands<X8, TM> f[2];
     Scales<TM> s;
-    read_scales<TM>(s, lds, scales, l);
-    read_step<X8, TM, 0>(f[0], lds, b, l);
+    read_scales<TM, 0, 4 + TM>(s, lds, scales, l);
+    read_step<X8, TM, 0, 0, kPieces<X8, TM>>(f[0], lds, b, l);
     steps01<X8, TM, true>(acc, f, s, ld, lds, l, b);
     pin<TM>(acc);
     ld.advance(a, list, count, nslots);
@@ -621,7 +685,7 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLdsBytes];
     const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
-    Tile* list = (Tile*)(lds + kEntryBase);
+    TileList list;
     int rows_end;
     int count;
     {
@@ -631,14 +695,16 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
         count = uniform(make_list(a, end_sh, first_sh, scan_sh, list, &rows_end));
         rows_end = uniform(rows_end);
     }
-    __syncthreads();                                     // the list is complete, the scan's arrays are free
-    if (count > 0 && uniform(list[count - 1].r0) == uniform(list[count - 1].r1)) --count;
+    __syncthreads();                                     // the scan's arrays are free
+    if (count > 0) {
+        const Tile last = list.at(count - 1);
+        if (last.r0 == last.r1) --count;
+    }
 
     if (count > 0) {
         const Lane l = {(uint32_t)(lane & 31), (uint32_t)(lane >> 5), (uint32_t)((lane >> 1) & 7),
                         (uint32_t)(wave >> 1), (uint32_t)(wave & 1)};
         const int nslots = (a.K + kSlotK - 1) / kSlotK;
-        using S = Spread<X8>;
         Loader<X8> ld;
         ld.set_lanes(a, lds, wave, lane);
         ld.entry = ld.xentry = 0;
@@ -647,19 +713,15 @@ void mxfp4_mm_tile_kernel(const MmArgs a)
         if constexpr (X8) ld.set_x_tile(a, list, count, nslots);
         else if (a.K < kSlotK) ld.toggle_half();
         ld.issue_scales();
-        ld.template issue_some<0, S::kLoadsC>(0);
+        ld.template issue_some<0, X8 ? 8 : 16>(0);
         if constexpr (X8) ld.template issue_x<0, 0, 8>();
         ld.advance(a, list, count, nslots);
         if constexpr (X8) ld.template issue_x<1, 0, 8>();
-        ld.template issue_some<0, S::kLoadsA>(1);
+        ld.template issue_some<0, X8 ? 4 : kLoads3b>(1);
         slot_barrier<0>();
         uint32_t b = 0, scales = 0;
         for (int e = 0; e < count; ++e) {
-            Tile t = list[e];
-            t.g = uniform(t.g);
-            t.r0 = uniform(t.r0);
-            t.r1 = uniform(t.r1);
-            t.c = uniform(t.c);
+            const Tile t = list.at(e);
             // a group's last tile runs at the smallest of three heights that holds its rows
             const int rows = t.r1 - t.r0;
             if (rows > 128) tile_product<X8, 4, F32OUT>(ld, a, lds, list, count, t, l, nslots, b, scales);
@@ -690,13 +752,12 @@ hipError_t launch_mxfp4_mm_tile(const void* xq, const void* xs, bool x8, int64_t
     const int64_t cols = (N + kCols - 1) / kCols;
     const auto tiles = [&](int rows) { return (((int64_t)M + rows - 1) / rows + G) * cols; };   // at most
     const int rows = tiles(256) >= kManyTiles * cus ? 256 : 128;
-    // One workgroup a CU, fewer when there are not that many tiles, more (which then run one
-    // after the other) when a workgroup's list would not hold its tiles.
-    const int64_t most = tiles(rows);
-    const int64_t parts = most * (rows / 64);
+    // One workgroup a CU, fewer when there are not that many tiles, a multiple of it (which
+    // then run one after the other) when a workgroup's list would not hold its tiles: it
+    // has at most (most + 8) / grid + 1.
+    const int64_t most = tiles(rows), parts = most * (rows / 64);
     int64_t grid = parts < cus ? parts : cus;
-    const int64_t least = (most + kMaxEntries - kXcds - 1) / (kMaxEntries - kXcds);
-    grid = grid < least ? least : grid;
+    grid *= (most + kXcds + grid * (kMaxEntries - 1) - 1) / (grid * (kMaxEntries - 1));
     grid = (grid + kXcds - 1) / kXcds * kXcds;
     const MmArgs a = {(const uint8_t*)xq, (const uint8_t*)xs, (const uint8_t*)wq, (const uint8_t*)wsc, offs, y,
                       (uint32_t)ldx, (uint32_t)ldxs, M, N, K, G, rows};

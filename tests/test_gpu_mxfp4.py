@@ -251,6 +251,26 @@ def test_product_many_groups():
     check(*operands(M, N, K, G, mxq.MXQ_FMT_E2M1, 9), ends, mxq.MXQ_FMT_E2M1, torch.float32)
 
 
+def test_product_more_tiles_than_one_launch_of_workgroups_lists():
+    """Over 16384 output tiles of 256 x 256, sampled rows against the plain product."""
+    M, N, K = 131072 + 77, 8192, 128
+    ends = [70001, 70300, M - 3]
+    wq = torch.randint(0, 256, (3, N, K // 2), dtype=torch.uint8, device="cuda")
+    ws = torch.randint(122, 130, (3, N, K // 32), dtype=torch.uint8, device="cuda")
+    xq = torch.randint(0, 256, (M, K // 2), dtype=torch.uint8, device="cuda")
+    xs = torch.randint(122, 130, (M, K // 32), dtype=torch.uint8, device="cuda")
+    offs = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    y = mxq.mxfp4_grouped_mm(xq, xs, wq, ws, offs, mxq.MXQ_FMT_E2M1, out_dtype=torch.float32)
+    assert torch.all(y[M - 3:] == 0)
+    starts = [0] + ends[:-1]
+    for g, (a, b) in enumerate(zip(starts, ends)):
+        rows = sorted({a, a + 1, (a + b) // 2, b - 2, b - 1} | {a + (b - a) * i // 57 for i in range(57)})
+        x = P.mxfp4_decode(xq[rows].cpu().numpy(), xs[rows].cpu().numpy())
+        w = P.mxfp4_decode(wq[g].cpu().numpy(), ws[g].cpu().numpy())
+        size = np.abs(x) @ np.abs(w).T
+        assert np.all(np.abs(y[rows].double().cpu().numpy() - x @ w.T) <= K / 16 * 2.0 ** -24 * size)
+
+
 def test_product_weights_past_two_to_the_31_bytes():
     """Weights of 2.7 GB: the last experts' rows, sampled columns, against the plain product."""
     G, N, K, M = 128, 8192, 5120, 24
