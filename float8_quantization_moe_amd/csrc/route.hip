@@ -235,33 +235,39 @@ void route_topk_kernel(const void* __restrict__ logits, const float* __restrict_
         for (int i = 0; i < NE; ++i) key[i] = l[i] > MXQ_NEG_INF && key[i] > MXQ_NEG_INF ? key[i] : MXQ_NEG_INF;   // (NaN too)
 
         if (groups) {                                            // (uniform)
+            // each lane's four neighbours are of one group if that has a multiple of 4: then
+            // their two largest go to LDS, else all four
+            const bool quads = a.group_size % 4 == 0;
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                float4 w;
-                w.x = key[4 * j] > MXQ_NEG_INF ? v[4 * j] : MXQ_NEG_INF;
-                w.y = key[4 * j + 1] > MXQ_NEG_INF ? v[4 * j + 1] : MXQ_NEG_INF;
-                w.z = key[4 * j + 2] > MXQ_NEG_INF ? v[4 * j + 2] : MXQ_NEG_INF;
-                w.w = key[4 * j + 3] > MXQ_NEG_INF ? v[4 * j + 3] : MXQ_NEG_INF;
-                float* dst = values + 4 * (lane + L * j);
-                dst[0] = w.x, dst[1] = w.y, dst[2] = w.z, dst[3] = w.w;
+                float w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c] = key[4 * j + c] > MXQ_NEG_INF ? v[4 * j + c] : MXQ_NEG_INF;
+                if (quads) {
+                    const float a1 = fmaxf(w[0], w[1]), a2 = fminf(w[0], w[1]), b1 = fmaxf(w[2], w[3]), b2 = fminf(w[2], w[3]);
+                    ((float2*)values)[lane + L * j] = make_float2(fmaxf(a1, b1), fmaxf(fminf(a1, b1), fmaxf(a2, b2)));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) values[4 * (lane + L * j) + c] = w[c];
+                }
             }
             wave_order();
-            // 2^lg lanes a group, each every 2^lg-th of its values, from a place of its own on:
+            // 2^lg lanes a group, each every 2^lg-th of its entries, from a place of its own on:
             // groups of 16 or more floats start in the same few banks (32768 x 256, 8 groups:
             // 34.7 -> 27.2 us; 16384 x 512: 31.0 -> 27.9)
-            const int lg = a.lanes_log2, P = 1 << lg;
+            const int lg = a.lanes_log2, P = 1 << lg, entries = quads ? a.group_size / 4 : a.group_size;
             for (int g0 = lane >> lg; g0 - (lane >> lg) < a.n_groups; g0 += L >> lg) {
                 const int g = g0 < a.n_groups ? g0 : 0, p = lane & (P - 1);
-                const int n = (a.group_size - p + P - 1) >> lg;
-                const float* of = values + g * a.group_size + p;
+                const int n = (entries - p + P - 1) >> lg;
                 float v1 = MXQ_NEG_INF, v2 = MXQ_NEG_INF;
                 int at = n > 0 ? lane_id() % n : 0;
-#pragma unroll 4
+#pragma unroll 2
                 for (int i = 0; i < n; ++i) {
-                    const float t = of[at << lg];
+                    const int k = g * entries + p + (at << lg);
+                    const float2 t = quads ? ((const float2*)values)[k] : make_float2(values[k], MXQ_NEG_INF);
                     at = at + 1 < n ? at + 1 : 0;
-                    v2 = fmaxf(v2, fminf(v1, t));
-                    v1 = fmaxf(v1, t);
+                    v2 = fmaxf(fmaxf(v2, t.y), fminf(v1, t.x));
+                    v1 = fmaxf(v1, t.x);
                 }
                 for (int d = 1; d < P; d *= 2) {
                     const float o1 = __shfl_xor(v1, d), o2 = __shfl_xor(v2, d);
