@@ -18,13 +18,20 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u_dword __attribute__((ext_vector_type(4), aligned(4)));   // 16 bytes at a multiple of 4
 
-// The tile kernel takes a call from 8 rows a group and 40 rows more on.  This kernel
-// passes over a group's weights once for every 16 rows, so what decides is the
-// largest group: of one group all rows, of many with uneven sizes several times the
-// average.  Measured at 8192 x 5120, MXFP8 tokens, this kernel / the tile kernel:
-// 1 group, 32 rows 14.5 / 21.9 us, 64 rows 25.3 / 22.6; 4 groups, 64 rows 31.5 /
-// 28.4; 16 groups, 64 rows 61 / 73, 128 rows 86 / 81.
-constexpr int64_t kManyRows = 8, kManyRowsMore = 40;
+// From this many rows on the tile kernel takes a call.  This kernel passes over a group's
+// weights once for every 16 rows, so what decides is the largest group; the tile kernel
+// takes 10 us and more however few the rows, which counts where the experts are small.
+// Measured (uneven groups; MXFP8 tokens, this kernel / the tile kernel, us):
+//   8192 x 5120   1 group, 64 rows 25 / 25, 96 rows 37 / 25; 16 groups, 96 rows 73 / 77, 128 rows 84 / 77
+//   4096 x 4096   4 groups, 72 rows 19 / 23, 100 rows 23 / 23; 8 groups, 72 rows 24 / 24
+//   2048 x 2048   2 groups, 64 rows 9.6 / 14.4, 100 rows 13.9 / 14.7; 32 groups, 128 rows 16.6 / 16.3
+//   1736 x 1408   16 groups, 168 rows 9.8 / 12.6, 256 rows 13.0 / 12.9
+//   1024 x 2048   64 groups, 200 rows 15.0 / 16.2, 300 rows 19.8 / 18.6
+//   1024 x 1024   1 group, 64 rows 8.3 / 10.8, 128 rows 13.8 / 11.2
+int64_t many_rows(int64_t N, int64_t K, int64_t G)
+{
+    return 80 + (N * K >= (int64_t)1 << 22 ? G / 2 : 12 * G < 176 ? 12 * G : 176);
+}
 constexpr int kTN = 2, kTM = 1;       // 32 columns x 16 rows a workgroup: 24.4 us at 8 rows of 16 groups (16 columns
                                       // 27.7, 64 columns 31 and more; 32 rows 42)
 constexpr int kStepK = 128;           // k of one 16x16 MFMA: four scale blocks
@@ -275,7 +282,7 @@ hipError_t launch_mxfp4_mm(const void* xq, const void* xs, bool x8, int64_t ldx,
                            const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
                            void* workspace, hipStream_t stream)
 {
-    if (M >= kManyRows * G + kManyRowsMore)
+    if (M >= many_rows(N, K, G))
         return launch_mxfp4_mm_tile(xq, xs, x8, ldx, ldxs, wq, wsc, offs, M, N, K, G, y, f32_out, stream);
     const FewArgs a = {(const uint8_t*)xq, (const uint8_t*)xs, (const uint8_t*)wq, (const uint8_t*)wsc, offs, y,
                        ldx, ldxs, M, N, K, G};

@@ -50,9 +50,10 @@ static_assert(kLdsBytes <= 160 * 1024, "LDS of a CU");
 // E2M1) against 17.7 / 14.5; the other way round above that: one group of 16384 rows
 // 632 / 486 against 538 / 379.
 constexpr int kManyTiles = 1;
-// Column tiles of a block of the tile order; one group of 16384 x 8192 x 5120, E4M3: 2
-// 521 us, 3 533, 4 580, 8 575 (1 measured slower before); 16 groups 625 / 642 / 643 / 691.
-constexpr int kColBlock = 2;                             // column tiles of a block of the tile order
+// Column tiles of a block of the tile order.  One group of 16384 x 8192 x 5120, E4M3 / E2M1:
+// 1 530 / 359 us, 2 482 / 317, 3 471 / 316, 4 468 / 316; 16 ragged groups 559 / 389, 553 /
+// 389, 557 / 392, 557 / 394.
+constexpr int kColBlock = 2;
 // CUs by which the order moves on each round.  The short last tiles of equal groups come at
 // one place of every round, and would come to the same CUs; with a shift of 6, 16640 x 8192
 // x 5120 over 16 ragged groups, E4M3, 622 -> 590 us, 20000 x 4096 x 4096 over 24 320 -> 300
