@@ -78,7 +78,7 @@ void add_rmsnorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __res
                 if (r) rr[c] = T::load8(r + at, i);
             }
         }
-        float ss = 0.0f;
+        float ss[8] = {};                                 // eight short sums: an eighth of a chain's roundings
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = lane + c * LANES;
@@ -95,10 +95,13 @@ void add_rmsnorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __res
                 }
                 if (h) T::store8(h + at, i, xr[c]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss += a[e] * a[e];
+                for (int e = 0; e < 8; ++e) ss[e] += a[e] * a[e];
             }
         }
-        const float rs = 1.0f / sqrtf(row_sum<LANES>(ss, sh, turn) / (float)K + eps);
+        const float sum = ((ss[0] + ss[1]) + (ss[2] + ss[3])) + ((ss[4] + ss[5]) + (ss[6] + ss[7]));
+        // (in doubles, rounded once: with three roundings in floats rstd was off by 0.75 units
+        // of 2^-24 in the mean square against 0.6)
+        const float rs = (float)(1.0 / sqrt((double)row_sum<LANES>(sum, sh, turn) / K + (double)eps));
         if (rstd && lane == 0) rstd[m] = rs;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
