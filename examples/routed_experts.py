@@ -76,8 +76,7 @@ def forward(b: Block, x: torch.Tensor, residual: torch.Tensor):
 
     F = b.up[0].shape[1]
     up = torch.empty((pairs, F), dtype=torch.bfloat16, device=x.device)
-    work = torch.empty(mxq.mxq_mxfp4_grouped_mm_workspace_bytes(pairs, F, K, E), dtype=torch.uint8, device=x.device)
-    mxq.mxq_mxfp4_grouped_mm_packed(packed, b.up[0], b.up[1], ends, up, work)
+    mxq.mxq_mxfp4_grouped_mm_packed(packed, b.up[0], b.up[1], ends, up)
     q, s = mxq.quantize_mxfp4(torch.nn.functional.silu(up))
     rows = mxq.mxfp4_grouped_mm(q, s, b.down[0], b.down[1], ends, x_format=mxq.MXQ_FMT_E2M1)
 

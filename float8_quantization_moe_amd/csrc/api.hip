@@ -352,16 +352,9 @@ static mxq_status check_mxfp4_mm_sizes(int64_t M, int64_t N, int64_t K, int64_t 
     return mxq::mxfp4_mm_sizes_ok(M, N, K, G) ? MXQ_OK : MXQ_ERR_SHAPE;
 }
 
-size_t mxq_mxfp4_grouped_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t G)
-{
-    if (check_mxfp4_mm_sizes(M, N, K, G) != MXQ_OK) return 0;
-    return mxq::mxfp4_mm_workspace_bytes(M, N, G);
-}
-
 mxq_status mxq_mxfp4_grouped_mm(const void* xq, const void* xs_e8m0, int x_format, const void* wq_e2m1,
                                 const void* ws_e8m0, const int32_t* group_end_offs, int64_t M, int64_t N, int64_t K,
-                                int32_t G, int out_dtype, void* y, void* workspace, size_t workspace_bytes,
-                                void* stream)
+                                int32_t G, int out_dtype, void* y, void* stream)
 {
     const mxq_status st = check_mxfp4_mm_sizes(M, N, K, G);
     if (st != MXQ_OK) return st;
@@ -372,17 +365,15 @@ mxq_status mxq_mxfp4_grouped_mm(const void* xq, const void* xs_e8m0, int x_forma
     if (!aligned16(xq) || !aligned16(xs_e8m0) || !aligned16(wq_e2m1) || !aligned16(ws_e8m0) || !aligned16(y))
         return MXQ_ERR_ALIGN;
     if (((uintptr_t)group_end_offs & 3u) != 0) return MXQ_ERR_ALIGN;
-    if (!workspace || workspace_bytes < mxq::mxfp4_mm_workspace_bytes(M, N, G)) return MXQ_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
     const bool x8 = x_format == MXQ_FMT_E4M3;
     return hip_status(mxq::launch_mxfp4_mm(xq, xs_e8m0, x8, x8 ? K : K / 2, K / 32, wq_e2m1, ws_e8m0, group_end_offs,
-                                           (int)M, (int)N, (int)K, (int)G, y, out_dtype == MXQ_OUT_F32, workspace,
+                                           (int)M, (int)N, (int)K, (int)G, y, out_dtype == MXQ_OUT_F32,
                                            (hipStream_t)stream));
 }
 
 mxq_status mxq_mxfp4_grouped_mm_packed(const void* packed, const void* wq_e2m1, const void* ws_e8m0,
                                        const int32_t* group_end_offs, int64_t M, int64_t N, int64_t K, int32_t G,
-                                       int out_dtype, void* y, void* workspace, size_t workspace_bytes, void* stream)
+                                       int out_dtype, void* y, void* stream)
 {
     const mxq_status st = check_mxfp4_mm_sizes(M, N, K, G);
     if (st != MXQ_OK) return st;
@@ -392,12 +383,10 @@ mxq_status mxq_mxfp4_grouped_mm_packed(const void* packed, const void* wq_e2m1, 
     if (!packed || !wq_e2m1 || !ws_e8m0 || !group_end_offs || !y) return MXQ_ERR_NULL;
     if (!aligned16(packed) || !aligned16(wq_e2m1) || !aligned16(ws_e8m0) || !aligned16(y)) return MXQ_ERR_ALIGN;
     if (((uintptr_t)group_end_offs & 3u) != 0) return MXQ_ERR_ALIGN;
-    if (!workspace || workspace_bytes < mxq::mxfp4_mm_workspace_bytes(M, N, G)) return MXQ_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
     const int64_t ldp = K + K / 32;
     const uint8_t* base = static_cast<const uint8_t*>(packed);
     return hip_status(mxq::launch_mxfp4_mm(base, base + K, true, ldp, ldp, wq_e2m1, ws_e8m0, group_end_offs, (int)M,
-                                           (int)N, (int)K, (int)G, y, out_dtype == MXQ_OUT_F32, workspace,
+                                           (int)N, (int)K, (int)G, y, out_dtype == MXQ_OUT_F32,
                                            (hipStream_t)stream));
 }
 

@@ -57,11 +57,10 @@ hipError_t launch_mxfp4_quantize(const void* x, int64_t M, int64_t K, void* q, v
                                  hipStream_t stream);
 hipError_t launch_mxfp4_dequantize(const void* q, const void* s, int64_t M, int64_t K, void* y, hipStream_t stream);
 bool mxfp4_mm_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t G);
-size_t mxfp4_mm_workspace_bytes(int64_t M, int64_t N, int32_t G);
 // ldx, ldxs: row strides in bytes of the token codes (a multiple of 16) and scales (of 4).
 hipError_t launch_mxfp4_mm(const void* xq, const void* xs, bool x8, int64_t ldx, int64_t ldxs, const void* wq,
                            const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
-                           void* workspace, hipStream_t stream);
+                           hipStream_t stream);
 // Its part for groups of many rows.
 hipError_t launch_mxfp4_mm_tile(const void* xq, const void* xs, bool x8, int64_t ldx, int64_t ldxs, const void* wq,
                                 const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,

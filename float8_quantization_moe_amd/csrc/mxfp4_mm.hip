@@ -276,11 +276,9 @@ bool mxfp4_mm_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t G)
     return grouped_mm_sizes_ok(M, N, K, G);
 }
 
-size_t mxfp4_mm_workspace_bytes(int64_t M, int64_t N, int32_t G) { return grouped_mm_workspace_bytes(M, N, G); }
-
 hipError_t launch_mxfp4_mm(const void* xq, const void* xs, bool x8, int64_t ldx, int64_t ldxs, const void* wq,
                            const void* wsc, const int32_t* offs, int M, int N, int K, int G, void* y, bool f32_out,
-                           void* workspace, hipStream_t stream)
+                           hipStream_t stream)
 {
     if (M >= many_rows(N, K, G))
         return launch_mxfp4_mm_tile(xq, xs, x8, ldx, ldxs, wq, wsc, offs, M, N, K, G, y, f32_out, stream);

@@ -50,7 +50,7 @@ EXPORTED = ("mxq_abi_version", "mxq_status_string", "mxq_last_hip_error", "mxq_q
             "mxq_set_group_scale_knobs", "mxq_group_scale_fp8_noalloc", "mxq_group_scale_route_counters",
             "mxq_add_rmsnorm", "mxq_add_rmsnorm_bwd_workspace_bytes", "mxq_add_rmsnorm_bwd", "mxq_route_topk",
             "mxq_route_topk_bwd", "mxq_quantize_mxfp4", "mxq_dequantize_mxfp4",
-            "mxq_mxfp4_grouped_mm_workspace_bytes", "mxq_mxfp4_grouped_mm", "mxq_mxfp4_grouped_mm_packed")
+            "mxq_mxfp4_grouped_mm", "mxq_mxfp4_grouped_mm_packed")
 
 GROUP_METHODS = {"auto": 0, "hold": 1, "twopass": 2, "split": 3}
 
@@ -129,12 +129,10 @@ def lib() -> ctypes.CDLL:
         L.mxq_quantize_mxfp4.argtypes = [P, i64, i64, ci, P, P, P]
         L.mxq_dequantize_mxfp4.restype = ci
         L.mxq_dequantize_mxfp4.argtypes = [P, P, i64, i64, P, P]
-        L.mxq_mxfp4_grouped_mm_workspace_bytes.restype = sz
-        L.mxq_mxfp4_grouped_mm_workspace_bytes.argtypes = [i64, i64, i64, i32]
         L.mxq_mxfp4_grouped_mm.restype = ci
-        L.mxq_mxfp4_grouped_mm.argtypes = [P, P, ci, P, P, P, i64, i64, i64, i32, ci, P, P, sz, P]
+        L.mxq_mxfp4_grouped_mm.argtypes = [P, P, ci, P, P, P, i64, i64, i64, i32, ci, P, P]
         L.mxq_mxfp4_grouped_mm_packed.restype = ci
-        L.mxq_mxfp4_grouped_mm_packed.argtypes = [P, P, P, P, i64, i64, i64, i32, ci, P, P, sz, P]
+        L.mxq_mxfp4_grouped_mm_packed.argtypes = [P, P, P, P, i64, i64, i64, i32, ci, P, P]
         _lib = L
     return _lib
 
@@ -638,12 +636,8 @@ def dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, stream=None) -> torch.Ten
     return y
 
 
-def mxq_mxfp4_grouped_mm_workspace_bytes(M: int, N: int, K: int, G: int) -> int:
-    return int(lib().mxq_mxfp4_grouped_mm_workspace_bytes(int(M), int(N), int(K), int(G)))
-
-
 def mxq_mxfp4_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, x_format: int, wq: torch.Tensor, ws: torch.Tensor,
-                         group_end_offs: torch.Tensor, y: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+                         group_end_offs: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     """xq (M, K) E4M3 or (M, K/2) E2M1 by x_format, xs (M, K/32), wq (G, N, K/2) E2M1, ws (G, N, K/32),
     group_end_offs int32[G] (device) -> y (M, N) bf16 or float32."""
     if xq.dim() != 2 or wq.dim() != 3 or y.dim() != 2:
@@ -661,15 +655,12 @@ def mxq_mxfp4_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, x_format: int, wq: 
     po = _dev(group_end_offs, "group_end_offs", torch.int32, G)
     code = _float_code(y, "y")
     py = _dev(y, "y")
-    pw = _dev(workspace, "workspace")
-    wbytes = workspace.numel() * workspace.element_size()
-    _check(lib().mxq_mxfp4_grouped_mm(pxq, pxs, int(x_format), pwq, pws, po, M, N, K, G, code, py, pw, wbytes,
+    _check(lib().mxq_mxfp4_grouped_mm(pxq, pxs, int(x_format), pwq, pws, po, M, N, K, G, code, py,
                                       _stream(stream)), "mxq_mxfp4_grouped_mm")
 
 
 def mxq_mxfp4_grouped_mm_packed(packed: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
-                                group_end_offs: torch.Tensor, y: torch.Tensor, workspace: torch.Tensor,
-                                stream=None) -> None:
+                                group_end_offs: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     """packed (M, K + K/32) uint8 MXFP8 token rows, wq (G, N, K/2) / ws (G, N, K/32) -> y (M, N) bf16 or float32."""
     if packed.dim() != 2 or wq.dim() != 3 or y.dim() != 2:
         raise ValueError("packed must be 2-D, wq 3-D (G, N, K/2), y 2-D (M, N)")
@@ -683,9 +674,7 @@ def mxq_mxfp4_grouped_mm_packed(packed: torch.Tensor, wq: torch.Tensor, ws: torc
     po = _dev(group_end_offs, "group_end_offs", torch.int32, G)
     code = _float_code(y, "y")
     py = _dev(y, "y")
-    pw = _dev(workspace, "workspace")
-    wbytes = workspace.numel() * workspace.element_size()
-    _check(lib().mxq_mxfp4_grouped_mm_packed(pp, pwq, pws, po, M, N, K, G, code, py, pw, wbytes, _stream(stream)),
+    _check(lib().mxq_mxfp4_grouped_mm_packed(pp, pwq, pws, po, M, N, K, G, code, py, _stream(stream)),
            "mxq_mxfp4_grouped_mm_packed")
 
 
@@ -695,7 +684,5 @@ def mxfp4_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: t
     M = xq.shape[0]
     G, N, half = wq.shape
     y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
-    wsp = torch.empty(max(mxq_mxfp4_grouped_mm_workspace_bytes(M, N, 2 * half, G), 16), dtype=torch.uint8,
-                      device=xq.device)
-    mxq_mxfp4_grouped_mm(xq, xs, x_format, wq, ws, group_end_offs, y, wsp, stream)
+    mxq_mxfp4_grouped_mm(xq, xs, x_format, wq, ws, group_end_offs, y, stream)
     return y

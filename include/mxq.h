@@ -565,7 +565,7 @@ mxq_status mxq_dequantize_mxfp4(const void* q_e2m1, const void* s_e8m0, int64_t 
  *   wq_e2m1  (G, N, K/2) E2M1 codes and ws_e8m0 (G, N, K/32) scales
  *            (mxq_quantize_mxfp4 of the (G*N, K) weight).
  * Offsets, clamping, zero rows past the last end, out_dtype, alignment and
- * errors as mxq_scaled_grouped_mm.  The matrix cores sum the exact products of a
+ * errors as mxq_scaled_grouped_mm; it needs no workspace.  The matrix cores sum the exact products of a
  * block; with E4M3 tokens products far below a block's largest (2^-14 and less of
  * it) are cut off there, with E2M1 tokens a block's sum is exact; blocks are added
  * in fp32 and the result is rounded once.  NaN codes and scale 0xFF are outside
@@ -575,19 +575,16 @@ mxq_status mxq_dequantize_mxfp4(const void* q_e2m1, const void* s_e8m0, int64_t 
  * 1 <= G <= 4095 and a tile list of fewer than 2^30 entries (MXQ_ERR_SHAPE);
  * M == 0 or N == 0 is a no-op.
  */
-size_t mxq_mxfp4_grouped_mm_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t G);
 mxq_status mxq_mxfp4_grouped_mm(const void* xq, const void* xs_e8m0, int x_format, const void* wq_e2m1,
                                 const void* ws_e8m0, const int32_t* group_end_offs, int64_t M, int64_t N,
-                                int64_t K, int32_t G, int out_dtype, void* y, void* workspace,
-                                size_t workspace_bytes, void* stream);
+                                int64_t K, int32_t G, int out_dtype, void* y, void* stream);
 
 /* The same on MXFP8 token rows as mxq_dispatch_pack_mx packs them (K e4m3 codes
  * then K/32 e8m0 scales); K % 512 == 0.  Bit-identical to mxq_mxfp4_grouped_mm on
  * the unpacked codes and scales. */
 mxq_status mxq_mxfp4_grouped_mm_packed(const void* packed, const void* wq_e2m1, const void* ws_e8m0,
                                        const int32_t* group_end_offs, int64_t M, int64_t N, int64_t K,
-                                       int32_t G, int out_dtype, void* y, void* workspace,
-                                       size_t workspace_bytes, void* stream);
+                                       int32_t G, int out_dtype, void* y, void* stream);
 
 #ifdef __cplusplus
 }

@@ -121,12 +121,11 @@ def multiply(xq, xs, wq, ws, ends, fmt, dtype):
     M, (G, N, half) = xq.shape[0], wq.shape
     size = 2 if dtype == torch.bfloat16 else 4
     y = guarded(M * N * size, torch.uint8)
-    wsp = guarded(max(16, mxq.mxq_mxfp4_grouped_mm_workspace_bytes(M, N, 2 * half, G)), torch.uint8)
     dev = [torch.from_numpy(np.ascontiguousarray(t)).cuda() for t in (xq, xs, wq, ws)]
     offs = torch.tensor(ends, dtype=torch.int32, device="cuda")
-    mxq.mxq_mxfp4_grouped_mm(dev[0], dev[1], fmt, dev[2], dev[3], offs, y.t.view(dtype).view(M, N), wsp.t)
+    mxq.mxq_mxfp4_grouped_mm(dev[0], dev[1], fmt, dev[2], dev[3], offs, y.t.view(dtype).view(M, N))
     torch.cuda.synchronize()
-    assert y.guard_intact() and wsp.guard_intact()
+    assert y.guard_intact()
     return y.t.view(dtype).view(M, N)
 
 
@@ -233,10 +232,9 @@ def test_packed_rows_are_the_unpacked_product(M):
     w = torch.from_numpy((0.05 * rng.standard_normal((G * N, K))).astype(np.float32)).to(torch.bfloat16).cuda()
     wq, ws = mxq.quantize_mxfp4(w, mxq.MXQ_SCALE_RCEIL)
     wq, ws = wq.view(G, N, -1), ws.view(G, N, -1)
-    wsp = torch.empty(mxq.mxq_mxfp4_grouped_mm_workspace_bytes(M * k, N, K, G), dtype=torch.uint8, device="cuda")
     for dtype in (torch.bfloat16, torch.float32):
         y = torch.empty((M * k, N), dtype=dtype, device="cuda")
-        mxq.mxq_mxfp4_grouped_mm_packed(packed, wq, ws, ends, y, wsp)
+        mxq.mxq_mxfp4_grouped_mm_packed(packed, wq, ws, ends, y)
         z = mxq.mxfp4_grouped_mm(packed[:, :K].contiguous(), packed[:, K:].contiguous(), wq, ws, ends, out_dtype=dtype)
         assert torch.equal(y, z)
         assert torch.all(y[int(ends[-1]):] == 0) and torch.any(y[:int(ends[-1])] != 0)

@@ -90,23 +90,18 @@ def test_mxfp4_codec(L):
 
 
 def test_mxfp4_grouped_mm(L):
-    wb = L.mxq_mxfp4_grouped_mm_workspace_bytes
-    need = wb(700, 264, 1024, 5)
-    assert need > 0
-    assert wb(700, 264, 1000, 5) == 0 and wb(700, 260, 1024, 5) == 0 and wb(700, 264, 1024, 0) == 0
-    assert wb(700, 264, 1024, 4096) == 0 and wb(1 << 31, 264, 1024, 5) == 0 and wb(700, 264, 0, 5) == 0
-    f = caller(L.mxq_mxfp4_grouped_mm, "xq xs fmt wq ws offs M N K G dt y wsp wb st", xq=A, xs=A, fmt=0, wq=A, ws=A, offs=A,
-               M=700, N=264, K=1024, G=5, dt=0, y=A, wsp=A, wb=need, st=0)
+    f = caller(L.mxq_mxfp4_grouped_mm, "xq xs fmt wq ws offs M N K G dt y st", xq=A, xs=A, fmt=0, wq=A, ws=A, offs=A,
+               M=700, N=264, K=1024, G=5, dt=0, y=A, st=0)
     assert f(K=64) == SHAPE and f(N=4) == SHAPE and f(M=-1) == SHAPE and f(G=0) == SHAPE and f(K=1 << 24) == SHAPE
+    assert f(K=1000) == SHAPE and f(N=260) == SHAPE and f(G=4096) == SHAPE and f(M=1 << 31) == SHAPE and f(K=0) == SHAPE
     assert f(fmt=2) == DTYPE and f(dt=2) == DTYPE
     for p in ("xq", "xs", "wq", "ws", "offs", "y"):
         assert f(**{p: 0}) == NULL
         assert f(**{p: A + 2}) == ALIGN
-    assert f(wsp=0) == WORKSPACE and f(wb=need - 1) == WORKSPACE and f(wsp=A + 8) == ALIGN
     assert f(M=0, xq=0, y=0) == 0 and f(N=0, wq=0, y=0) == 0
-    g = caller(L.mxq_mxfp4_grouped_mm_packed, "p wq ws offs M N K G dt y wsp wb st", p=A, wq=A, ws=A, offs=A, M=700, N=264,
-               K=1024, G=5, dt=0, y=A, wsp=A, wb=need, st=0)
-    assert g(K=1152) == SHAPE and g(dt=7) == DTYPE and g(p=0) == NULL and g(p=A + 8) == ALIGN and g(wb=0) == WORKSPACE
+    g = caller(L.mxq_mxfp4_grouped_mm_packed, "p wq ws offs M N K G dt y st", p=A, wq=A, ws=A, offs=A, M=700, N=264,
+               K=1024, G=5, dt=0, y=A, st=0)
+    assert g(K=1152) == SHAPE and g(dt=7) == DTYPE and g(p=0) == NULL and g(p=A + 8) == ALIGN
     assert g(offs=A + 1) == ALIGN and g(M=0, p=0, y=0) == 0
 
 
