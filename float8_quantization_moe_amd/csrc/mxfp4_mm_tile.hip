@@ -10,6 +10,7 @@
 // A slot is four MFMA steps of 64 k; a step's operands are read from LDS during the step
 // before it.  With one wave a SIMD nothing issues while a load or an LDS read waits for
 // its pipe, so both are spread between the MFMAs, one or two after each (`mfmas`).
+// (Eight waves of 128 x 64, two a SIMD: 485 us against 488, E4M3, and 333 against 324.)
 //
 // The slots of successive tiles form one stream: the loads run ahead of the
 // products across the end of a tile, so the next tile's operands arrive while this
