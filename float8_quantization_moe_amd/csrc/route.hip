@@ -373,7 +373,8 @@ void route_topk_kernel(const void* __restrict__ logits, const float* __restrict_
 //   softmax: dl_e = s_e (g_e - sum_j g_j s_j) everywhere (g = 0 where not selected).
 // Softmax with renormalisation is the softmax over the selected logits alone, so
 // its gradient is 0 elsewhere and the other logits are not read.
-// Same layout as the forward; the selected experts' g pass through LDS.
+// Same layout as the forward, rows are the work of single waves; the selected experts'
+// g pass through LDS.
 template <bool F32L, bool SIGMOID, int L, int C>
 __global__ __launch_bounds__(kRouteThreads)
 void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __restrict__ ids,
@@ -415,6 +416,7 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
             total = lanes_sum<L>(sum);
             total = total > 0.0f ? total : 1.0f;
         }
+        const float unit = 1.0f / total;                          // (one rounding more than dividing: 2^-24 of the value)
         for (int e = lane; e < kMaxE; e += L) grad[sub][e] = 0.0f;
 
         // this lane's slots: the selected expert, its logit and gradient
@@ -427,7 +429,7 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
             id[i] = -1;
             ls[i] = MXQ_NEG_INF;
             g[i] = 0.0f;
-            if (t < topk) {
+            if (L * i < topk && t < topk) {                       // (the first is uniform)
                 const int e = ids[mr * topk + t];
                 if (e >= 0 && e < E) {
                     id[i] = e;
@@ -448,23 +450,23 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
             sc[i] = 0.0f;
-            if (id[i] >= 0) sc[i] = SIGMOID ? sigmoid_of(ls[i]) : expf(ls[i] - top) / total;
+            if (L * i < topk && id[i] >= 0) sc[i] = SIGMOID ? sigmoid_of(ls[i]) : expf(ls[i] - top) / total;
             sum += sc[i];
             dot += g[i] * sc[i];
         }
         sum = lanes_sum<L>(sum) + kTiny;
         dot = lanes_sum<L>(dot);
-        __syncthreads();
+        wave_order();
 #pragma unroll
         for (int i = 0; i < kSlots; ++i)
-            if (id[i] >= 0) {
+            if (L * i < topk && id[i] >= 0) {
                 float d = g[i];
                 if (renorm) d = (d - dot / sum) / sum;
                 if (SIGMOID) d *= sc[i] * (1.0f - sc[i]);
                 else if (renorm) d *= sc[i];
                 grad[sub][id[i]] = d;
             }
-        __syncthreads();
+        wave_order();
         if (live) {
 #pragma unroll
             for (int j = 0; j < C; ++j) {
@@ -473,7 +475,7 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     d[c] = grad[sub][e0 + c];
-                    if (dense) d[c] = p[j][c] / total * (d[c] - dot);
+                    if (dense) d[c] = p[j][c] * unit * (d[c] - dot);
                 }
                 if (vec) {
                     if (e0 < E) {
@@ -493,7 +495,7 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
                 }
             }
         }
-        __syncthreads();
+        wave_order();
     }
 }
 
