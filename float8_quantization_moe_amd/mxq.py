@@ -534,11 +534,15 @@ def add_rmsnorm(x: torch.Tensor, residual, weight: torch.Tensor, eps: float, str
 
 def add_rmsnorm_bwd(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dh=None, stream=None):
     """(dx, dweight) of mxq_add_rmsnorm_bwd."""
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D (M, K)")
     M, K = h.shape
     dx = torch.empty_like(h)
-    dweight = torch.empty(K, dtype=torch.float32, device=h.device)
-    ws = torch.empty(max(mxq_add_rmsnorm_bwd_workspace_bytes(M, K), 16), dtype=torch.uint8, device=h.device)
+    dweight = h.new_empty(K, dtype=torch.float32)
+    ws = h.new_empty(max(mxq_add_rmsnorm_bwd_workspace_bytes(M, K), 16), dtype=torch.uint8)
     mxq_add_rmsnorm_bwd(h, weight, rstd, dy, dh, dx, dweight, ws, stream)
+    if stream is not None:                     # the workspace is not free again before that stream is done with it
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
     return dx, dweight
 
 

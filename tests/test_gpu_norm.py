@@ -179,6 +179,24 @@ def test_no_rows():
     assert torch.all(dw == 0)
 
 
+@pytest.mark.parametrize("as_handle", [False, True], ids=["stream", "handle"])
+def test_backward_keeps_its_workspace_while_another_stream_runs(as_handle):
+    M, K = 512, 1024
+    torch.manual_seed(3)
+    h, dy = (torch.randn(M, K, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w, rstd = torch.ones(K, dtype=torch.bfloat16, device="cuda"), torch.rand(M, device="cuda") + 0.5
+    dx, dw = mxq.add_rmsnorm_bwd(h, w, rstd, dy)
+    size = mxq.mxq_add_rmsnorm_bwd_workspace_bytes(M, K)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)                       # a bounded spin: the call's kernels come after it
+    dx2, dw2 = mxq.add_rmsnorm_bwd(h, w, rstd, dy, stream=st.cuda_stream if as_handle else st)
+    held = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2) and len(held) == 4
+
+
 def test_other_stream():
     x, r, w = inputs(257, 5120, "bf16", 8)
     want = mxq.add_rmsnorm(x, r, w, EPS)
