@@ -268,6 +268,10 @@ constexpr int kNormMaxGrid = 1 << 22;
 // resident together (16640 x 5120: 256 / 512 / 768 / 1024 took 147 / 119 / 129 / 134 us;
 // 16640 x 1024: 512 / 1024 / 2048 25.4 / 27.5 / 31.0).
 constexpr int kBwdParts = 512;
+// Up to this many rows for each of a workgroup's row slots one workgroup takes them all, and
+// dw is its part: no second launch (1 to 16 rows, 64 to 5120 values: 12.3 us a call against
+// 15.4; 4 rows of 16384: 15.5 both).
+constexpr int kBwdOne = 4;
 // Inputs that do not fit the 256 MB last-level cache are read as streams (16640 x 5120:
 // 119 us, plain loads 128); smaller ones may be in it, where their writer left them
 // (4096 x 8192: 47.6 us, as streams 54).  The forward pass measured no such gain.
@@ -293,6 +297,7 @@ int64_t bwd_grid(int64_t M, int K)
 {
     const int rows = rows_per_group(K);
     const int64_t groups = (M + rows - 1) / rows;
+    if (groups <= kBwdOne) return groups < 1 ? groups : 1;
     return groups < kBwdParts ? groups : kBwdParts;
 }
 
@@ -333,7 +338,7 @@ hipError_t launch_add_rmsnorm_bwd(const void* h, const void* w, const float* rst
                                   hipStream_t stream)
 {
     const int64_t grid = bwd_grid(M, (int)K);
-    float* part = (float*)workspace;
+    float* part = grid == 1 ? dw : (float*)workspace;
     const bool nt = M * K * (f32 ? 4 : 2) * (dh ? 3 : 2) > kCacheBytes;
     if (grid > 0) {
 #define MXQ_LAUNCH(T, L, C, NT)                                                                                     \
@@ -351,6 +356,7 @@ hipError_t launch_add_rmsnorm_bwd(const void* h, const void* w, const float* rst
 #undef MXQ_CALL
 #undef MXQ_LAUNCH
     }
+    if (grid == 1) return hipGetLastError();
     hipLaunchKernelGGL(dweight_kernel, dim3((unsigned)((K / 4 + 7) / 8)), dim3(256), 0, stream, part,
                        (int)grid, (int)K, dw);
     return hipGetLastError();
