@@ -17,7 +17,7 @@
 //
 // Both are HBM bound (a few operations a value): the row is read once and held in
 // registers between its reduction and its use, LANES threads a row with C chunks
-// of 8 values each.  65536 x 5120 bf16 with every output: 507 us, 5.97 TB/s; backward of
+// of 8 values each.  65536 x 5120 bf16 with every output: 512 us, 5.9 TB/s; backward of
 // 16640 x 5120 with dh: 119 us, 5.7 TB/s.  The sum of a row is one fp32 tree in a fixed order, so
 // results are reproducible.
 #include "device_common.hpp"
