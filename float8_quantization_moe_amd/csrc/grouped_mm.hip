@@ -220,11 +220,13 @@ __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p)
 // VGPR result; its completion is counted by vmcnt, which the pair barrier waits
 // on explicitly.  Written in asm so that the compiler does not add a
 // conservative wait for it before every later LDS read.  (M0 is reserved by the
-// compiler and set before each of its own uses; nothing else here reads it.)
+// compiler and set before each of its own uses; nothing else here reads it.  A load
+// into LDS needs a wait state after M0 is written, which the compiler does not add
+// inside an asm block: the s_nop.)
 // The whole offset is the lane's (VGPR) offset, which the range check covers.
 __device__ __forceinline__ void dma16(const v4i& srd, uint32_t lds, uint32_t voff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(srd)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(srd)
                  : "memory");
 }
 

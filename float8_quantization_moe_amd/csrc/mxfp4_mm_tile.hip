@@ -106,10 +106,15 @@ __device__ __forceinline__ v4i resource(const void* base, uint32_t bytes)
 
 // Buffer load straight into LDS: lane l's 16 bytes land at lds + 16 l.  Counted by
 // vmcnt, which slot_barrier waits on; in asm so that the compiler adds no wait of
-// its own before later LDS reads.
+// its own before later LDS reads.  Nor does it add the wait states that such a load
+// needs inside an asm block: one after M0 is written, and five after a vector
+// instruction (a v_readlane that fetches a spilled resource) has written a scalar
+// register that the load reads.  s_mov and s_nop WAIT are WAIT + 2 of them.
+template <int WAIT = 0>
 __device__ __forceinline__ void load_to_lds(const v4i& srd, uint32_t lds, uint32_t voff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(srd)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop %3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(srd),
+                 "n"(WAIT)
                  : "memory");
 }
 
@@ -347,10 +352,10 @@ struct Loader {
     __device__ __forceinline__ void issue_scales()
     {
         const uint32_t to = lds_scale + chunk * 2u * kScaleOperand;
-        load_to_lds(ws, to, off_ws[0]);
-        load_to_lds(ws, to + 1024u, off_ws[1]);
-        load_to_lds(xs, to + kScaleOperand, off_xs[0]);
-        load_to_lds(xs, to + kScaleOperand + 1024u, off_xs[1]);
+        load_to_lds<3>(ws, to, off_ws[0]);
+        load_to_lds<3>(ws, to + 1024u, off_ws[1]);
+        load_to_lds<3>(xs, to + kScaleOperand, off_xs[0]);
+        load_to_lds<3>(xs, to + kScaleOperand + 1024u, off_xs[1]);
         chunk ^= 1u;
     }
     // Load I of the slot's codes into ring slot b: W, then (E2M1) X.
