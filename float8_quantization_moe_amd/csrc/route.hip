@@ -371,8 +371,13 @@ void route_topk_kernel(const void* __restrict__ logits, const float* __restrict_
 //         (scale * u_j - sum_i scale * u_i s_i / D) / D;
 //   sigmoid: dl_e = s_e (1 - s_e) g_e at the selected experts, 0 elsewhere;
 //   softmax: dl_e = s_e (g_e - sum_j g_j s_j) everywhere (g = 0 where not selected).
-// Softmax with renormalisation is the softmax over the selected logits alone, so
-// its gradient is 0 elsewhere and the other logits are not read.
+// Softmax with renormalisation, in terms that do not cancel: q = the softmax over the
+// selected logits alone, S = the sum of their s, D = S + 1e-20, m = sum_j scale u_j q_j;
+// then sum_j g_j s_j = m (S / D) (1e-20 / D) and
+//   dl_e = q_e (S / D) (scale u_e - m + m 1e-20 / D)  where selected, and everywhere
+//          - s_e m (S / D) (1e-20 / D).
+// That is q's own gradient unless S is as small as 1e-20, which takes a bias or groups
+// that keep a row's large logits out.
 // Same layout as the forward, rows are the work of single waves; the selected experts'
 // g pass through LDS.
 template <bool F32L, bool SIGMOID, int L, int C>
@@ -387,7 +392,6 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
     __shared__ float grad[kRows][kMaxE + 4];
     const int lane = (int)threadIdx.x % L, sub = (int)threadIdx.x / L;
     const bool vec = E % 4 == 0;
-    const bool dense = !SIGMOID && !renorm;
     for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < M; m0 += (int64_t)gridDim.x * kRows) {
         const int64_t m = m0 + sub;
         const bool live = m < M;
@@ -396,7 +400,7 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
 
         float l[C][4], p[C][4];
         float top = MXQ_NEG_INF, total = 1.0f;
-        if (dense) {                                              // (uniform)
+        if constexpr (!SIGMOID) {
 #pragma unroll
             for (int j = 0; j < C; ++j) {
                 load4<F32L>(row, 4 * (lane + L * j), E, vec, l[j]);
@@ -440,30 +444,44 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
             }
             seltop = fmaxf(seltop, ls[i]);
         }
-        float sum = 0.0f, dot = 0.0f;
+        // softmax, renormalised: the selected scores are q times their sum, and `first` is the
+        // score of the largest of them
+        float sum = 0.0f, dot = 0.0f, first = 0.0f;
+        float seltotal = total;
         if constexpr (!SIGMOID) {
-            if (!dense) {
-                top = lanes_max_f<L>(seltop);
-                top = top > MXQ_NEG_INF ? top : 0.0f;
+            if (renorm) {                                         // (uniform)
+                seltop = lanes_max_f<L>(seltop);
+                if (seltop > MXQ_NEG_INF) first = expf(seltop - top) * unit;
+                top = seltop > MXQ_NEG_INF ? seltop : 0.0f;
+                seltotal = 1.0f;
             }
         }
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
             sc[i] = 0.0f;
-            if (L * i < topk && id[i] >= 0) sc[i] = SIGMOID ? sigmoid_of(ls[i]) : expf(ls[i] - top) / total;
+            if (L * i < topk && id[i] >= 0) sc[i] = SIGMOID ? sigmoid_of(ls[i]) : expf(ls[i] - top) / seltotal;
             sum += sc[i];
             dot += g[i] * sc[i];
         }
         sum = lanes_sum<L>(sum) + kTiny;
         dot = lanes_sum<L>(dot);
+        float kept = 1.0f, tiny = 0.0f, rest = dot;               // rest: what s_e is multiplied by everywhere
+        if constexpr (!SIGMOID) {
+            if (renorm) {                                         // (uniform)
+                const float D = first * sum + kTiny;
+                kept = first * sum / D;
+                tiny = dot / sum * (kTiny / D);
+                rest = tiny * kept;
+            }
+        }
         wave_order();
 #pragma unroll
         for (int i = 0; i < kSlots; ++i)
             if (L * i < topk && id[i] >= 0) {
                 float d = g[i];
-                if (renorm) d = (d - dot / sum) / sum;
+                if (renorm) d = (d - dot / sum + tiny) / sum;
                 if (SIGMOID) d *= sc[i] * (1.0f - sc[i]);
-                else if (renorm) d *= sc[i];
+                else if (renorm) d *= sc[i] * kept;
                 grad[sub][id[i]] = d;
             }
         wave_order();
@@ -475,7 +493,7 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     d[c] = grad[sub][e0 + c];
-                    if (dense) d[c] = p[j][c] * unit * (d[c] - dot);
+                    if constexpr (!SIGMOID) d[c] = renorm ? d[c] - p[j][c] * unit * rest : p[j][c] * unit * (d[c] - rest);
                 }
                 if (vec) {
                     if (e0 < E) {

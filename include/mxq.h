@@ -523,10 +523,11 @@ mxq_status mxq_route_topk(const void* logits, int dtype, int64_t M, int32_t E, c
  * fp32 (M, topk), for the expert_ids that the forward selected (distinct in a
  * row; ids outside [0, E) count as empty slots).  flags: MXQ_ROUTE_RENORM or 0, as
  * in the forward.  The selection itself and the bias have no gradient.  With
- * sigmoid, or with softmax and MXQ_ROUTE_RENORM (then the weights are a softmax
- * over the selected logits), only the selected logits get one; every other value
- * of dlogits is written as zero.  logits and dlogits 16-byte aligned; sizes and
- * errors as mxq_route_topk.
+ * sigmoid only the selected logits get one; every other value of dlogits is
+ * written as zero.  With softmax every logit gets one; with MXQ_ROUTE_RENORM that
+ * of the others is about 1e-20 of the weights' unless the selected scores are as
+ * small as the 1e-20 of the forward's divisor.  logits and dlogits 16-byte
+ * aligned; sizes and errors as mxq_route_topk.
  */
 mxq_status mxq_route_topk_bwd(const void* logits, int dtype, int64_t M, int32_t E, int score,
                               const int32_t* expert_ids, int32_t topk, int flags, float scale,
