@@ -361,48 +361,76 @@ def mxq_scaled_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, 
 
 
 # ---------------------------------------------------------------- helpers ---
-# Allocate outputs with torch and call the entry points above.
+# Allocate outputs and workspaces with torch and call the entry points above.  A helper
+# given a stream (a torch stream or a raw handle) runs as it would under
+# `with torch.cuda.stream(stream):`, its allocations included: torch hands out memory that
+# is free in the order of the current stream's work, so a block taken on another stream
+# could still be in use there, and a dropped one be handed out again before this stream
+# is done with it.  The caller orders the stream after the work that makes the inputs.
+
+def _stream_of(stream, t: torch.Tensor) -> torch.cuda.Stream:
+    """`stream` as a torch stream; a raw handle is one of the tensor's device."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    device = t.device if t.is_cuda else None
+    return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+
 
 def quantize_mx(x: torch.Tensor, stream=None):
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, x)):
+            return quantize_mx(x)
     M, K = x.shape
     q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     s = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-    mxq_quantize_mx(x, q, s, stream)
+    mxq_quantize_mx(x, q, s)
     return q, s
 
 
 def dequantize_mx(q: torch.Tensor, s: torch.Tensor, stream=None) -> torch.Tensor:
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, q)):
+            return dequantize_mx(q, s)
     y = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    mxq_dequantize_mx(q, s, y, stream)
+    mxq_dequantize_mx(q, s, y)
     return y
 
 
 def group_scale_fp8(x: torch.Tensor, group_end_offs: torch.Tensor, out_layout: int = MXQ_LAYOUT_ROW,
                     stream=None):
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, x)):
+            return group_scale_fp8(x, group_end_offs, out_layout)
     M, K = x.shape
     G = group_end_offs.numel()
     q = torch.empty((M, K) if out_layout == MXQ_LAYOUT_ROW else (K, M), dtype=torch.uint8, device=x.device)
     scales = torch.empty((G, K), dtype=torch.float32, device=x.device)
     ws = torch.empty(max(mxq_group_scale_workspace_bytes(M, K, G), 16), dtype=torch.uint8, device=x.device)
-    mxq_group_scale_fp8(x, group_end_offs, out_layout, q, scales, ws, stream)
+    mxq_group_scale_fp8(x, group_end_offs, out_layout, q, scales, ws)
     return q, scales
 
 
 def transpose_u8(inp: torch.Tensor, stream=None) -> torch.Tensor:
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, inp)):
+            return transpose_u8(inp)
     R, C = inp.shape
     out = torch.empty((C, R), dtype=torch.uint8, device=inp.device)
-    mxq_transpose_u8(inp, out, stream)
+    mxq_transpose_u8(inp, out)
     return out
 
 
 def scaled_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
                       group_end_offs: torch.Tensor, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, xq)):
+            return scaled_grouped_mm(xq, xs, wq, ws, group_end_offs, out_dtype)
     M, K = xq.shape
     G, N, _ = wq.shape
     y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
     wsp = torch.empty(max(mxq_grouped_mm_workspace_bytes(M, N, K, G), 16), dtype=torch.uint8,
                       device=xq.device)
-    mxq_scaled_grouped_mm(xq, xs, wq, ws, group_end_offs, y, wsp, stream)
+    mxq_scaled_grouped_mm(xq, xs, wq, ws, group_end_offs, y, wsp)
     return y
 
 
@@ -516,6 +544,9 @@ def mxq_add_rmsnorm_bwd(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tenso
 
 def add_rmsnorm(x: torch.Tensor, residual, weight: torch.Tensor, eps: float, stream=None):
     """(h, y, q, s, rstd) of mxq_add_rmsnorm; h is x itself when there is no residual."""
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, x)):
+            return add_rmsnorm(x, residual, weight, eps)
     if x.dim() != 2:
         raise ValueError("x must be 2-D (M, K)")
     M, K = x.shape
@@ -528,21 +559,22 @@ def add_rmsnorm(x: torch.Tensor, residual, weight: torch.Tensor, eps: float, str
     s = x.new_empty((M, K // 32), dtype=torch.uint8)
     rstd = x.new_empty(M, dtype=torch.float32)
     _check(lib().mxq_add_rmsnorm(px, pr, pw, code, M, K, eps, 0 if residual is None else h.data_ptr(), y.data_ptr(),
-                                 q.data_ptr(), s.data_ptr(), rstd.data_ptr(), _stream(stream)), "mxq_add_rmsnorm")
+                                 q.data_ptr(), s.data_ptr(), rstd.data_ptr(), _stream(None)), "mxq_add_rmsnorm")
     return h, y, q, s, rstd
 
 
 def add_rmsnorm_bwd(h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor, dh=None, stream=None):
     """(dx, dweight) of mxq_add_rmsnorm_bwd."""
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, h)):
+            return add_rmsnorm_bwd(h, weight, rstd, dy, dh)
     if h.dim() != 2:
         raise ValueError("h must be 2-D (M, K)")
     M, K = h.shape
     dx = torch.empty_like(h)
     dweight = h.new_empty(K, dtype=torch.float32)
     ws = h.new_empty(max(mxq_add_rmsnorm_bwd_workspace_bytes(M, K), 16), dtype=torch.uint8)
-    mxq_add_rmsnorm_bwd(h, weight, rstd, dy, dh, dx, dweight, ws, stream)
-    if stream is not None:                     # the workspace is not free again before that stream is done with it
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    mxq_add_rmsnorm_bwd(h, weight, rstd, dy, dh, dx, dweight, ws)
     return dx, dweight
 
 
@@ -586,20 +618,26 @@ def route_topk(logits: torch.Tensor, topk: int, bias=None, score: str = "softmax
                topk_groups: int = 1, renormalize: bool = False, group_top2: bool = False, scale: float = 1.0,
                stream=None):
     """(expert_ids, weights), each (M, topk), of mxq_route_topk."""
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, logits)):
+            return route_topk(logits, topk, bias, score, n_groups, topk_groups, renormalize, group_top2, scale)
     M = logits.shape[0]
     ids = logits.new_empty((M, topk), dtype=torch.int32)
     weights = logits.new_empty((M, topk), dtype=torch.float32)
     flags = (MXQ_ROUTE_RENORM if renormalize else 0) | (MXQ_ROUTE_GROUP_TOP2 if group_top2 else 0)
-    mxq_route_topk(logits, bias, SCORES[score], n_groups, topk_groups, flags, scale, ids, weights, stream)
+    mxq_route_topk(logits, bias, SCORES[score], n_groups, topk_groups, flags, scale, ids, weights)
     return ids, weights
 
 
 def route_topk_bwd(logits: torch.Tensor, expert_ids: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
                    renormalize: bool = False, scale: float = 1.0, stream=None) -> torch.Tensor:
     """dlogits of mxq_route_topk_bwd."""
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, logits)):
+            return route_topk_bwd(logits, expert_ids, dweights, score, renormalize, scale)
     dlogits = torch.empty_like(logits)
     mxq_route_topk_bwd(logits, SCORES[score], expert_ids, MXQ_ROUTE_RENORM if renormalize else 0, scale, dweights,
-                       dlogits, stream)
+                       dlogits)
     return dlogits
 
 
@@ -627,16 +665,22 @@ def mxq_dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, y: torch.Tensor, stre
 
 
 def quantize_mxfp4(x: torch.Tensor, rule: int = MXQ_SCALE_FLOOR, stream=None):
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, x)):
+            return quantize_mxfp4(x, rule)
     M, K = x.shape
     q = x.new_empty((M, K // 2), dtype=torch.uint8)
     s = x.new_empty((M, K // 32), dtype=torch.uint8)
-    mxq_quantize_mxfp4(x, rule, q, s, stream)
+    mxq_quantize_mxfp4(x, rule, q, s)
     return q, s
 
 
 def dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, stream=None) -> torch.Tensor:
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, q)):
+            return dequantize_mxfp4(q, s)
     y = q.new_empty((q.shape[0], 2 * q.shape[1]), dtype=torch.bfloat16)
-    mxq_dequantize_mxfp4(q, s, y, stream)
+    mxq_dequantize_mxfp4(q, s, y)
     return y
 
 
@@ -685,8 +729,11 @@ def mxq_mxfp4_grouped_mm_packed(packed: torch.Tensor, wq: torch.Tensor, ws: torc
 def mxfp4_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
                      group_end_offs: torch.Tensor, x_format: int = MXQ_FMT_E4M3, out_dtype=torch.bfloat16,
                      stream=None) -> torch.Tensor:
+    if stream is not None:
+        with torch.cuda.stream(_stream_of(stream, xq)):
+            return mxfp4_grouped_mm(xq, xs, wq, ws, group_end_offs, x_format, out_dtype)
     M = xq.shape[0]
     G, N, half = wq.shape
     y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
-    mxq_mxfp4_grouped_mm(xq, xs, x_format, wq, ws, group_end_offs, y, stream)
+    mxq_mxfp4_grouped_mm(xq, xs, x_format, wq, ws, group_end_offs, y)
     return y
