@@ -81,6 +81,13 @@ __device__ __forceinline__ void sigmoids_of(const float (&l)[N], float (&s)[N])
     }
 }
 
+// A sigmoid's derivative s (1 - s), in a form that does not cancel where s rounds to 1.
+__device__ __forceinline__ float sigmoid_slope(float l)
+{
+    const float e = expf(-fabsf(l)), r = reciprocal_step(1.0f + e);
+    return e * r * r;
+}
+
 // Key and index as one number; doubles of these bits are finite and in their order.
 __device__ __forceinline__ double ranked(uint32_t key, uint32_t id)
 {
@@ -480,7 +487,7 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
             if (L * i < topk && id[i] >= 0) {
                 float d = g[i];
                 if (renorm) d = (d - dot / sum + tiny) / sum;
-                if (SIGMOID) d *= sc[i] * (1.0f - sc[i]);
+                if (SIGMOID) d *= sigmoid_slope(ls[i]);
                 else if (renorm) d *= sc[i] * kept;
                 grad[sub][id[i]] = d;
             }

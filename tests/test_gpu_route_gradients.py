@@ -139,3 +139,34 @@ def test_rows_with_nothing_selected(dtype):
     dw = torch.randn((5, 2), generator=torch.Generator().manual_seed(3)).cuda()
     _, _, _, got = check(l, ids, dw, 1.0, dtype)
     assert (got[:2] == 0).all() and (got[2, 7:] == 0).all()
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["raw", "renorm"])
+@pytest.mark.parametrize("top", [5.0, 12.0, 17.0, 25.0, 60.0])
+def test_sigmoid_of_large_logits(top, renorm):
+    """The slope s (1 - s) of a sigmoid near 1 is exp(-l), not the rounding of 1 - s.
+
+    Its exponential is good to 2^-24 (2 + l / 2) (the exponent's rounding and a few units), the rest to six units: 2^-19 of
+    the slope up to l = 60.  With renormalisation the slope is multiplied by a difference, good to 2^-19 of its terms."""
+    M, E, k = 12, 64, 5
+    g = torch.Generator().manual_seed(int(top))
+    l = (top * (2 * torch.rand((M, E), generator=g) - 1)).cuda()
+    ids, _ = mxq.route_topk(l, k, score="sigmoid")
+    ids[1::2] = E - 1 - ids[1::2] if (ids >= 0).all() else ids[1::2]       # other experts than the largest too
+    dw = torch.randn((M, k), generator=g).cuda()
+    got = f64(mxq.route_topk_bwd(l, ids, dw, score="sigmoid", renormalize=renorm, scale=2.0))
+    L, I, D = f64(l), ids.cpu().numpy().astype(np.int64), 2.0 * f64(dw)
+    x = np.take_along_axis(L, I, 1)
+    e = np.exp(-np.abs(x))
+    slope = e / (1 + e) ** 2
+    u, size = D, np.abs(D)
+    if renorm:
+        s = np.where(x > 0, 1, e) / (1 + e)
+        t = s.sum(-1, keepdims=True) + P.TINY
+        u = (D - (D * s).sum(-1, keepdims=True) / t) / t
+        size = (np.abs(D) + (np.abs(D) * s).sum(-1, keepdims=True) / t) / t
+    tol = slope * (2.0 ** -19 * np.abs(u) + (2.0 ** -19 * size if renorm else 0))
+    assert np.all(np.abs(np.take_along_axis(got, I, 1) - slope * u) <= tol + 1e-36)
+    other = np.ones((M, E), bool)
+    np.put_along_axis(other, I, False, 1)
+    assert (got[other] == 0).all()
