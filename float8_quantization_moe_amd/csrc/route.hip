@@ -425,7 +425,7 @@ void route_topk_bwd_kernel(const void* __restrict__ logits, const int32_t* __res
                     sum += p[j][c];
                 }
             total = lanes_sum<L>(sum);
-            total = total > 0.0f ? total : 1.0f;
+            total = total == 0.0f ? 1.0f : total;                 // (a NaN stays: the whole row's gradient is NaN)
         }
         const float unit = 1.0f / total;                          // (one rounding more than dividing: 2^-24 of the value)
         for (int e = lane; e < kMaxE; e += L) grad[sub][e] = 0.0f;

@@ -526,8 +526,10 @@ mxq_status mxq_route_topk(const void* logits, int dtype, int64_t M, int32_t E, c
  * sigmoid only the selected logits get one; every other value of dlogits is
  * written as zero.  With softmax every logit gets one; with MXQ_ROUTE_RENORM that
  * of the others is about 1e-20 of the weights' unless the selected scores are as
- * small as the 1e-20 of the forward's divisor.  logits and dlogits 16-byte
- * aligned; sizes and errors as mxq_route_topk.
+ * small as the 1e-20 of the forward's divisor.  A row that holds a NaN or +inf has
+ * a gradient of NaN with softmax; sigmoid reads the selected logits only, and others
+ * do not show.  logits and dlogits 16-byte aligned; sizes and errors as
+ * mxq_route_topk.
  */
 mxq_status mxq_route_topk_bwd(const void* logits, int dtype, int64_t M, int32_t E, int score,
                               const int32_t* expert_ids, int32_t topk, int flags, float scale,

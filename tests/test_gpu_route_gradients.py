@@ -170,3 +170,27 @@ def test_sigmoid_of_large_logits(top, renorm):
     other = np.ones((M, E), bool)
     np.put_along_axis(other, I, False, 1)
     assert (got[other] == 0).all()
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["raw", "renorm"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E", [5, 40, 128, 250, 300, 1000])
+def test_a_row_with_nan_or_infinity_has_a_gradient_of_nan(E, dtype, renorm):
+    """As its weights are; the rows beside it, which share its wave, are as without it."""
+    M, k = 21, 3
+    l = torch.randn((M, E), generator=torch.Generator().manual_seed(E)).to(DT[dtype]).cuda()
+    ids, _ = mxq.route_topk(l, k)
+    dw = torch.randn((M, k), generator=torch.Generator().manual_seed(1)).cuda()
+    want = mxq.route_topk_bwd(l, ids, dw, renormalize=renorm)
+    bad = l.clone()
+    bad[3, E - 1] = float("nan")                         # (of an expert that need not be selected)
+    bad[8, 0] = float("inf")
+    bad[13] = float("nan")
+    bad[14, 1:] = -float("inf")                          # no fault: a row with one expert left
+    got = mxq.route_topk_bwd(bad, ids, dw, renormalize=renorm)
+    for r in (3, 8, 13):
+        assert torch.isnan(got[r]).all()
+        assert torch.isnan(mxq.route_topk(bad, k, renormalize=renorm)[1][r]).all()
+    assert torch.isfinite(got[14]).all()
+    rest = [r for r in range(M) if r not in (3, 8, 13, 14)]
+    assert torch.equal(got[rest], want[rest])
