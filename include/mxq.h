@@ -568,11 +568,14 @@ mxq_status mxq_dequantize_mxfp4(const void* q_e2m1, const void* s_e8m0, int64_t 
  *   wq_e2m1  (G, N, K/2) E2M1 codes and ws_e8m0 (G, N, K/32) scales
  *            (mxq_quantize_mxfp4 of the (G*N, K) weight).
  * Offsets, clamping, zero rows past the last end, out_dtype, alignment and
- * errors as mxq_scaled_grouped_mm; it needs no workspace.  The matrix cores sum the exact products of a
- * block; with E4M3 tokens products far below a block's largest (2^-14 and less of
- * it) are cut off there, with E2M1 tokens a block's sum is exact; blocks are added
- * in fp32 and the result is rounded once.  NaN codes and scale 0xFF are outside
- * the contract.  Weights are constants of a serving program: there is no backward.
+ * errors as mxq_scaled_grouped_mm; it needs no workspace.  The matrix cores sum
+ * the exact products of a block; with E4M3 tokens products far below a block's
+ * largest (2^-14 and less of it) are cut off there, with E2M1 tokens a block's sum
+ * is exact; blocks are added in fp32 and the result is rounded once.  A token row
+ * with a scale of 0xFF or an E4M3 NaN code, as the quantizers write for Inf and NaN,
+ * gives a row of NaN, a weight row with a scale of 0xFF a column of NaN in its
+ * group's rows; nothing else changes.  Weights are constants of a serving program:
+ * there is no backward.
  *
  * Requires K > 0, K % 128 == 0, K <= 2^22, N % 8 == 0, 0 <= M, N <= 2^31 - 1024,
  * 1 <= G <= 4095 and a tile list of fewer than 2^30 entries (MXQ_ERR_SHAPE);
