@@ -131,11 +131,6 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v)
 {
     return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
-template <int L>
-__device__ __forceinline__ uint32_t lanes_min(uint32_t v)
-{
-    return lanes_reduce<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-}
 
 // --------------------------------------------- 8 values of bf16 or fp32 --
 // kBytes of one value; load8 / store8 move values 8i .. 8i+7 of a row.

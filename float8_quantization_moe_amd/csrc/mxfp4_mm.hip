@@ -19,8 +19,10 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u_dword __attribute__((ext_vector_type(4), aligned(4)));   // 16 bytes at a multiple of 4
 
 // From this many rows on the tile kernel takes a call.  This kernel passes over a group's
-// weights once for every 16 rows, so what decides is the largest group; the tile kernel
-// takes 10 us and more however few the rows, which counts where the experts are small.
+// weights once for every 16 rows, so the largest group would decide, but its rows are known
+// on the device only: the rule goes by all rows, and a call whose rows are mostly one
+// group's takes longer here than it need.  The tile kernel takes 10 us and more however few
+// the rows, which counts where the experts are small.
 // Measured (uneven groups; MXFP8 tokens, this kernel / the tile kernel, us):
 //   8192 x 5120   1 group, 64 rows 25 / 25, 96 rows 37 / 25; 16 groups, 96 rows 73 / 77, 128 rows 84 / 77
 //   4096 x 4096   4 groups, 72 rows 19 / 23, 100 rows 23 / 23; 8 groups, 72 rows 24 / 24

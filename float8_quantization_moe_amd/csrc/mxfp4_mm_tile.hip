@@ -10,8 +10,8 @@
 // A slot is four MFMA steps of 64 k; a step's operands are read from LDS during the step
 // before it.  With one wave a SIMD nothing issues while a load or an LDS read waits for
 // its pipe, so both are spread between the MFMAs, one or two after each (`mfmas`).
-// Measured, E4M3 / E2M1: one group of 16384 x 8192 x 5120 485 / 325 us (2.8 / 4.2 PFLOP/s), 16640
-// rows in 16 ragged groups 565 / 394.  What bounds it is the clock under this power (on
+// Measured, E4M3 / E2M1: one group of 16384 x 8192 x 5120 480 / 328 us (2.9 / 4.2 PFLOP/s), 16640
+// rows in 16 ragged groups 553 / 393.  What bounds it is the clock under this power (on
 // zeros 370 / 244 us) and the load path; eight waves of 128 x 64, two a SIMD, took 485 / 333.
 //
 // The slots of successive tiles form one stream: the loads run ahead of the
@@ -109,7 +109,9 @@ __device__ __forceinline__ v4i resource(const void* base, uint32_t bytes)
 // its own before later LDS reads.  Nor does it add the wait states that such a load
 // needs inside an asm block: one after M0 is written, and five after a vector
 // instruction (a v_readlane that fetches a spilled resource) has written a scalar
-// register that the load reads.  s_mov and s_nop WAIT are WAIT + 2 of them.
+// register that the load reads.  s_mov and s_nop WAIT are WAIT + 2 of them.  Scales,
+// whose resources the compiler spills, take all five; five at every load took 1 % longer
+// (16640 rows in 16 groups 558 / 396 us against 553 / 393).  A test reads the assembly.
 template <int WAIT = 0>
 __device__ __forceinline__ void load_to_lds(const v4i& srd, uint32_t lds, uint32_t voff)
 {

@@ -6,7 +6,8 @@
 //                         residual stream that the next layer reads, so the norm
 //                         is that of the stored h and the backward pass needs
 //                         nothing else);
-//   rstd = 1 / sqrt(mean(h^2) + eps)        fp32 throughout;
+//   rstd = 1 / sqrt(mean(h^2) + eps)        the sum in fp32, the rest in doubles,
+//                         rounded once;
 //   y = h * rstd * w      rounded once to the stored type;
 //   q, s = the MXFP8 encoding of y rounded to bf16: the bytes mxq_quantize_mx
 //          writes for y, so that the fused call replaces the two calls bit for bit.
@@ -18,8 +19,8 @@
 // Both are HBM bound (a few operations a value): the row is read once and held in
 // registers between its reduction and its use, LANES threads a row with C chunks
 // of 8 values each.  65536 x 5120 bf16 with every output: 512 us, 5.9 TB/s; backward of
-// 16640 x 5120 with dh: 119 us, 5.7 TB/s.  The sum of a row is one fp32 tree in a fixed order, so
-// results are reproducible.
+// 16640 x 5120 with dh: 119 us, 5.7 TB/s.  The sum of a row is eight short chains a lane and one
+// tree, in a fixed order, so results are reproducible.
 #include "device_common.hpp"
 #include "internal.hpp"
 #include "mx_block.hpp"
@@ -265,8 +266,9 @@ void dweight_kernel(const float* __restrict__ part, int rows, int K, float* __re
 
 constexpr int kNormMaxGrid = 1 << 22;
 // Workgroups of the backward pass at most, and so parts of dw: two a CU, which are
-// resident together (16640 x 5120: 256 / 512 / 768 / 1024 took 147 / 119 / 129 / 134 us;
-// 16640 x 1024: 512 / 1024 / 2048 25.4 / 27.5 / 31.0).
+// resident together up to K = 8192 (16640 x 5120: 256 / 512 / 768 / 1024 took 147 / 119 / 129 /
+// 134 us; 16640 x 1024: 512 / 1024 / 2048 25.4 / 27.5 / 31.0).  Longer rows need more than half
+// of the registers, so that the second half runs after the first; not timed apart.
 constexpr int kBwdParts = 512;
 // Up to this many rows for each of a workgroup's row slots one workgroup takes them all, and
 // dw is its part: no second launch (1 to 16 rows, 64 to 5120 values: 12.3 us a call against

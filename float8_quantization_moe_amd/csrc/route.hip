@@ -385,6 +385,9 @@ void route_topk_kernel(const void* __restrict__ logits, const float* __restrict_
 //          - s_e m (S / D) (1e-20 / D).
 // That is q's own gradient unless S is as small as 1e-20, which takes a bias or groups
 // that keep a row's large logits out.
+// Bound by a row's dependent steps rather than its bytes: 65536 x 64 bf16, top-6, softmax
+// 8.0 us (bytes 3.4), renormalised 8.7; 65536 x 128 fp32, top-8, renormalised softmax 15.8
+// (11.4), sigmoid 12.0.
 // Same layout as the forward, rows are the work of single waves; the selected experts'
 // g pass through LDS.
 template <bool F32L, bool SIGMOID, int L, int C>

@@ -456,7 +456,8 @@ mxq_status mxq_scaled_grouped_mm_packed(const void* packed, const void* wq_e4m3,
  *
  * The norm is that of the stored (rounded) h, so mxq_add_rmsnorm_bwd needs only h
  * and rstd.  Squares are summed in fp32: a row whose sum of squares passes the
- * largest fp32 value comes out as zeros.  A NaN or Inf in a row makes the row NaN
+ * largest fp32 value comes out as zeros, and with eps = 0 one whose squares all
+ * fall below the smallest as infinities.  A NaN or Inf in a row makes the row NaN
  * (scales 0xFF).  h and y may each be x or residual themselves (in place), not
  * one another, and overlap nothing else.
  *
@@ -479,6 +480,7 @@ mxq_status mxq_add_rmsnorm(const void* x, const void* residual, const void* weig
  * dx may be dy or dh itself (in place).  Sizes and errors as mxq_add_rmsnorm
  * without q; M == 0 writes a zero dweight.  The workspace holds the rows' parts
  * of dweight; it needs no initialisation, and two calls in flight must not share it.
+ * (It is required for few rows too, which leave it untouched.)
  */
 size_t mxq_add_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
 mxq_status mxq_add_rmsnorm_bwd(const void* h, const void* weight, const float* rstd, const void* dy,
