@@ -457,9 +457,10 @@ mxq_status mxq_scaled_grouped_mm_packed(const void* packed, const void* wq_e4m3,
  * The norm is that of the stored (rounded) h, so mxq_add_rmsnorm_bwd needs only h
  * and rstd.  Squares are summed in fp32: a row whose sum of squares passes the
  * largest fp32 value comes out as zeros, and with eps = 0 one whose squares all
- * fall below the smallest as infinities.  A NaN or Inf in a row makes the row NaN
- * (scales 0xFF).  h and y may each be x or residual themselves (in place), not
- * one another, and overlap nothing else.
+ * fall below the smallest as infinities.  A NaN in h makes the row NaN
+ * (scales 0xFF); an Inf, whose rstd is 0, makes itself and its block of codes NaN
+ * and the row's finite values zeros.  h and y may each be x or residual themselves
+ * (in place), not one another, and overlap nothing else.
  *
  * Requires K % 8 == 0 (K % 32 == 0 with q), K <= 16384, M*K <= 2^40
  * (MXQ_ERR_SHAPE); eps >= 0 (MXQ_ERR_RULE).  Tensors 16-byte aligned, rstd 4-byte.

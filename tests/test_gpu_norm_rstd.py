@@ -25,3 +25,20 @@ def test_rstd(M, K, eps, dtype):
     C = -(-K // 8 // (64 if K <= 2048 else 256))
     bound = ((C + 12) / 2 + 1) * 2.0 ** -24
     assert np.all(np.abs(rstd.double().cpu().numpy() - want) <= bound * want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("K", [64, 2048, 5120])
+def test_nan_and_infinity_as_the_formula_has_them(K, dtype):
+    """rstd is NaN, or 0: a row with NaN is NaN; one with an infinity is 0, and inf * 0 where it stands."""
+    x = torch.randn((4, K), generator=torch.Generator().manual_seed(K)).to(dtype).cuda()
+    r = torch.zeros_like(x)
+    x[0, K - 1] = float("nan")
+    x[1, 33], x[3, 0], r[3, 0] = -float("inf"), float("inf"), -float("inf")          # (the last sum is NaN)
+    h, y, q, s, rstd = mxq.add_rmsnorm(x, r, torch.ones(K, dtype=dtype, device="cuda"), 1e-5)
+    for row in (0, 3):
+        assert torch.isnan(y[row]).all() and (s[row] == 255).all() and (q[row] == 0x7F).all() and torch.isnan(rstd[row])
+    at = torch.arange(K, device="cuda") == 33
+    assert torch.equal(torch.isnan(y[1]), at) and (y[1][~at] == 0).all() and rstd[1] == 0
+    assert torch.equal(s[1] == 255, torch.arange(K // 32, device="cuda") == 1)
+    assert torch.isfinite(y[2]).all()
