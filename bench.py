@@ -96,7 +96,7 @@ def parse_args():
     return p.parse_args()
 
 
-COUNTER_SOURCES = ["mx_codec.hip", "mx_dim0.hip", "device_common.hpp"]
+COUNTER_SOURCES = ["mx_codec.hip", "mx_dim0.hip", "mx_block.hpp", "device_common.hpp"]
 # Legs beside the step: NEXT-row variants, the group-scaling sweep over 16-128
 # groups, the MX codec at the token shape, group scaling beside streaming copies,
 # and the grouped GEMM.
