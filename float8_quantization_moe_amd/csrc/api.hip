@@ -11,6 +11,7 @@ namespace {
 thread_local int g_last_hip_error = 0;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // Largest element count accepted by the flat kernels (keeps every index in range
 // of 64-bit arithmetic with a wide margin; 2^40 elements is 2 TB of bf16).
@@ -284,7 +285,7 @@ mxq_status mxq_dispatch_pack_mx(const void* x_bf16, int64_t M, int64_t K, const 
                   ((uintptr_t)src_pair & 3u) != 0))
         return MXQ_ERR_ALIGN;
     if (workspace_bytes < mxq::dispatch_workspace_bytes(M * topk, E)) return MXQ_ERR_WORKSPACE;
-    hipError_t e = mxq::launch_dispatch_order(expert_ids, M * topk, E, src_pair, group_end_offs, workspace,
+    hipError_t e = mxq::launch_dispatch_order(expert_ids, M * topk, E, src_pair, nullptr, group_end_offs, workspace,
                                               (hipStream_t)stream);
     if (e == hipSuccess)
         e = mxq::launch_mx_dispatch_pack(x_bf16, K, src_pair, topk, group_end_offs, E, packed, M * topk,
@@ -486,6 +487,191 @@ mxq_status mxq_route_topk_bwd(const void* logits, int dtype, int64_t M, int32_t 
     return hip_status(mxq::launch_route_topk_bwd(logits, dtype == MXQ_OUT_F32, M, E, score == MXQ_SCORE_SIGMOID,
                                                  expert_ids, topk, (flags & MXQ_ROUTE_RENORM) != 0, scale, dweights,
                                                  dlogits, (hipStream_t)stream));
+}
+
+// ------------------------------------------------------------- layer norm ---
+mxq_status mxq_add_layernorm(const void* x, const void* residual, const void* weight, const void* bias, int dtype,
+                             int64_t M, int64_t K, float eps, void* h, void* y, void* q_e4m3, void* s_e8m0,
+                             float* mean, float* rstd, void* stream)
+{
+    const mxq_status st = check_norm(M, K, dtype, q_e4m3 != nullptr || s_e8m0 != nullptr);
+    if (st != MXQ_OK) return st;
+    if (!(eps >= 0.0f)) return MXQ_ERR_RULE;
+    if (M == 0 || K == 0) return MXQ_OK;
+    if (!x || !weight || (!y && !q_e4m3) || (q_e4m3 == nullptr) != (s_e8m0 == nullptr)) return MXQ_ERR_NULL;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(bias) || !aligned16(h) ||
+        !aligned16(y) || !aligned16(q_e4m3) || !aligned16(s_e8m0) || !aligned4(mean) || !aligned4(rstd))
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_add_layernorm(x, residual, weight, bias, dtype == MXQ_OUT_F32, M, K, eps, h, y, q_e4m3,
+                                                s_e8m0, mean, rstd, (hipStream_t)stream));
+}
+
+size_t mxq_add_layernorm_bwd_workspace_bytes(int64_t M, int64_t K)
+{
+    if (check_norm(M, K, MXQ_OUT_BF16, false) != MXQ_OK) return 0;
+    return mxq::add_layernorm_bwd_workspace_bytes(M, K);
+}
+
+mxq_status mxq_add_layernorm_bwd(const void* h, const void* weight, const float* mean, const float* rstd,
+                                 const void* dy, const void* dh, int dtype, int64_t M, int64_t K, void* dx,
+                                 float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const mxq_status st = check_norm(M, K, dtype, false);
+    if (st != MXQ_OK) return st;
+    if (K == 0) return MXQ_OK;
+    if (!dweight || (M > 0 && (!h || !weight || !mean || !rstd || !dy || !dx))) return MXQ_ERR_NULL;
+    if (!aligned16(dweight) || !aligned16(dbias) ||
+        (M > 0 && (!aligned16(h) || !aligned16(weight) || !aligned16(dy) || !aligned16(dh) || !aligned16(dx) ||
+                   !aligned4(mean) || !aligned4(rstd))))
+        return MXQ_ERR_ALIGN;
+    if (M > 0 && (!workspace || workspace_bytes < mxq::add_layernorm_bwd_workspace_bytes(M, K)))
+        return MXQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_add_layernorm_bwd(h, weight, mean, rstd, dy, dh, dtype == MXQ_OUT_F32, M, K, dx, dweight,
+                                                    dbias, workspace, (hipStream_t)stream));
+}
+
+// -------------------------------------------- rows to the experts and back ---
+static mxq_status check_pairs(int64_t M, int64_t K, int64_t topk, int dtype)
+{
+    const mxq_status st = check_2d(M, K);
+    if (st != MXQ_OK) return st;
+    if (K % 8 != 0 || K > ((int64_t)1 << 23) || topk < 1 || topk > 64) return MXQ_ERR_SHAPE;
+    if (M >= (int64_t)1 << 31 || M * topk >= ((int64_t)1 << 31) - 256) return MXQ_ERR_SHAPE;
+    if (dtype != MXQ_OUT_BF16 && dtype != MXQ_OUT_F32) return MXQ_ERR_DTYPE;
+    return MXQ_OK;
+}
+
+static mxq_status check_dispatch_rows(int64_t M, int64_t K, int64_t topk, int64_t E, int dtype)
+{
+    const mxq_status st = check_pairs(M, K, topk, dtype);
+    if (st == MXQ_ERR_SHAPE) return st;
+    if (K == 0 || E < 1 || E > mxq::dispatch_max_experts()) return MXQ_ERR_SHAPE;
+    if ((M * topk + 255) / 256 * E >= ((int64_t)1 << 31) || M * topk > kMaxElems / K) return MXQ_ERR_SHAPE;
+    return st;
+}
+
+size_t mxq_dispatch_rows_workspace_bytes(int64_t M, int32_t topk, int32_t E)
+{
+    if (check_dispatch_rows(M, 8, topk, E, MXQ_OUT_BF16) != MXQ_OK) return 0;
+    return mxq::dispatch_workspace_bytes(M * topk, E);
+}
+
+mxq_status mxq_dispatch_rows(const void* x, int dtype, int64_t M, int64_t K, const int32_t* expert_ids, int32_t topk,
+                             int32_t E, void* rows, int32_t* group_end_offs, int32_t* src_pair, int32_t* pair_row,
+                             void* workspace, size_t workspace_bytes, void* stream)
+{
+    const mxq_status st = check_dispatch_rows(M, K, topk, E, dtype);
+    if (st != MXQ_OK) return st;
+    if (!group_end_offs || !workspace) return !group_end_offs ? MXQ_ERR_NULL : MXQ_ERR_WORKSPACE;
+    if (M > 0 && (!x || !expert_ids || !rows || !src_pair || !pair_row)) return MXQ_ERR_NULL;
+    if (!aligned4(group_end_offs) || !aligned16(workspace)) return MXQ_ERR_ALIGN;
+    if (M > 0 && (!aligned16(x) || !aligned16(rows) || !aligned4(expert_ids) || !aligned4(src_pair) || !aligned4(pair_row)))
+        return MXQ_ERR_ALIGN;
+    if (workspace_bytes < mxq::dispatch_workspace_bytes(M * topk, E)) return MXQ_ERR_WORKSPACE;
+    hipError_t e = mxq::launch_dispatch_order(expert_ids, M * topk, E, src_pair, pair_row, group_end_offs, workspace,
+                                              (hipStream_t)stream);
+    if (e == hipSuccess && M > 0)
+        e = mxq::launch_dispatch_rows(x, K * (dtype == MXQ_OUT_F32 ? 4 : 2), M, topk, pair_row, group_end_offs, E, rows,
+                                      src_pair, (hipStream_t)stream);
+    return hip_status(e);
+}
+
+mxq_status mxq_pair_rows(const int32_t* src_pair, int64_t pairs, int32_t* pair_row, void* stream)
+{
+    if (pairs < 0 || pairs >= ((int64_t)1 << 31) - 256) return MXQ_ERR_SHAPE;
+    if (pairs == 0) return MXQ_OK;
+    if (!src_pair || !pair_row) return MXQ_ERR_NULL;
+    if (!aligned4(src_pair) || !aligned4(pair_row)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_pair_rows(src_pair, pairs, pair_row, (hipStream_t)stream));
+}
+
+static mxq_status check_combine(int64_t R, int64_t K, int64_t M, int64_t topk, int dtype)
+{
+    const mxq_status st = check_pairs(M, K, topk, dtype);
+    if (st == MXQ_ERR_SHAPE || check_2d(R, K) != MXQ_OK || R >= (int64_t)1 << 31) return MXQ_ERR_SHAPE;
+    return st;
+}
+
+mxq_status mxq_combine_rows(const void* rows, int dtype, int64_t R, int64_t K, const int32_t* pair_row, int64_t M,
+                            int32_t topk, const float* weights, void* out, void* stream)
+{
+    const mxq_status st = check_combine(R, K, M, topk, dtype);
+    if (st != MXQ_OK) return st;
+    if (M == 0 || K == 0) return MXQ_OK;
+    if ((!rows && R > 0) || !pair_row || !out) return MXQ_ERR_NULL;
+    if (!aligned16(rows) || !aligned16(out) || !aligned4(pair_row) || !aligned4(weights)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_combine_rows(rows, dtype == MXQ_OUT_F32, R, K, pair_row, M, topk, weights, out,
+                                               (hipStream_t)stream));
+}
+
+mxq_status mxq_combine_rows_bwd(const void* dout, const void* rows, int dtype, int64_t R, int64_t K,
+                                const int32_t* pair_row, int64_t M, int32_t topk, const float* weights, void* drows,
+                                float* dweights, void* stream)
+{
+    const mxq_status st = check_combine(R, K, M, topk, dtype);
+    if (st != MXQ_OK) return st;
+    if (M == 0 || (K == 0 && !dweights)) return MXQ_OK;
+    if (!pair_row || (K > 0 && (!dout || (R > 0 && (!drows || (!rows && dweights)))))) return MXQ_ERR_NULL;
+    if (!aligned16(dout) || !aligned16(rows) || !aligned16(drows) || !aligned4(pair_row) || !aligned4(weights) ||
+        !aligned4(dweights))
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_combine_rows_bwd(dout, rows, dtype == MXQ_OUT_F32, R, K, pair_row, M, topk, weights, drows,
+                                                   dweights, (hipStream_t)stream));
+}
+
+// ------------------------------------------------ grouped products in bf16 ---
+static mxq_status check_bf16_mm_sizes(int product, int64_t M, int64_t N, int64_t K, int64_t G)
+{
+    return mxq::bf16_mm_sizes_ok(product, M, N, K, G) ? MXQ_OK : MXQ_ERR_SHAPE;
+}
+
+size_t mxq_bf16_grouped_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int32_t G)
+{
+    if (product != MXQ_PRODUCT_Y && product != MXQ_PRODUCT_DX && product != MXQ_PRODUCT_DW) return 0;
+    if (check_bf16_mm_sizes(product, M, N, K, G) != MXQ_OK) return 0;
+    return mxq::bf16_mm_workspace_bytes(product, M, N, K, G);
+}
+
+static mxq_status bf16_mm(int product, const void* rows, const void* other, const int32_t* offs, int64_t M, int64_t N,
+                          int64_t K, int32_t G, int out_dtype, int accumulate, void* out, void* workspace,
+                          size_t workspace_bytes, void* stream)
+{
+    const mxq_status st = check_bf16_mm_sizes(product, M, N, K, G);
+    if (st != MXQ_OK) return st;
+    if (out_dtype != MXQ_OUT_BF16 && out_dtype != MXQ_OUT_F32) return MXQ_ERR_DTYPE;
+    if (accumulate != 0 && accumulate != 1) return MXQ_ERR_RULE;
+    if (accumulate && out_dtype != MXQ_OUT_F32) return MXQ_ERR_DTYPE;
+    if (M == 0 && (product != MXQ_PRODUCT_DW || accumulate)) return MXQ_OK;
+    if (!offs || !out || (M > 0 && !rows) || ((M > 0 || product != MXQ_PRODUCT_DW) && !other)) return MXQ_ERR_NULL;
+    if (!aligned16(rows) || !aligned16(other) || !aligned16(out) || !aligned4(offs)) return MXQ_ERR_ALIGN;
+    const size_t need = mxq::bf16_mm_workspace_bytes(product, M, N, K, G);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MXQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_bf16_mm(product, rows, other, offs, (int)M, (int)N, (int)K, (int)G, out,
+                                          out_dtype == MXQ_OUT_F32, accumulate != 0, workspace, (hipStream_t)stream));
+}
+
+mxq_status mxq_bf16_grouped_mm(const void* x, const void* w, const int32_t* group_end_offs, int64_t M, int64_t N,
+                               int64_t K, int32_t G, int out_dtype, void* y, void* workspace, size_t workspace_bytes,
+                               void* stream)
+{
+    return bf16_mm(MXQ_PRODUCT_Y, x, w, group_end_offs, M, N, K, G, out_dtype, 0, y, workspace, workspace_bytes, stream);
+}
+
+mxq_status mxq_bf16_grouped_mm_dx(const void* dy, const void* w, const int32_t* group_end_offs, int64_t M, int64_t N,
+                                  int64_t K, int32_t G, int out_dtype, void* dx, void* workspace,
+                                  size_t workspace_bytes, void* stream)
+{
+    return bf16_mm(MXQ_PRODUCT_DX, dy, w, group_end_offs, M, N, K, G, out_dtype, 0, dx, workspace, workspace_bytes, stream);
+}
+
+mxq_status mxq_bf16_grouped_mm_dw(const void* dy, const void* x, const int32_t* group_end_offs, int64_t M, int64_t N,
+                                  int64_t K, int32_t G, int out_dtype, int accumulate, void* dw, void* workspace,
+                                  size_t workspace_bytes, void* stream)
+{
+    return bf16_mm(MXQ_PRODUCT_DW, dy, x, group_end_offs, M, N, K, G, out_dtype, accumulate, dw, workspace, workspace_bytes,
+                   stream);
 }
 
 }  // extern "C"

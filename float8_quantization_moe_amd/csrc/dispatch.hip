@@ -18,7 +18,8 @@
 // workgroup derives its block's first rows from the whole table), which saves
 // the one-workgroup launch.
 // The rows themselves (gather + MX quantize + pack) are written by
-// mx_dispatch_pack_kernel in mx_codec.hip.
+// mx_dispatch_pack_kernel in mx_codec.hip, as they are by rows.hip, which also takes the
+// row of each pair (pair_row, the inverse of src_pair; null where nobody asks for it).
 #include "device_common.hpp"
 #include "internal.hpp"
 
@@ -128,14 +129,16 @@ void dp_scan_kernel(int32_t* __restrict__ bcount, int nblk, int E, int32_t* __re
 
 __global__ __launch_bounds__(kDpThreads)
 void dp_place_kernel(const int32_t* __restrict__ ids, int64_t P, int E, const int32_t* __restrict__ bbase,
-                     int32_t* __restrict__ src_pair)
+                     int32_t* __restrict__ src_pair, int32_t* __restrict__ pair_row)
 {
     __shared__ int wcnt[kDpWaves * kDpMaxExperts];
     const int64_t p = (int64_t)blockIdx.x * kDpThreads + threadIdx.x;
     int e = p < P ? ids[p] : -1;
     e = (e >= 0 && e < E) ? e : -1;
     const int rank = rank_in_block(e, E, id_bits(E), wcnt);
-    if (e >= 0) src_pair[bbase[(int64_t)blockIdx.x * E + e] + rank] = (int32_t)p;
+    const int row = e >= 0 ? bbase[(int64_t)blockIdx.x * E + e] + rank : -1;
+    if (e >= 0) src_pair[row] = (int32_t)p;
+    if (pair_row && p < P) pair_row[p] = row;
 }
 
 // Scan folded into the place pass, for small tables (nblk * E <= kDpFoldMax,
@@ -149,7 +152,7 @@ constexpr int kDpFoldMax = 16384;
 __global__ __launch_bounds__(kDpThreads)
 void dp_place_scan_kernel(const int32_t* __restrict__ ids, int64_t P, int E, int nblk,
                           const int32_t* __restrict__ bcount, int32_t* __restrict__ src_pair,
-                          int32_t* __restrict__ group_end)
+                          int32_t* __restrict__ pair_row, int32_t* __restrict__ group_end)
 {
     __shared__ int tot[kDpThreads], pre[kDpThreads], start[kDpThreads];
     __shared__ int wcnt[kDpWaves * kDpThreads];
@@ -192,7 +195,9 @@ void dp_place_scan_kernel(const int32_t* __restrict__ ids, int64_t P, int E, int
     int e = p < P ? ids[p] : -1;
     e = (e >= 0 && e < E) ? e : -1;
     const int rank = rank_in_block(e, E, id_bits(E), wcnt);
-    if (e >= 0) src_pair[start[e] - tot[e] + pre[e] + rank] = (int32_t)p;
+    const int row = e >= 0 ? start[e] - tot[e] + pre[e] + rank : -1;
+    if (e >= 0) src_pair[row] = (int32_t)p;
+    if (pair_row && p < P) pair_row[p] = row;
 }
 
 int dispatch_max_experts() { return kDpMaxExperts; }
@@ -203,8 +208,8 @@ size_t dispatch_workspace_bytes(int64_t P, int32_t E)
     return (size_t)(nblk > 0 ? nblk : 1) * (size_t)E * 4u;
 }
 
-hipError_t launch_dispatch_order(const int32_t* ids, int64_t P, int E, int32_t* src_pair, int32_t* group_end,
-                                 void* workspace, hipStream_t stream)
+hipError_t launch_dispatch_order(const int32_t* ids, int64_t P, int E, int32_t* src_pair, int32_t* pair_row,
+                                 int32_t* group_end, void* workspace, hipStream_t stream)
 {
     int32_t* bcount = static_cast<int32_t*>(workspace);
     const int nblk = (int)((P + kDpThreads - 1) / kDpThreads);
@@ -213,13 +218,13 @@ hipError_t launch_dispatch_order(const int32_t* ids, int64_t P, int E, int32_t* 
     }
     if (nblk > 0 && E <= kDpThreads && (int64_t)nblk * E <= kDpFoldMax) {
         hipLaunchKernelGGL(dp_place_scan_kernel, dim3((unsigned)nblk), dim3(kDpThreads), 0, stream, ids, P, E, nblk,
-                           (const int32_t*)bcount, src_pair, group_end);
+                           (const int32_t*)bcount, src_pair, pair_row, group_end);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(dp_scan_kernel, dim3(1), dim3(kDpScanThreads), 0, stream, bcount, nblk, E, group_end);
     if (nblk > 0) {
         hipLaunchKernelGGL(dp_place_kernel, dim3((unsigned)nblk), dim3(kDpThreads), 0, stream, ids, P, E,
-                           (const int32_t*)bcount, src_pair);
+                           (const int32_t*)bcount, src_pair, pair_row);
     }
     return hipGetLastError();
 }

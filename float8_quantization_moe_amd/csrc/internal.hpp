@@ -13,8 +13,9 @@ hipError_t launch_mx_dispatch_pack(const void* x, int64_t K, int32_t* src_pair, 
                                    int E, void* packed, int64_t nrows, hipStream_t stream);
 int dispatch_max_experts();
 size_t dispatch_workspace_bytes(int64_t P, int32_t E);
-hipError_t launch_dispatch_order(const int32_t* ids, int64_t P, int E, int32_t* src_pair, int32_t* group_end,
-                                 void* workspace, hipStream_t stream);
+// pair_row may be null.
+hipError_t launch_dispatch_order(const int32_t* ids, int64_t P, int E, int32_t* src_pair, int32_t* pair_row,
+                                 int32_t* group_end, void* workspace, hipStream_t stream);
 hipError_t launch_mx_quantize_dim0(const void* x, int64_t M, int64_t K, void* q, void* s, bool rceil,
                                    hipStream_t stream);
 hipError_t launch_mx_dequantize_dim0(const void* q, const void* s, int64_t M, int64_t K, void* y,
@@ -74,6 +75,30 @@ size_t add_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
 hipError_t launch_add_rmsnorm_bwd(const void* h, const void* w, const float* rstd, const void* dy, const void* dh,
                                   bool f32, int64_t M, int64_t K, void* dx, float* dw, void* workspace,
                                   hipStream_t stream);
+
+// Layer norm, in the norm's sizes.
+hipError_t launch_add_layernorm(const void* x, const void* r, const void* w, const void* b, bool f32, int64_t M, int64_t K,
+                                float eps, void* h, void* y, void* q, void* s, float* mean, float* rstd, hipStream_t stream);
+size_t add_layernorm_bwd_workspace_bytes(int64_t M, int64_t K);
+hipError_t launch_add_layernorm_bwd(const void* h, const void* w, const float* mean, const float* rstd, const void* dy,
+                                    const void* dh, bool f32, int64_t M, int64_t K, void* dx, float* dw, float* db,
+                                    void* workspace, hipStream_t stream);
+
+// Rows to their experts and back; row_bytes is a multiple of 16.
+hipError_t launch_dispatch_rows(const void* x, int64_t row_bytes, int64_t M, int topk, const int32_t* pair_row,
+                                const int32_t* group_end, int E, void* rows, int32_t* src_pair, hipStream_t stream);
+hipError_t launch_pair_rows(const int32_t* src_pair, int64_t pairs, int32_t* pair_row, hipStream_t stream);
+hipError_t launch_combine_rows(const void* rows, bool f32, int64_t R, int64_t K, const int32_t* pair_row, int64_t M, int topk,
+                               const float* weights, void* out, hipStream_t stream);
+hipError_t launch_combine_rows_bwd(const void* dout, const void* rows, bool f32, int64_t R, int64_t K, const int32_t* pair_row,
+                                   int64_t M, int topk, const float* weights, void* drows, float* dweights,
+                                   hipStream_t stream);
+
+// Grouped products in bf16; product is an mxq_product.
+bool bf16_mm_sizes_ok(int product, int64_t M, int64_t N, int64_t K, int64_t G);
+size_t bf16_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int64_t G);
+hipError_t launch_bf16_mm(int product, const void* rows, const void* other, const int32_t* offs, int M, int N, int K, int G,
+                          void* out, bool f32_out, bool accumulate, void* workspace, hipStream_t stream);
 
 // Routing.
 int route_max_experts();

@@ -1,0 +1,189 @@
+// rows.hip -- token rows to their experts and back (gfx950): the gather into expert order,
+// the weighted sum of each token's rows, and its gradients.
+//
+//   dispatch     rows[pair_row[t, j]] = x[t]
+//   combine      out[t] = sum over j of w[t, j] * rows[pair_row[t, j]]
+//   gradients    drows[pair_row[t, j]] = w[t, j] * dout[t]
+//                dw[t, j] = sum over k of dout[t, k] * rows[pair_row[t, j], k]
+//
+// All walk over tokens, not rows: a token's own row (x, out, dout) is then read or written
+// once, its topk rows once each, which is every byte once.  Sums are fp32, over j in order,
+// and over k in an order fixed by K.  HBM bound.
+#include "device_common.hpp"
+#include "internal.hpp"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kBatch = 8;                                 // rows of a token in flight at once
+constexpr int kMaxGrid = 1 << 22;
+
+// Row of pair p, -1 for none.
+__device__ __forceinline__ int64_t row_of(const int32_t* pair_row, int64_t p, int64_t R)
+{
+    const int64_t r = pair_row[p];
+    return r >= 0 && r < R ? r : -1;
+}
+
+// A wave takes 64 chunks of 16 bytes of a token.
+__global__ __launch_bounds__(kThreads)
+void dispatch_rows_kernel(const uint4* __restrict__ x, int64_t chunks, int64_t M, int topk, const int32_t* __restrict__ pair_row,
+                          const int32_t* __restrict__ group_end, int E, uint4* __restrict__ rows, int32_t* __restrict__ src_pair)
+{
+    const int64_t slices = (chunks + 63) / 64, P = M * topk;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < P; i += (int64_t)gridDim.x * kThreads)
+        if (i >= group_end[E - 1]) src_pair[i] = -1;      // past the last row
+    for (int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); u < M * slices; u += (int64_t)gridDim.x * kWaves) {
+        const int64_t t = u / slices, c = (u - t * slices) * 64 + lane_id();
+        if (c >= chunks) continue;
+        const uint4 v = x[t * chunks + c];
+        for (int j = 0; j < topk; ++j) {
+            const int64_t r = row_of(pair_row, t * topk + j, P);
+            if (r >= 0) rows[r * chunks + c] = v;
+        }
+    }
+}
+
+__global__ __launch_bounds__(kThreads)
+void fill_kernel(int32_t* p, int64_t n, int32_t v)
+{
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) p[i] = v;
+}
+
+__global__ __launch_bounds__(kThreads)
+void pair_rows_kernel(const int32_t* __restrict__ src_pair, int64_t n, int32_t* __restrict__ pair_row)
+{
+    for (int64_t r = (int64_t)blockIdx.x * kThreads + threadIdx.x; r < n; r += (int64_t)gridDim.x * kThreads) {
+        const int64_t p = src_pair[r];
+        if (p >= 0 && p < n) pair_row[p] = (int32_t)r;
+    }
+}
+
+// A wave takes 64 chunks of 8 values of a token.
+template <class T>
+__global__ __launch_bounds__(kThreads)
+void combine_rows_kernel(const uint8_t* __restrict__ rows, int64_t R, int64_t K, const int32_t* __restrict__ pair_row, int64_t M,
+                         int topk, const float* __restrict__ weights, uint8_t* __restrict__ out)
+{
+    const int64_t chunks = K / 8, slices = (chunks + 63) / 64, row_bytes = K * T::kBytes;
+    for (int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); u < M * slices; u += (int64_t)gridDim.x * kWaves) {
+        const int64_t t = u / slices, c = (u - t * slices) * 64 + lane_id();
+        if (c >= chunks) continue;
+        float acc[8] = {};
+        for (int j = 0; j < topk; ++j) {
+            const int64_t r = row_of(pair_row, t * topk + j, R);
+            if (r < 0) continue;
+            const float w = weights ? weights[t * topk + j] : 1.0f;
+            float v[8];
+            T::unpack(T::load8(rows + r * row_bytes, c), v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        }
+        T::store8(out + t * row_bytes, c, T::pack(acc));
+    }
+}
+
+// A workgroup takes a token and kBatch of its slots.  dweights null: only drows.
+template <class T>
+__global__ __launch_bounds__(kThreads)
+void combine_rows_bwd_kernel(const uint8_t* __restrict__ dout, const uint8_t* rows, int64_t R, int64_t K,
+                             const int32_t* __restrict__ pair_row, int64_t M, int topk, const float* __restrict__ weights,
+                             uint8_t* drows, float* __restrict__ dweights)
+{
+    __shared__ float sh[kWaves][kBatch];
+    const int64_t chunks = K / 8, row_bytes = K * T::kBytes;
+    const int batches = (topk + kBatch - 1) / kBatch;
+    for (int64_t u = blockIdx.x; u < M * batches; u += gridDim.x) {
+        const int64_t t = u / batches;
+        const int j0 = (int)(u - t * batches) * kBatch, n = topk - j0 < kBatch ? topk - j0 : kBatch;
+        const int64_t p0 = t * topk + j0;
+        float dot[kBatch] = {};
+        for (int64_t c = threadIdx.x; c < chunks; c += kThreads) {
+            float d[8];
+            T::unpack(T::load8(dout + t * row_bytes, c), d);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (j >= n) continue;
+                const int64_t r = row_of(pair_row, p0 + j, R);
+                if (r < 0) continue;
+                if (dweights) {
+                    float v[8];
+                    T::unpack(T::load8(rows + r * row_bytes, c), v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], v[e], dot[j]);
+                }
+                const float w = weights ? weights[p0 + j] : 1.0f;
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = w * d[e];
+                T::store8(drows + r * row_bytes, c, T::pack(o));
+            }
+        }
+        if (!dweights) continue;
+        __syncthreads();                                  // (the last token's sums have been read)
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float s = lanes_sum<64>(dot[j]);
+            if (lane_id() == 0) sh[threadIdx.x >> 6][j] = s;
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < n) {
+            float s = 0.0f;
+            for (int w = 0; w < kWaves; ++w) s += sh[w][threadIdx.x];
+            dweights[p0 + threadIdx.x] = s;
+        }
+    }
+}
+
+unsigned capped(int64_t blocks) { return (unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid); }
+
+}  // namespace
+
+hipError_t launch_dispatch_rows(const void* x, int64_t row_bytes, int64_t M, int topk, const int32_t* pair_row,
+                                const int32_t* group_end, int E, void* rows, int32_t* src_pair, hipStream_t stream)
+{
+    const int64_t chunks = row_bytes / 16, waves = M * ((chunks + 63) / 64);
+    hipLaunchKernelGGL(dispatch_rows_kernel, dim3(capped((waves + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream,
+                       (const uint4*)x, chunks, M, topk, pair_row, group_end, E, (uint4*)rows, src_pair);
+    return hipGetLastError();
+}
+
+hipError_t launch_pair_rows(const int32_t* src_pair, int64_t pairs, int32_t* pair_row, hipStream_t stream)
+{
+    const unsigned grid = capped((pairs + kThreads - 1) / kThreads);
+    hipLaunchKernelGGL(fill_kernel, dim3(grid), dim3(kThreads), 0, stream, pair_row, pairs, -1);
+    hipLaunchKernelGGL(pair_rows_kernel, dim3(grid), dim3(kThreads), 0, stream, src_pair, pairs, pair_row);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_rows(const void* rows, bool f32, int64_t R, int64_t K, const int32_t* pair_row, int64_t M, int topk,
+                               const float* weights, void* out, hipStream_t stream)
+{
+    const int64_t waves = M * ((K / 8 + 63) / 64);
+    const dim3 grid(capped((waves + kWaves - 1) / kWaves));
+    if (f32)
+        hipLaunchKernelGGL(combine_rows_kernel<F32>, grid, dim3(kThreads), 0, stream, (const uint8_t*)rows, R, K, pair_row, M,
+                           topk, weights, (uint8_t*)out);
+    else
+        hipLaunchKernelGGL(combine_rows_kernel<Bf16>, grid, dim3(kThreads), 0, stream, (const uint8_t*)rows, R, K, pair_row, M,
+                           topk, weights, (uint8_t*)out);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_rows_bwd(const void* dout, const void* rows, bool f32, int64_t R, int64_t K, const int32_t* pair_row,
+                                   int64_t M, int topk, const float* weights, void* drows, float* dweights, hipStream_t stream)
+{
+    const dim3 grid(capped(M * ((topk + kBatch - 1) / kBatch)));
+    if (f32)
+        hipLaunchKernelGGL(combine_rows_bwd_kernel<F32>, grid, dim3(kThreads), 0, stream, (const uint8_t*)dout,
+                           (const uint8_t*)rows, R, K, pair_row, M, topk, weights, (uint8_t*)drows, dweights);
+    else
+        hipLaunchKernelGGL(combine_rows_bwd_kernel<Bf16>, grid, dim3(kThreads), 0, stream, (const uint8_t*)dout,
+                           (const uint8_t*)rows, R, K, pair_row, M, topk, weights, (uint8_t*)drows, dweights);
+    return hipGetLastError();
+}
+
+}  // namespace mxq

@@ -39,6 +39,7 @@ MXQ_FMT_E4M3 = 0
 MXQ_FMT_E2M1 = 1
 MXQ_SCORE_SOFTMAX = 0
 MXQ_SCORE_SIGMOID = 1
+MXQ_PRODUCT_Y, MXQ_PRODUCT_DX, MXQ_PRODUCT_DW = 0, 1, 2
 MXQ_ROUTE_RENORM = 1
 MXQ_ROUTE_GROUP_TOP2 = 2
 
@@ -50,7 +51,10 @@ EXPORTED = ("mxq_abi_version", "mxq_status_string", "mxq_last_hip_error", "mxq_q
             "mxq_set_group_scale_knobs", "mxq_group_scale_fp8_noalloc", "mxq_group_scale_route_counters",
             "mxq_add_rmsnorm", "mxq_add_rmsnorm_bwd_workspace_bytes", "mxq_add_rmsnorm_bwd", "mxq_route_topk",
             "mxq_route_topk_bwd", "mxq_quantize_mxfp4", "mxq_dequantize_mxfp4",
-            "mxq_mxfp4_grouped_mm", "mxq_mxfp4_grouped_mm_packed")
+            "mxq_mxfp4_grouped_mm", "mxq_mxfp4_grouped_mm_packed", "mxq_bf16_grouped_mm_workspace_bytes",
+            "mxq_bf16_grouped_mm", "mxq_bf16_grouped_mm_dx", "mxq_bf16_grouped_mm_dw", "mxq_add_layernorm",
+            "mxq_add_layernorm_bwd_workspace_bytes", "mxq_add_layernorm_bwd", "mxq_dispatch_rows_workspace_bytes",
+            "mxq_dispatch_rows", "mxq_pair_rows", "mxq_combine_rows", "mxq_combine_rows_bwd")
 
 GROUP_METHODS = {"auto": 0, "hold": 1, "twopass": 2, "split": 3}
 
@@ -133,6 +137,30 @@ def lib() -> ctypes.CDLL:
         L.mxq_mxfp4_grouped_mm.argtypes = [P, P, ci, P, P, P, i64, i64, i64, i32, ci, P, P]
         L.mxq_mxfp4_grouped_mm_packed.restype = ci
         L.mxq_mxfp4_grouped_mm_packed.argtypes = [P, P, P, P, i64, i64, i64, i32, ci, P, P]
+        L.mxq_bf16_grouped_mm_workspace_bytes.restype = sz
+        L.mxq_bf16_grouped_mm_workspace_bytes.argtypes = [ci, i64, i64, i64, i32]
+        L.mxq_bf16_grouped_mm.restype = ci
+        L.mxq_bf16_grouped_mm.argtypes = [P, P, P, i64, i64, i64, i32, ci, P, P, sz, P]
+        L.mxq_bf16_grouped_mm_dx.restype = ci
+        L.mxq_bf16_grouped_mm_dx.argtypes = [P, P, P, i64, i64, i64, i32, ci, P, P, sz, P]
+        L.mxq_bf16_grouped_mm_dw.restype = ci
+        L.mxq_bf16_grouped_mm_dw.argtypes = [P, P, P, i64, i64, i64, i32, ci, ci, P, P, sz, P]
+        L.mxq_add_layernorm.restype = ci
+        L.mxq_add_layernorm.argtypes = [P, P, P, P, ci, i64, i64, f32, P, P, P, P, P, P, P]
+        L.mxq_add_layernorm_bwd_workspace_bytes.restype = sz
+        L.mxq_add_layernorm_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.mxq_add_layernorm_bwd.restype = ci
+        L.mxq_add_layernorm_bwd.argtypes = [P, P, P, P, P, P, ci, i64, i64, P, P, P, P, sz, P]
+        L.mxq_dispatch_rows_workspace_bytes.restype = sz
+        L.mxq_dispatch_rows_workspace_bytes.argtypes = [i64, i32, i32]
+        L.mxq_dispatch_rows.restype = ci
+        L.mxq_dispatch_rows.argtypes = [P, ci, i64, i64, P, i32, i32, P, P, P, P, P, sz, P]
+        L.mxq_pair_rows.restype = ci
+        L.mxq_pair_rows.argtypes = [P, i64, P, P]
+        L.mxq_combine_rows.restype = ci
+        L.mxq_combine_rows.argtypes = [P, ci, i64, i64, P, i64, i32, P, P, P]
+        L.mxq_combine_rows_bwd.restype = ci
+        L.mxq_combine_rows_bwd.argtypes = [P, P, ci, i64, i64, P, i64, i32, P, P, P, P]
         _lib = L
     return _lib
 
@@ -737,3 +765,179 @@ def mxfp4_grouped_mm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: t
     y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
     mxq_mxfp4_grouped_mm(xq, xs, x_format, wq, ws, group_end_offs, y)
     return y
+
+
+# ------------------------------------------------------- products in bf16 ---
+# (Their helpers, which allocate, are in training.py.)
+def mxq_bf16_grouped_mm_workspace_bytes(product: int, M: int, N: int, K: int, G: int) -> int:
+    return int(lib().mxq_bf16_grouped_mm_workspace_bytes(int(product), int(M), int(N), int(K), int(G)))
+
+
+def _bytes(t) -> int:
+    """Size of a workspace that may be None."""
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def mxq_bf16_grouped_mm(x: torch.Tensor, w: torch.Tensor, group_end_offs: torch.Tensor, y: torch.Tensor, workspace=None,
+                        stream=None) -> None:
+    """x (M, K), w (G, N, K) bf16, group_end_offs int32[G] (device) -> y (M, N) bf16 or float32."""
+    if x.dim() != 2 or w.dim() != 3 or y.dim() != 2:
+        raise ValueError("x must be (M, K), w (G, N, K) and y (M, N)")
+    M, K = x.shape
+    G, N, Kw = w.shape
+    if Kw != K or tuple(y.shape) != (M, N):
+        raise ValueError("operand shapes do not match")
+    px, pw = _dev(x, "x", torch.bfloat16), _dev(w, "w", torch.bfloat16)
+    po = _dev(group_end_offs, "group_end_offs", torch.int32, G)
+    code, py = _float_code(y, "y"), _dev(y, "y")
+    _check(lib().mxq_bf16_grouped_mm(px, pw, po, M, N, K, G, code, py, _opt(workspace, "workspace"), _bytes(workspace),
+                                     _stream(stream)), "mxq_bf16_grouped_mm")
+
+
+def mxq_bf16_grouped_mm_dx(dy: torch.Tensor, w: torch.Tensor, group_end_offs: torch.Tensor, dx: torch.Tensor,
+                           workspace=None, stream=None) -> None:
+    """dy (M, N), w (G, N, K) bf16, group_end_offs int32[G] (device) -> dx (M, K) bf16 or float32."""
+    if dy.dim() != 2 or w.dim() != 3 or dx.dim() != 2:
+        raise ValueError("dy must be (M, N), w (G, N, K) and dx (M, K)")
+    G, N, K = w.shape
+    M = dy.shape[0]
+    if dy.shape[1] != N or tuple(dx.shape) != (M, K):
+        raise ValueError("operand shapes do not match")
+    pd, pw = _dev(dy, "dy", torch.bfloat16), _dev(w, "w", torch.bfloat16)
+    po = _dev(group_end_offs, "group_end_offs", torch.int32, G)
+    code, px = _float_code(dx, "dx"), _dev(dx, "dx")
+    _check(lib().mxq_bf16_grouped_mm_dx(pd, pw, po, M, N, K, G, code, px, _opt(workspace, "workspace"), _bytes(workspace),
+                                        _stream(stream)), "mxq_bf16_grouped_mm_dx")
+
+
+def mxq_bf16_grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, group_end_offs: torch.Tensor, dw: torch.Tensor,
+                           accumulate: bool = False, workspace=None, stream=None) -> None:
+    """dy (M, N), x (M, K) bf16, group_end_offs int32[G] (device) -> dw (G, N, K) bf16 or float32; with accumulate
+    the sums are added to the float32 dw."""
+    if dy.dim() != 2 or x.dim() != 2 or dw.dim() != 3:
+        raise ValueError("dy must be (M, N), x (M, K) and dw (G, N, K)")
+    G, N, K = dw.shape
+    M = dy.shape[0]
+    if dy.shape[1] != N or tuple(x.shape) != (M, K):
+        raise ValueError("operand shapes do not match")
+    pd, px = _dev(dy, "dy", torch.bfloat16), _dev(x, "x", torch.bfloat16)
+    po = _dev(group_end_offs, "group_end_offs", torch.int32, G)
+    code, pw = _float_code(dw, "dw"), _dev(dw, "dw")
+    _check(lib().mxq_bf16_grouped_mm_dw(pd, px, po, M, N, K, G, code, int(bool(accumulate)), pw,
+                                        _opt(workspace, "workspace"), _bytes(workspace), _stream(stream)),
+           "mxq_bf16_grouped_mm_dw")
+
+
+# ------------------------------------------------------------- layer norm ---
+def mxq_add_layernorm(x: torch.Tensor, residual, weight: torch.Tensor, bias, eps: float, h=None, y=None, q=None, s=None,
+                      mean=None, rstd=None, stream=None) -> None:
+    """x (+ residual) (M, K), weight (K) and bias (K) or None, bf16 or float32 -> h = x + residual, y = the layer norm of
+    h (their type), q (M, K) / s (M, K/32) uint8 = MXFP8 of y, mean and rstd (M) float32; outputs may be None."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D (M, K)")
+    M, K = x.shape
+    code, dt, n = _float_code(x, "x"), x.dtype, M * K
+    px = _dev(x, "x")
+    pr = _opt(residual, "residual", dt, n)
+    pw = _dev(weight, "weight", dt, K)
+    pb = _opt(bias, "bias", dt, K)
+    ph = _opt(h, "h", dt, n)
+    py = _opt(y, "y", dt, n)
+    pq = _opt(q, "q", torch.uint8, n)
+    ps = _opt(s, "s", torch.uint8, M * (K // 32) if K % 32 == 0 else None)
+    pm = _opt(mean, "mean", torch.float32, M)
+    pd = _opt(rstd, "rstd", torch.float32, M)
+    _check(lib().mxq_add_layernorm(px, pr, pw, pb, code, M, K, float(eps), ph, py, pq, ps, pm, pd, _stream(stream)),
+           "mxq_add_layernorm")
+
+
+def mxq_add_layernorm_bwd_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().mxq_add_layernorm_bwd_workspace_bytes(int(M), int(K)))
+
+
+def mxq_add_layernorm_bwd(h: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, dy: torch.Tensor,
+                          dh, dx: torch.Tensor, dweight: torch.Tensor, dbias, workspace: torch.Tensor, stream=None) -> None:
+    """h, mean, rstd of mxq_add_layernorm and the gradients dy, dh (or None) -> dx (M, K), dweight (K) and dbias (K, or
+    None) float32."""
+    if h.dim() != 2:
+        raise ValueError("h must be 2-D (M, K)")
+    M, K = h.shape
+    code, dt, n = _float_code(h, "h"), h.dtype, M * K
+    ph = _dev(h, "h")
+    pw = _dev(weight, "weight", dt, K)
+    pm = _dev(mean, "mean", torch.float32, M)
+    pr = _dev(rstd, "rstd", torch.float32, M)
+    pg = _dev(dy, "dy", dt, n)
+    pd = _opt(dh, "dh", dt, n)
+    px = _dev(dx, "dx", dt, n)
+    pk = _dev(dweight, "dweight", torch.float32, K)
+    pb = _opt(dbias, "dbias", torch.float32, K)
+    pws = _dev(workspace, "workspace")
+    _check(lib().mxq_add_layernorm_bwd(ph, pw, pm, pr, pg, pd, code, M, K, px, pk, pb, pws, _bytes(workspace),
+                                       _stream(stream)), "mxq_add_layernorm_bwd")
+
+
+# --------------------------------------------- rows to the experts and back ---
+def mxq_dispatch_rows_workspace_bytes(M: int, topk: int, E: int) -> int:
+    return int(lib().mxq_dispatch_rows_workspace_bytes(int(M), int(topk), int(E)))
+
+
+def mxq_dispatch_rows(x: torch.Tensor, expert_ids: torch.Tensor, E: int, rows: torch.Tensor, group_end_offs: torch.Tensor,
+                      src_pair: torch.Tensor, pair_row: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """x (M, K) bf16 or float32, expert_ids (M, topk) int32 -> rows (M*topk, K) sorted stably by expert,
+    group_end_offs int32[E], src_pair int32[M*topk], pair_row int32 (M, topk)."""
+    if x.dim() != 2 or expert_ids.dim() != 2 or expert_ids.shape[0] != x.shape[0]:
+        raise ValueError("x must be (M, K) and expert_ids (M, topk)")
+    M, K = x.shape
+    topk = expert_ids.shape[1]
+    code = _float_code(x, "x")
+    px = _dev(x, "x")
+    pi = _dev(expert_ids, "expert_ids", torch.int32)
+    pr = _dev(rows, "rows", x.dtype, M * topk * K)
+    pe = _dev(group_end_offs, "group_end_offs", torch.int32, int(E))
+    ps = _dev(src_pair, "src_pair", torch.int32, M * topk)
+    pp = _dev(pair_row, "pair_row", torch.int32, M * topk)
+    pw = _dev(workspace, "workspace")
+    _check(lib().mxq_dispatch_rows(px, code, M, K, pi, topk, int(E), pr, pe, ps, pp, pw, _bytes(workspace),
+                                   _stream(stream)), "mxq_dispatch_rows")
+
+
+def mxq_pair_rows(src_pair: torch.Tensor, pair_row: torch.Tensor, stream=None) -> None:
+    """src_pair int32 (a dispatch's) -> pair_row int32, its inverse, as many elements."""
+    n = src_pair.numel()
+    ps = _dev(src_pair, "src_pair", torch.int32)
+    pp = _dev(pair_row, "pair_row", torch.int32, n)
+    _check(lib().mxq_pair_rows(ps, n, pp, _stream(stream)), "mxq_pair_rows")
+
+
+def mxq_combine_rows(rows: torch.Tensor, pair_row: torch.Tensor, weights, out: torch.Tensor, stream=None) -> None:
+    """rows (R, K) bf16 or float32, pair_row (M, topk) int32, weights (M, topk) float32 or None -> out (M, K)."""
+    if rows.dim() != 2 or pair_row.dim() != 2:
+        raise ValueError("rows must be (R, K) and pair_row (M, topk)")
+    R, K = rows.shape
+    M, topk = pair_row.shape
+    code = _float_code(rows, "rows")
+    pr = _dev(rows, "rows")
+    pp = _dev(pair_row, "pair_row", torch.int32)
+    pw = _opt(weights, "weights", torch.float32, M * topk)
+    po = _dev(out, "out", rows.dtype, M * K)
+    _check(lib().mxq_combine_rows(pr, code, R, K, pp, M, topk, pw, po, _stream(stream)), "mxq_combine_rows")
+
+
+def mxq_combine_rows_bwd(dout: torch.Tensor, rows, pair_row: torch.Tensor, weights, drows: torch.Tensor, dweights=None,
+                         stream=None) -> None:
+    """dout (M, K), rows (R, K) or None (without dweights), pair_row (M, topk) int32, weights (M, topk) float32 or None
+    -> drows (R, K) of dout's type, dweights (M, topk) float32 or None."""
+    if dout.dim() != 2 or drows.dim() != 2 or pair_row.dim() != 2:
+        raise ValueError("dout must be (M, K), drows (R, K) and pair_row (M, topk)")
+    R, K = drows.shape
+    M, topk = pair_row.shape
+    code, dt = _float_code(dout, "dout"), dout.dtype
+    pd = _dev(dout, "dout", dt, M * K)
+    pr = _opt(rows, "rows", dt, R * K)
+    pp = _dev(pair_row, "pair_row", torch.int32)
+    pw = _opt(weights, "weights", torch.float32, M * topk)
+    px = _dev(drows, "drows", dt)
+    pk = _opt(dweights, "dweights", torch.float32, M * topk)
+    _check(lib().mxq_combine_rows_bwd(pd, pr, code, R, K, pp, M, topk, pw, px, pk, _stream(stream)),
+           "mxq_combine_rows_bwd")

@@ -61,8 +61,9 @@ typedef enum mxq_status {
     MXQ_ERR_HIP = 6,         /* a HIP runtime call failed (launch, device query)    */
     MXQ_ERR_NOT_IMPLEMENTED = 7,
     MXQ_ERR_DTYPE = 8,       /* unknown mxq_out_dtype or mxq_format value           */
-    MXQ_ERR_RULE = 9         /* unknown mxq_scale_rule or mxq_score value, unknown
-                                flag, or an eps that is negative or NaN             */
+    MXQ_ERR_RULE = 9         /* unknown mxq_scale_rule, mxq_score or mxq_product
+                                value, unknown flag, or an eps that is negative or
+                                NaN                                                 */
 } mxq_status;
 
 typedef enum mxq_layout {
@@ -98,6 +99,12 @@ typedef enum mxq_score {
     MXQ_SCORE_SOFTMAX = 0,   /* softmax over a row's logits                          */
     MXQ_SCORE_SIGMOID = 1    /* 1 / (1 + exp(-l)) of each logit                      */
 } mxq_score;
+
+typedef enum mxq_product {
+    MXQ_PRODUCT_Y = 0,       /* mxq_bf16_grouped_mm                                  */
+    MXQ_PRODUCT_DX = 1,      /* mxq_bf16_grouped_mm_dx                               */
+    MXQ_PRODUCT_DW = 2       /* mxq_bf16_grouped_mm_dw                               */
+} mxq_product;
 
 typedef enum mxq_route_flags {
     MXQ_ROUTE_RENORM = 1,    /* divide the selected scores by their sum              */
@@ -594,6 +601,133 @@ mxq_status mxq_mxfp4_grouped_mm(const void* xq, const void* xs_e8m0, int x_forma
 mxq_status mxq_mxfp4_grouped_mm_packed(const void* packed, const void* wq_e2m1, const void* ws_e8m0,
                                        const int32_t* group_end_offs, int64_t M, int64_t N, int64_t K,
                                        int32_t G, int out_dtype, void* y, void* stream);
+
+/*
+ * Grouped products in bf16: a training step's three products of the token rows of
+ * group g with expert weight W_g (N, K), for every group:
+ *   mxq_bf16_grouped_mm     Y[m, :]  = X[m, :] W_g^T      y (M, N) of out_dtype;
+ *   mxq_bf16_grouped_mm_dx  dX[m, :] = dY[m, :] W_g       dx (M, K) of out_dtype;
+ *   mxq_bf16_grouped_mm_dw  dW_g = sum over the group's rows of dY[m, :]^T X[m, :]
+ *                           dw (G, N, K) of out_dtype.
+ *
+ *   x (M, K), w (G, N, K), dy (M, N): bf16.  group_end_offs: DEVICE int32[G], clamped
+ *   as in mxq_group_scale_fp8 and read on the device only.
+ *   accumulate  0: dw is written (zeros for a group without rows).  1: the sums are
+ *           added to what dw holds, in fp32 (a group without rows keeps its own); needs
+ *           MXQ_OUT_F32 (MXQ_ERR_DTYPE otherwise), any other value: MXQ_ERR_RULE.
+ *   workspace   DEVICE scratch of mxq_bf16_grouped_mm_workspace_bytes(product, M, N,
+ *           K, G) bytes, for either out_dtype; where that is 0 it may be NULL.  It
+ *           holds parts of sums that are split over several workgroups; it needs no
+ *           initialisation, and two calls in flight must not share it.
+ *
+ * Rows at or past the last end belong to no group: their y and dx are written as
+ * zeros, and what they hold reaches no result.  Products are exact, sums are fp32 in
+ * an order fixed by the sizes, and the result is rounded once.  A NaN or an infinity
+ * reaches the results whose sums it enters, and no others.
+ *
+ * Requires 8 <= K, N <= 2^20, K % 8 == 0, N % 8 == 0, 0 <= M <= 2^31 - 1024,
+ * 1 <= G <= 4095, G*N*K <= 2^40, and fewer than 2^30 tiles of 64 x 256 results
+ * (MXQ_ERR_SHAPE).  M == 0 is a no-op for y and dx; dw is then written as zeros (or
+ * kept).  All buffers 16-byte aligned except group_end_offs (4-byte).
+ */
+size_t mxq_bf16_grouped_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int32_t G);
+mxq_status mxq_bf16_grouped_mm(const void* x, const void* w, const int32_t* group_end_offs, int64_t M, int64_t N,
+                               int64_t K, int32_t G, int out_dtype, void* y, void* workspace,
+                               size_t workspace_bytes, void* stream);
+mxq_status mxq_bf16_grouped_mm_dx(const void* dy, const void* w, const int32_t* group_end_offs, int64_t M,
+                                  int64_t N, int64_t K, int32_t G, int out_dtype, void* dx, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+mxq_status mxq_bf16_grouped_mm_dw(const void* dy, const void* x, const int32_t* group_end_offs, int64_t M,
+                                  int64_t N, int64_t K, int32_t G, int out_dtype, int accumulate, void* dw,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Residual addition and layer norm of token rows, with the MXFP8 encoding of the
+ * normalised rows: mxq_add_rmsnorm with the row's mean taken off and a bias.
+ *   bias     (K) of dtype, or NULL (zeros).
+ *   mean     (M) fp32 output, the row mean of h; or NULL.
+ *   rstd     (M) fp32 output 1 / sqrt(mean((h - mean)^2) + eps); or NULL.
+ *   y        (M, K) output (h - mean) * rstd * weight + bias, rounded once; or NULL (with q).
+ * Everything else as mxq_add_rmsnorm, errors included.  The mean is taken first and
+ * the squares are those of the differences from it, in fp32.  A NaN or an infinity in h
+ * makes its whole row NaN (scales 0xFF), as do values whose sum, or squares whose sum,
+ * pass the largest fp32 value; with eps = 0 a row of equal values comes out as NaN.
+ */
+mxq_status mxq_add_layernorm(const void* x, const void* residual, const void* weight, const void* bias, int dtype,
+                             int64_t M, int64_t K, float eps, void* h, void* y, void* q_e4m3, void* s_e8m0,
+                             float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients of mxq_add_layernorm, given h, mean and rstd as it wrote them, dy and dh
+ * (the gradient that reaches h along the residual stream, or NULL); with
+ * n = (h - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - mean(g) - n * mean(g * n)) + dh, of x and of residual alike,
+ *   rounded once;
+ *   dweight (K) fp32 = sum over the rows of dy * n;
+ *   dbias   (K) fp32 = sum over the rows of dy; or NULL.
+ * dx may be dy or dh itself (in place).  Sizes, errors and workspace as
+ * mxq_add_rmsnorm_bwd; M == 0 writes zero dweight and dbias.
+ */
+size_t mxq_add_layernorm_bwd_workspace_bytes(int64_t M, int64_t K);
+mxq_status mxq_add_layernorm_bwd(const void* h, const void* weight, const float* mean, const float* rstd,
+                                 const void* dy, const void* dh, int dtype, int64_t M, int64_t K, void* dx,
+                                 float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Token rows to their experts without encoding: mxq_dispatch_pack_mx's order, with
+ * the rows as they are, and the way back beside it.
+ *   dtype           MXQ_OUT_BF16 or MXQ_OUT_F32: the type of x and rows.
+ *   x               (M, K) tokens; expert_ids DEVICE int32 (M, topk), as there.
+ *   rows            (M*topk, K) output: row r is token src_pair[r] / topk.  Rows at or
+ *                   past the last end are not written.
+ *   group_end_offs, src_pair   as there.
+ *   pair_row        DEVICE int32 (M, topk) output: the row of each pair, -1 for a
+ *                   dropped one: the inverse of src_pair.
+ *   workspace       DEVICE scratch of mxq_dispatch_rows_workspace_bytes(M, topk, E)
+ *                   bytes, 16-B aligned, no initialisation needed.
+ * Its gradient is mxq_combine_rows without weights.  Requires K % 8 == 0,
+ * 0 < K <= 2^23; topk, E, M*topk, alignment and errors as mxq_dispatch_pack_mx;
+ * MXQ_ERR_DTYPE for another dtype.  M == 0 writes only group_end_offs (all zero).
+ */
+size_t mxq_dispatch_rows_workspace_bytes(int64_t M, int32_t topk, int32_t E);
+mxq_status mxq_dispatch_rows(const void* x, int dtype, int64_t M, int64_t K, const int32_t* expert_ids, int32_t topk,
+                             int32_t E, void* rows, int32_t* group_end_offs, int32_t* src_pair, int32_t* pair_row,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* The row of each pair from a dispatch's src_pair (mxq_dispatch_pack_mx leaves only
+ * that): pair_row[src_pair[r]] = r, -1 for pairs of no row.  Both DEVICE int32[pairs];
+ * entries of src_pair outside [0, pairs) name no pair, and no two name the same.
+ * 0 <= pairs < 2^31 - 256 (MXQ_ERR_SHAPE). */
+mxq_status mxq_pair_rows(const int32_t* src_pair, int64_t pairs, int32_t* pair_row, void* stream);
+
+/*
+ * The return trip: the weighted sum of each token's rows.
+ *   rows       (R, K) of dtype (MXQ_OUT_BF16 or MXQ_OUT_F32).
+ *   pair_row   DEVICE int32 (M, topk): the rows of token t; an entry outside [0, R) is
+ *              an empty slot, which adds nothing.
+ *   weights    fp32 (M, topk), or NULL: ones (the gradient of mxq_dispatch_rows).
+ *   out        (M, K) output: sum over j, in order, of weights[t, j] * rows[pair_row[t, j]],
+ *              in fp32, rounded once; zeros for a token without rows.
+ * Requires K % 8 == 0, K <= 2^23, 1 <= topk <= 64, R < 2^31, M*topk < 2^31 - 256 and
+ * M*K and R*K at most 2^40 (MXQ_ERR_SHAPE).  rows and out 16-byte aligned, the other
+ * arrays 4-byte.  M == 0 or K == 0 is a no-op; rows may be NULL if R == 0.
+ */
+mxq_status mxq_combine_rows(const void* rows, int dtype, int64_t R, int64_t K, const int32_t* pair_row, int64_t M,
+                            int32_t topk, const float* weights, void* out, void* stream);
+
+/*
+ * Gradients of mxq_combine_rows, from dout (M, K), the gradient of out:
+ *   drows (R, K)     drows[pair_row[t, j]] = weights[t, j] * dout[t], rounded once; rows
+ *                    that no pair names are not written, and no two pairs name the same.
+ *   dweights (M, topk) fp32: the sum over k of dout[t, k] * rows[pair_row[t, j], k], 0 for
+ *                    an empty slot; or NULL (then rows may be NULL too).
+ * weights may be NULL (ones).  drows may be rows itself (in place).  Sizes and errors as
+ * mxq_combine_rows; K == 0 writes zero dweights.
+ */
+mxq_status mxq_combine_rows_bwd(const void* dout, const void* rows, int dtype, int64_t R, int64_t K,
+                                const int32_t* pair_row, int64_t M, int32_t topk, const float* weights, void* drows,
+                                float* dweights, void* stream);
 
 #ifdef __cplusplus
 }
