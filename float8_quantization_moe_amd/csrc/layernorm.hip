@@ -170,12 +170,13 @@ void add_layernorm_bwd_kernel(const uint8_t* __restrict__ h, const uint8_t* __re
     const int sub = (int)threadIdx.x / LANES;
     const int K8 = K / 8;
     const int64_t row_bytes = (int64_t)K * T::kBytes;
+    constexpr bool kHoldW = LANES < 512;                  // (a row's w anew from the cache where registers are short)
     typename T::Raw wr[C];
     float aw[C][8], ab[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = lane + c * LANES;
-        if (i < K8) wr[c] = T::load8(w, i);
+        if (kHoldW && i < K8) wr[c] = T::load8(w, i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) aw[c][e] = ab[c][e] = 0.0f;
     }
@@ -201,7 +202,7 @@ void add_layernorm_bwd_kernel(const uint8_t* __restrict__ h, const uint8_t* __re
                 float a[8], g[8], f[8];
                 T::unpack(hr[c], a);
                 T::unpack(gr[c], g);
-                T::unpack(wr[c], f);
+                T::unpack(kHoldW ? wr[c] : T::load8(w, i), f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float n = (a[e] - mu) * rs, u = g[e] * f[e];
@@ -221,7 +222,7 @@ void add_layernorm_bwd_kernel(const uint8_t* __restrict__ h, const uint8_t* __re
                 float a[8], g[8], f[8], o[8];
                 T::unpack(hr[c], a);
                 T::unpack(gr[c], g);
-                T::unpack(wr[c], f);
+                T::unpack(kHoldW ? wr[c] : T::load8(w, i), f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] = rs * (g[e] * f[e] - m1 - (a[e] - mu) * rs * m2);
                 if (dh) {
