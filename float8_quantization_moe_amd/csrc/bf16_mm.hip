@@ -2,10 +2,29 @@
 // group g with weight W_g (N, K):
 //   Y[m, :] = X[m, :] W_g^T;   dX[m, :] = dY[m, :] W_g;   dW_g = sum over m of dY[m, :]^T X[m, :].
 //
-// A wave computes 32 x 32 results with v_mfma_f32_32x32x16_bf16, its operands straight from
-// global memory.
+// One kernel serves the three: a tile of results is 256 columns (of the operand that MFMA
+// takes as A: W for Y and dX, X for dW) by at most 256 rows (operand B: X, dY, dY), and the
+// sum runs along the memory rows of an operand ("along", X and W of Y, dY of dX) or across
+// them ("across": W of dX, both of dW).
+//
+// Persistent workgroups (one a CU, 4 waves in 2 x 2 of 128 x 128 results) walk over tiles.  The
+// sum advances 64 values a slot through a 2-slot LDS ring of 32 KB of each operand, filled by
+// buffer-load-to-LDS in whole 128-byte lines.  A slot is four MFMA steps of 16; a step's
+// operands are read from LDS during the step before it.  An "along" operand is 256 rows of 128
+// bytes in LDS, read 16 bytes a lane; an "across" one 64 rows of 512 bytes, read with the
+// transposing LDS read, which gives a lane four consecutive values of its own column.  With one
+// wave a SIMD nothing issues while a load or an LDS read waits for its pipe, so both are spread
+// between the MFMAs.
+//
+// The slots of successive tiles form one stream: the loads run ahead of the products across the
+// end of a tile, so the next tile's operands arrive while this one's results are stored.
+//
+// Every workgroup finds its own tiles from the group offsets (a scan in LDS), so no launch comes
+// before.  Where there are fewer tiles than CUs, the sum is split: the parts go to the workspace
+// in fp32 and a second launch adds them in order.
 #include "device_common.hpp"
 #include "internal.hpp"
+#include "mm_tile.hpp"
 
 #include "../../include/mxq.h"
 
@@ -13,92 +32,704 @@ namespace mxq {
 
 namespace {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
+constexpr int kThreads = kTileThreads;
+constexpr int kCols = 256;                               // columns of a tile
+constexpr int kSlotK = 64;
+constexpr uint32_t kOperandBytes = 32 * 1024;            // of one operand in one slot
+constexpr uint32_t kSlotBytes = 2 * kOperandBytes;
+constexpr uint32_t kLdsBytes = 2 * kSlotBytes;
+constexpr int kMaxEntries = 64;                          // tiles of one workgroup: one a lane
+constexpr int kColBlock = 4;                             // column tiles of a block of the tile order
+constexpr int kXcds = 8;
+constexpr int kMaxGroups = 4095;
+constexpr int kMaxSplit = 16;
+static_assert((2 * (kMaxGroups + 2) + kThreads) * 4 <= (int)kLdsBytes, "the scan's arrays fit the ring");
+
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef unsigned short v8u16 __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i* LdsV4i;
+typedef __attribute__((address_space(3))) v4s* LdsV4s;
 
 struct MmArgs {
-    const uint16_t *rows, *other;                         // X or dY; W or X
+    const uint16_t *a, *b;                               // W or X; X or dY
     const int32_t* offs;
     void* out;
     int M, N, K, G;
-    bool accumulate;
+    int rows;                                            // rows of a tile, at most: 128 or 256
+    int split;                                           // parts of the sum
 };
 
-// Values k0 .. k0 + 7 of an operand's row i along the sum; zeros past `rows` and `depth`.
-// TRANS: the sum runs over the rows of memory.
-template <bool TRANS>
-__device__ __forceinline__ v8u16 operand(const uint16_t* p, int64_t ld, int i, int rows, int k0, int depth)
-{
-    v8u16 v = {};
-    if (i < rows) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (k0 + e < depth) v[e] = TRANS ? p[(int64_t)(k0 + e) * ld + i] : p[(int64_t)i * ld + k0 + e];
+// The three products: which operands run across memory rows; what a tile's columns, its rows
+// and the sum's length are.
+template <int P>
+struct Shape {
+    static constexpr bool kDw = P == MXQ_PRODUCT_DW;
+    static constexpr bool kAcrossA = P != MXQ_PRODUCT_Y, kAcrossB = kDw;
+    static __host__ __device__ __forceinline__ int cols(int N, int K) { return P == MXQ_PRODUCT_Y ? N : K; }
+    static __device__ __forceinline__ int depth(int N, int K) { return P == MXQ_PRODUCT_Y ? K : N; }      // (not dW's)
+    static __device__ __forceinline__ uint32_t lda(int N, int K) { return 2u * (uint32_t)K; }
+    static __device__ __forceinline__ uint32_t ldb(int N, int K) { return 2u * (uint32_t)(P == MXQ_PRODUCT_Y ? K : N); }
+};
+
+struct Tile {
+    int g, r0, r1, c;                                    // group, rows [r0, r1) (dW: of the group's N), column tile
+    int k0, k1, part;                                    // the sum's range (dW: token rows), its part
+};
+
+// A workgroup's list: tile e in lane e of every wave.
+struct TileList {
+    Tile mine;
+    __device__ __forceinline__ Tile at(int e) const
+    {
+        return Tile{__builtin_amdgcn_readlane(mine.g, e),  __builtin_amdgcn_readlane(mine.r0, e),
+                    __builtin_amdgcn_readlane(mine.r1, e), __builtin_amdgcn_readlane(mine.c, e),
+                    __builtin_amdgcn_readlane(mine.k0, e), __builtin_amdgcn_readlane(mine.k1, e),
+                    __builtin_amdgcn_readlane(mine.part, e)};
     }
-    return v;
+};
+
+__device__ __forceinline__ int slots_of(const Tile& t)
+{
+    const int n = (t.k1 - t.k0 + kSlotK - 1) / kSlotK;
+    return n > 0 ? n : 1;                                // (an empty sum: one slot that loads nothing)
 }
 
-template <int PRODUCT, bool F32OUT>
-__global__ __launch_bounds__(64)
+// -------------------------------------------------------------- tile list ---
+// Part p of S of a sum of n values from `base`: whole slots but for the last.
+__device__ __forceinline__ void part_of(Tile& t, int base, int n, int p, int S)
+{
+    const int slots = (n + kSlotK - 1) / kSlotK;
+    const int a = (int)((int64_t)slots * p / S) * kSlotK, b = (int)((int64_t)slots * (p + 1) / S) * kSlotK;
+    t.part = p;
+    t.k0 = base + (a < n ? a : n);
+    t.k1 = base + (b < n ? b : n);
+}
+
+// Place `i` of a block-ordered grid of `rows` x `cols` tiles: kColBlock columns at a time, a
+// block's rows one after the other.
+__device__ __forceinline__ void place_in(int i, int rows, int cols, int* r, int* c)
+{
+    const int cb = i / (rows * kColBlock), rem = i - cb * rows * kColBlock;
+    const int width = cols - cb * kColBlock < kColBlock ? cols - cb * kColBlock : kColBlock;
+    *r = rem / width;
+    *c = cb * kColBlock + rem % width;
+}
+
+// Fills `list` with this workgroup's tiles and returns their number; *rows_end is the last
+// group's clamped end.  end_sh: the groups' clamped ends; first_sh: each group's first row tile.
+template <int P>
+__device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_sh, TileList& list, int* rows_end)
+{
+    const int t = (int)threadIdx.x, R = a.rows, S = a.split;
+    const int per = (a.G + kThreads - 1) / kThreads;
+    const int ga = t * per < a.G ? t * per : a.G, gb = ga + per < a.G ? ga + per : a.G;
+    int top = 0;
+    for (int g = ga; g < gb; ++g) {
+        const int e = a.offs[g];
+        top = e > top ? e : top;
+        end_sh[g] = top < a.M ? top : a.M;
+    }
+    const int upto = block_scan<true>(top, scan_sh);
+    scan_sh[t] = upto;
+    __syncthreads();
+    const int before = t ? scan_sh[t - 1] : 0;
+    const int base = before < a.M ? before : a.M;
+    for (int g = ga; g < gb; ++g) end_sh[g] = end_sh[g] > base ? end_sh[g] : base;
+    __syncthreads();
+
+    const int NC = (Shape<P>::cols(a.N, a.K) + kCols - 1) / kCols;
+    const int x = (int)blockIdx.x % kXcds, cu = (int)blockIdx.x / kXcds, cus = (int)gridDim.x / kXcds;
+    const int j = lane_id();
+    list.mine = Tile{0, 0, 0, 0, 0, 0, 0};
+    *rows_end = end_sh[a.G - 1];
+
+    if constexpr (Shape<P>::kDw) {
+        // Every group has the same tiles and its own length of sum: a round of one tile a
+        // CU is cut over the XCDs, so that each has its share of every group.
+        const int NR = (a.N + R - 1) / R, per_group = NR * NC * S;
+        const int V = a.G * per_group, grid = (int)gridDim.x;
+        const int full = V / grid, over = V - full * grid;
+        const int lo = (int)((int64_t)over * x / kXcds), last = (int)((int64_t)over * (x + 1) / kXcds) - lo;
+        const int count = full + (cu < last);
+        if (j < count) {
+            const int L = j < full ? j * grid + (x + j) % kXcds * cus + cu : full * grid + lo + cu;
+            Tile tl;
+            tl.g = L / per_group;
+            const int rem = L - tl.g * per_group;
+            int r;
+            place_in(rem / S, NR, NC, &r, &tl.c);
+            tl.r0 = r * R;
+            tl.r1 = tl.r0 + R < a.N ? tl.r0 + R : a.N;
+            const int start = tl.g ? end_sh[tl.g - 1] : 0;
+            part_of(tl, start, end_sh[tl.g] - start, rem % S, S);
+            list.mine = tl;
+        }
+        return count < kMaxEntries ? count : kMaxEntries;
+    }
+
+    int tiles = 0;
+    for (int g = ga, start = base; g < gb; ++g) {
+        tiles += (end_sh[g] - start + R - 1) / R;
+        start = end_sh[g];
+    }
+    int first = block_scan<false>(tiles, scan_sh) - tiles;
+    for (int g = ga, start = base; g < gb; ++g) {
+        first_sh[g] = first;
+        first += (end_sh[g] - start + R - 1) / R;
+        start = end_sh[g];
+    }
+    if (t == kThreads - 1) first_sh[a.G] = first;
+    __syncthreads();
+
+    // Each XCD walks one contiguous stretch, its CUs side by side; the tiles left after the
+    // last full round are cut in row parts of 64 or more while that gives no more than one for
+    // each CU.
+    const int V = first_sh[a.G] * NC * S;
+    const int lo = (int)((int64_t)V * x / kXcds), n = (int)((int64_t)V * (x + 1) / kXcds) - lo;
+    const int full = n / cus, over = n - full * cus;
+    const int parts = 4 * over <= cus && R == 256 ? 4 : 2 * over <= cus ? 2 : 1;
+    const int count = full + (cu < over * parts);
+    if (j < count) {
+        const int L = lo + j * cus + (j < full ? (cu + 6 * j) % cus : cu / parts);
+        const int V2 = L / S;
+        int p = 0, r = a.G - 1;                          // the last group whose tiles start at or before V2
+        while (p < r) {
+            const int mid = (p + r + 1) >> 1;
+            if (first_sh[mid] * NC <= V2) p = mid;
+            else r = mid - 1;
+        }
+        int rt;
+        Tile tl;
+        place_in(V2 - first_sh[p] * NC, first_sh[p + 1] - first_sh[p], NC, &rt, &tl.c);
+        const int height = j < full ? R : R / parts, part = j < full ? 0 : cu % parts;
+        tl.g = p;
+        tl.r0 = (p ? end_sh[p - 1] : 0) + rt * R + part * height;
+        tl.r1 = tl.r0 + height < end_sh[p] ? tl.r0 + height : end_sh[p];
+        if (tl.r1 < tl.r0) tl.r1 = tl.r0;                // a part past the group's rows
+        part_of(tl, 0, Shape<P>::depth(a.N, a.K), L % S, S);
+        list.mine = tl;
+    }
+    return count < kMaxEntries ? count : kMaxEntries;
+}
+
+// ------------------------------------------------------------------ loads ---
+// The stream of slots to load.  A wave loads a quarter of each operand's slot, 8 loads of 1 KB
+// of each.
+//
+// "Along": LDS rows of 128 bytes hold their eight 16-byte chunks at c ^ ((row >> 1) & 7): the
+// 16 lanes that a 128-bit LDS read serves at a time then meet 16 different bank groups.
+// "Across": LDS rows of 512 bytes hold their eight 64-byte parts at p ^ (row & 3): the four
+// rows of a transposing read then meet different banks.  The swizzles are applied to the
+// source offsets (the LDS side is linear in the lane).
+template <bool ACROSS>
+struct Operand {
+    v4i r;                                               // resource that starts at the next slot
+    int rows;                                            // ACROSS: the sum's values from the next slot on
+    uint32_t off[8];                                     // lane offsets of the wave's loads
+    uint32_t tail;                                       // bit 31 of bytes 0 and 2: this lane's chunk of even, odd loads is past a row's end
+
+    __device__ __forceinline__ void set_lanes(uint32_t ld, int depth, int wave, int lane)
+    {
+        if constexpr (ACROSS) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t row = (uint32_t)(16 * wave + 2 * i + (lane >> 5));
+                const uint32_t part = (((uint32_t)lane >> 2) & 7u) ^ (row & 3u);
+                off[i] = row * ld + 64u * part + 16u * ((uint32_t)lane & 3u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t row = (uint32_t)(64 * wave + 8 * i + (lane >> 3));
+                const uint32_t chunk = ((uint32_t)lane & 7u) ^ ((row >> 1) & 7u);
+                off[i] = row * ld + 16u * chunk;
+            }
+            const uint32_t even = ((uint32_t)lane & 7u) ^ ((uint32_t)lane >> 4), chunks = (uint32_t)(depth % kSlotK) / 8u;
+            tail = ((even >= chunks) << 0) | (((even ^ 4u) >= chunks) << 1);
+        }
+    }
+    // The last slot of a sum that ends inside it: chunks past the end load zeros (their lanes'
+    // offsets leave the resource).  Called again to undo it.
+    __device__ __forceinline__ void toggle_tail()
+    {
+        if constexpr (!ACROSS) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) off[i] ^= (tail << ((i & 1) ? 30 : 31)) & 0x80000000u;
+        }
+    }
+    // A tile's first slot: `base` its first value, n its rows of ld bytes ("along") or the sum's
+    // length ("across"); `skip` bytes of the first row come before it.
+    __device__ __forceinline__ void set(const uint16_t* base, int n, uint32_t ld, uint32_t skip)
+    {
+        rows = n;
+        const int used = ACROSS && n > kSlotK ? kSlotK : n;
+        r = resource(base, used > 0 ? (uint32_t)used * ld - skip : 0u);
+    }
+    // (Signed, so that the bound is a scalar maximum.)
+    __device__ __forceinline__ void step(uint32_t ld, uint32_t skip)
+    {
+        const uint32_t bytes = ACROSS ? kSlotK * ld : 2u * kSlotK;
+        const uint64_t base = (((uint64_t)(uint32_t)r.y << 32) | (uint32_t)r.x) + bytes;
+        int left;
+        if constexpr (ACROSS) {
+            rows -= kSlotK;
+            left = rows > kSlotK ? (int)(kSlotK * ld - skip) : rows > 0 ? (int)((uint32_t)rows * ld - skip) : 0;
+        } else {
+            left = r.z - (int)bytes > 0 ? r.z - (int)bytes : 0;
+        }
+        r = v4i{(int)(uint32_t)base, (int)(uint32_t)(base >> 32), left, 0x00020000};
+    }
+};
+
+template <int P>
+struct Loader {
+    using S = Shape<P>;
+    Operand<S::kAcrossA> a;
+    Operand<S::kAcrossB> b;
+    int entry, left;                                     // the tile's place in the list; its slots from the next one on
+    uint32_t skip_a, skip_b;                             // bytes of a memory row before the tile ("across")
+    bool ends, masked;                                   // the tile's sum ends inside its last slot; the tail is masked now
+    uint32_t lds_data;                                   // LDS address of the wave's part of ring slot 0
+
+    __device__ __forceinline__ void set_lanes(const MmArgs& m, const uint8_t* lds, int wave, int lane)
+    {
+        a.set_lanes(S::lda(m.N, m.K), S::depth(m.N, m.K), wave, lane);
+        b.set_lanes(S::ldb(m.N, m.K), S::depth(m.N, m.K), wave, lane);
+        lds_data = (uint32_t)uniform((int)((uint32_t)(uintptr_t)(LdsPtr)lds + 8192u * (uint32_t)wave));
+        masked = false;
+    }
+
+    // The first slot of tile `entry` of the list; past the list's end, one that loads nothing.
+    __device__ __forceinline__ void set_tile(const MmArgs& m, const TileList& list, int count)
+    {
+        const bool some = entry < count;
+        const Tile t = list.at(some ? entry : 0);
+        const int c0 = t.c * kCols, cols = S::cols(m.N, m.K), n = some ? t.k1 - t.k0 : 0;
+        const int width = !some ? 0 : cols - c0 < kCols ? cols - c0 : kCols;
+        left = some ? slots_of(t) : 1;
+        if constexpr (S::kDw) {
+            skip_a = 2u * (uint32_t)c0;
+            skip_b = 2u * (uint32_t)t.r0;
+            a.set(m.a + (int64_t)t.k0 * m.K + c0, n, S::lda(m.N, m.K), skip_a);
+            b.set(m.b + (int64_t)t.k0 * m.N + t.r0, n, S::ldb(m.N, m.K), skip_b);
+        } else {
+            const int64_t depth = S::depth(m.N, m.K);
+            if constexpr (S::kAcrossA) {
+                skip_a = 2u * (uint32_t)c0;
+                a.set(m.a + ((int64_t)t.g * m.N + t.k0) * m.K + c0, n, S::lda(m.N, m.K), skip_a);
+            } else {
+                skip_a = 2u * (uint32_t)t.k0;
+                a.set(m.a + ((int64_t)t.g * m.N + c0) * depth + t.k0, width, S::lda(m.N, m.K), skip_a);
+            }
+            skip_b = 2u * (uint32_t)t.k0;
+            b.set(m.b + (int64_t)t.r0 * depth + t.k0, some ? t.r1 - t.r0 : 0, S::ldb(m.N, m.K), skip_b);
+            ends = t.k1 % kSlotK != 0;
+        }
+        mask();
+    }
+    __device__ __forceinline__ void mask()
+    {
+        if constexpr (!S::kDw) {
+            const bool want = ends && left == 1;
+            if (want != masked) {
+                a.toggle_tail();
+                b.toggle_tail();
+                masked = want;
+            }
+        }
+    }
+    // On to the next slot of the stream.
+    __device__ __forceinline__ void advance(const MmArgs& m, const TileList& list, int count)
+    {
+        if (left == 1) {
+            ++entry;
+            set_tile(m, list, count);
+        } else {
+            --left;
+            a.step(S::lda(m.N, m.K), skip_a);
+            b.step(S::ldb(m.N, m.K), skip_b);
+            mask();
+        }
+    }
+    // Load I of the slot into ring slot s: A, then B.
+    template <int I>
+    __device__ __forceinline__ void issue(uint32_t s)
+    {
+        const uint32_t to = lds_data + s * kSlotBytes;
+        if constexpr (I < 8) load_to_lds(a.r, to + 1024u * I, a.off[I]);
+        else load_to_lds(b.r, to + kOperandBytes + 1024u * (I - 8), b.off[I - 8]);
+    }
+    template <int I, int END>
+    __device__ __forceinline__ void issue_some(uint32_t s)
+    {
+        if constexpr (I < END) {
+            issue<I>(s);
+            issue_some<I + 1, END>(s);
+        }
+    }
+};
+
+// --------------------------------------------------------------- products ---
+// In a 16-value step lane (r, h) = (lane % 32, lane / 32) holds the values 8h .. 8h + 7 of row
+// (or column) r of each 32-wide part.
+template <bool ACROSS, int T>
+struct Fragments {
+    v4i v[T];
+};
+
+// A lane's LDS addresses of an operand in the ring slot that is read: "along", by the step, for
+// part 0 (part i is 32 rows on); "across", by the part, for step 0 and the first of its two
+// reads (step n is 16 rows on, the second read four).
+template <bool ACROSS>
+struct Places {
+    uint32_t at[4];
+    // base: the operand's place in the slot; part: the wave's first 32-wide part.
+    __device__ __forceinline__ void set(uint32_t base, uint32_t part)
+    {
+        const uint32_t lane = (uint32_t)lane_id();
+#pragma unroll
+        for (uint32_t n = 0; n < 4; ++n) {
+            if constexpr (ACROSS) {                      // row 8h + s, four columns of one half of a 64-byte part
+                const uint32_t s = (lane >> 2) & 3u;
+                at[n] = base + (8u * (lane >> 5) + s) * 512u + (((part + n) ^ s) << 6) + 32u * ((lane >> 4) & 1u) + 8u * (lane & 3u);
+            } else {                                     // row r, chunk 2n + h
+                at[n] = base + (32u * part + (lane & 31u)) * 128u + (((2u * n + (lane >> 5)) ^ ((lane >> 1) & 7u)) << 4);
+            }
+        }
+    }
+    __device__ __forceinline__ void other_slot()
+    {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) at[n] ^= kSlotBytes;
+    }
+};
+
+// Piece Q of a step's operand (0 .. T - 1, twice that "across").
+template <bool ACROSS, int ST, int Q, int T>
+__device__ __forceinline__ void read_piece(Fragments<ACROSS, T>& f, const Places<ACROSS>& l)
+{
+    if constexpr (ACROSS) {
+        constexpr int i = Q / 2, half = Q % 2;
+        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)(l.at[i] + 8192u * ST + 2048u * half));
+        const uint2 w = __builtin_bit_cast(uint2, v);
+        f.v[i][2 * half] = (int)w.x;
+        f.v[i][2 * half + 1] = (int)w.y;
+    } else {
+        f.v[Q] = *(LdsV4i)(uintptr_t)(l.at[ST] + 4096u * Q);
+    }
+}
+template <int P>
+struct Lane {
+    uint32_t row, h;
+    uint32_t wn, wm;                                     // the wave's place in the 2 x 2
+    Places<Shape<P>::kAcrossA> a;
+    Places<Shape<P>::kAcrossB> b;
+};
+template <int P, int TM>
+struct Operands {
+    Fragments<Shape<P>::kAcrossA, 4> a;
+    Fragments<Shape<P>::kAcrossB, TM> b;
+};
+template <int P, int TM>
+constexpr int kPieces = 4 * (Shape<P>::kAcrossA ? 2 : 1) + TM * (Shape<P>::kAcrossB ? 2 : 1);
+// Pieces Q .. END - 1 of step ST's operands.
+template <int P, int TM, int ST, int Q, int END>
+__device__ __forceinline__ void read_step(Operands<P, TM>& f, const Lane<P>& l)
+{
+    if constexpr (Q < END) {
+        constexpr int na = 4 * (Shape<P>::kAcrossA ? 2 : 1);
+        if constexpr (Q < na) read_piece<Shape<P>::kAcrossA, ST, Q>(f.a, l.a);
+        else read_piece<Shape<P>::kAcrossB, ST, Q - na>(f.b, l.b);
+        read_step<P, TM, ST, Q + 1, END>(f, l);
+    }
+}
+
+// MFMAs I .. END - 1 of a step, each followed by its share of the other work of that stretch:
+// work(k, n) does part k of n.  ZERO: the sums start here.
+template <int P, int TM, bool ZERO, int I, int END, int K = 0, class Work>
+__device__ __forceinline__ void mfmas(v16f (&acc)[4][TM], const Operands<P, TM>& f, const Work& work)
+{
+    if constexpr (I < END) {
+        constexpr int i = I / TM, j = I % TM;
+        v16f c = acc[i][j];
+        if constexpr (ZERO) c = v16f{};
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, f.a.v[i]), __builtin_bit_cast(v8bf, f.b.v[j]),
+                                                            c, 0, 0, 0);
+        work(Int<K>{}, Int<K + END - I>{});
+        __builtin_amdgcn_sched_barrier(0);
+        mfmas<P, TM, ZERO, I + 1, END, K + 1>(acc, f, work);
+    }
+}
+// The bounds of part k of n of a .. b.
+#define MXQ_PART(a, b) (a) + K.value * ((b) - (a)) / N.value, (a) + (K.value + 1) * ((b) - (a)) / N.value
+
+// The order of a slot's four steps in halves, what is loaded under each (16 loads a slot), and
+// the barriers between them ("read": all waves' LDS reads are done; "there": all waves' loads
+// have landed):
+//   step 0        slot + 1: 8 .. 13
+//   step 1        slot + 1: 14, 15
+//   step 2        (the slot is read)
+//     2nd half    slot + 2: 0, 1
+//   step 3        slot + 2: 2 .. 4
+//                 (slot + 1 is there)
+//     2nd half    slot + 2: 5 .. 7
+// A place in LDS is loaded anew from half a step after its last operands were asked for, and
+// waited for half a step before its first are used.
+constexpr int kLoads2 = 2, kLoads3 = 5, kLoads3b = 8, kLoads0 = 14;   // loads issued by the end of each stretch
+
+template <int P, int TM, bool FIRST>
+__device__ __forceinline__ void steps01(v16f (&acc)[4][TM], Operands<P, TM> (&f)[2], Loader<P>& ld, const Lane<P>& l, uint32_t s)
+{
+    constexpr int h = 2 * TM, n = 4 * TM, Q = kPieces<P, TM>;
+    __builtin_amdgcn_sched_barrier(0);
+    mfmas<P, TM, FIRST, 0, n>(acc, f[0], [&](auto K, auto N) {
+        read_step<P, TM, 1, MXQ_PART(0, Q)>(f[1], l);
+        ld.template issue_some<MXQ_PART(kLoads3b, kLoads0)>(s ^ 1u);
+    });
+    mfmas<P, TM, false, 0, h>(acc, f[1], [&](auto K, auto N) {
+        ld.template issue_some<MXQ_PART(kLoads0, 16)>(s ^ 1u);
+        read_step<P, TM, 2, MXQ_PART(0, Q / 2)>(f[0], l);
+    });
+    mfmas<P, TM, false, h, n>(acc, f[1], [&](auto K, auto N) { read_step<P, TM, 2, MXQ_PART(Q / 2, Q)>(f[0], l); });
+}
+
+// On exit f[0] holds the next slot's first step, unless this is the tile's LAST.
+template <int P, int TM, bool LAST>
+__device__ __forceinline__ void steps23(v16f (&acc)[4][TM], Operands<P, TM> (&f)[2], Loader<P>& ld, Lane<P>& l, uint32_t s)
+{
+    constexpr int h = 2 * TM, n = 4 * TM, Q = kPieces<P, TM>;
+    mfmas<P, TM, false, 0, h>(acc, f[0], [&](auto K, auto N) { read_step<P, TM, 3, MXQ_PART(0, Q)>(f[1], l); });
+    l.a.other_slot();
+    l.b.other_slot();
+    slot_barrier<63>();
+    mfmas<P, TM, false, h, n>(acc, f[0], [&](auto K, auto N) { ld.template issue_some<MXQ_PART(0, kLoads2)>(s); });
+    mfmas<P, TM, false, 0, h>(acc, f[1], [&](auto K, auto N) { ld.template issue_some<MXQ_PART(kLoads2, kLoads3)>(s); });
+    slot_barrier<kLoads3>();                             // (newer: the slot after it)
+    mfmas<P, TM, false, h, n>(acc, f[1], [&](auto K, auto N) {
+        if constexpr (!LAST) read_step<P, TM, 0, MXQ_PART(0, Q)>(f[0], l);
+        ld.template issue_some<MXQ_PART(kLoads3, kLoads3b)>(s);
+    });
+}
+#undef MXQ_PART
+
+// The sums are needed here: without this the compiler moves MFMAs past the loads that are meant
+// to run under them, into the next basic block.
+template <int TM>
+__device__ __forceinline__ void pin(v16f (&acc)[4][TM])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) asm volatile("" : "+a"(acc[i][j]));
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Stores: lane (r, h) holds, of row r of each 32 x 32 part, columns 8 q + 4 h .. + 3 for
+// q = 0 .. 3.  bf16: the halves of the wave exchange every other 4 columns, so that a lane
+// has 8 consecutive ones (16 bytes); then pieces change lanes so that stores cover whole lines.
+template <int P, int TM, bool F32OUT, bool ADD>
+__device__ __forceinline__ void store_tile(const v16f (&acc)[4][TM], const MmArgs& a, const Tile& t, const Lane<P>& l)
+{
+    constexpr int kSize = F32OUT ? 4 : 2, kParts = F32OUT ? 1 : 2;
+    const int cols = Shape<P>::cols(a.N, a.K);
+    const int r1 = ADD && t.k0 == t.k1 ? t.r0 : t.r1;    // (nothing to add: nothing is touched)
+    const int64_t rows_before = (int64_t)t.part * (Shape<P>::kDw ? (int64_t)a.G * a.N : a.M) + (Shape<P>::kDw ? (int64_t)t.g * a.N : 0);
+    uint8_t* out = (uint8_t*)a.out + rows_before * cols * kSize;
+    const int n_lane = (int)(64u * (l.row >> 3 & 1u) + 32u * (l.row >> 4) + 16u * l.h) / kSize;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+        const int m = t.r0 + (int)(32u * TM * l.wm + 32u * j + (l.row & 7u));
+#pragma unroll
+        for (int i = 0; i < 4; i += kParts) {
+            __builtin_amdgcn_sched_barrier(0);           // (one block at a time in VGPRs)
+            v4i p[4];
+            if constexpr (F32OUT) {
+                const v16f& v = acc[i][j];
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) p[s][k] = __float_as_int(v[4 * s + k]);
+            } else {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const v16f& v = acc[i + s / 2][j];
+                    const int q = 8 * (s % 2);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const auto w = __builtin_amdgcn_permlane32_swap(f32_pair_to_bf16(v[q + 2 * k], v[q + 2 * k + 1]),
+                                                                        f32_pair_to_bf16(v[q + 2 * k + 4], v[q + 2 * k + 5]), false, false);
+                        p[s][k] = (int)w[0];
+                        p[s][k + 2] = (int)w[1];
+                    }
+                }
+            }
+            join_lines(p);
+            const int n = t.c * kCols + (int)(128u * l.wn) + 32 * i + n_lane;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int row = m + 16 * (s % 2) + 8 * (s / 2);
+                if (row < r1 && n < cols) {
+                    v4i* to = (v4i*)(out + ((int64_t)row * cols + n) * kSize);
+                    if constexpr (ADD) {
+                        const v4i old = *to;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) p[s][k] = __float_as_int(__int_as_float(old[k]) + __int_as_float(p[s][k]));
+                    }
+                    *to = p[s];
+                }
+            }
+        }
+    }
+}
+
+// One tile: its slots are the next to come out of the stream, the first of them in ring slot s;
+// the loads are part way into the slot after it.
+template <int P, int TM, bool F32OUT, bool ADD>
+__device__ __forceinline__ void tile_product(Loader<P>& ld, const MmArgs& a, const TileList& list, int count, const Tile& t,
+                                             Lane<P>& l, uint32_t base, uint32_t& s)
+{
+    v16f acc[4][TM];
+    Operands<P, TM> f[2];
+    l.b.set(base + s * kSlotBytes + kOperandBytes, TM * l.wm);
+    const int nslots = uniform(slots_of(t));
+    s = (uint32_t)uniform((int)s);                       // (a scalar register's, which the loads' M0 needs)
+    read_step<P, TM, 0, 0, kPieces<P, TM>>(f[0], l);
+    steps01<P, TM, true>(acc, f, ld, l, s);
+    pin<TM>(acc);
+    ld.advance(a, list, count);
+    for (int i = 1; i < nslots; ++i) {
+        steps23<P, TM, false>(acc, f, ld, l, s);
+        pin<TM>(acc);
+        s ^= 1u;
+        steps01<P, TM, false>(acc, f, ld, l, s);
+        pin<TM>(acc);
+        ld.advance(a, list, count);
+    }
+    steps23<P, TM, true>(acc, f, ld, l, s);
+    pin<TM>(acc);
+    s ^= 1u;
+    store_tile<P, TM, F32OUT, ADD>(acc, a, t, l);
+}
+
+template <int P, bool F32OUT, bool ADD>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void bf16_mm_kernel(const MmArgs a)
 {
-    constexpr bool dw = PRODUCT == MXQ_PRODUCT_DW;
-    const int lane = lane_id(), r = lane & 31, h = lane >> 5;
-    const int cols = PRODUCT == MXQ_PRODUCT_Y ? a.N : a.K;
-    const int c0 = (int)blockIdx.x * 32;
-    // group and rows of this tile
-    int g = 0, lo = 0, hi = 0, tile = (int)blockIdx.y;
-    if (dw) g = (int)blockIdx.z;
-    int end = 0;
-    for (int i = 0; i < a.G; ++i) {
-        int e = a.offs[i];
-        e = e > end ? (e < a.M ? e : a.M) : end;
-        const int tiles = (e - end + 31) / 32;
-        if (dw ? i == g : tile < tiles) {
-            g = i;
-            lo = end;
-            hi = e;
-            break;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLdsBytes];
+    const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
+    TileList list;
+    int rows_end;
+    int count;
+    {
+        int* end_sh = (int*)lds;
+        int* first_sh = end_sh + kMaxGroups + 1;
+        int* scan_sh = first_sh + kMaxGroups + 1;
+        count = uniform(make_list<P>(a, end_sh, first_sh, scan_sh, list, &rows_end));
+        rows_end = uniform(rows_end);
+    }
+    __syncthreads();                                     // the scan's arrays are free
+    if (count > 0) {
+        const Tile last = list.at(count - 1);
+        if (last.r0 == last.r1) --count;
+    }
+
+    if (count > 0) {
+        Lane<P> l;
+        l.row = (uint32_t)(lane & 31);
+        l.h = (uint32_t)(lane >> 5);
+        l.wn = (uint32_t)(wave >> 1);
+        l.wm = (uint32_t)(wave & 1);
+        const uint32_t base = (uint32_t)(uintptr_t)(LdsPtr)lds;
+        l.a.set(base, 4 * l.wn);
+        Loader<P> ld;
+        ld.set_lanes(a, lds, wave, lane);
+        ld.entry = 0;
+        ld.set_tile(a, list, count);
+        ld.template issue_some<0, 16>(0);
+        ld.advance(a, list, count);
+        ld.template issue_some<0, kLoads3b>(1);
+        slot_barrier<0>();
+        uint32_t s = 0;
+        for (int e = 0; e < count; ++e) {
+            const Tile t = list.at(e);
+            // a group's last tile runs at the smallest of three heights that holds its rows
+            const int rows = t.r1 - t.r0;
+            if (rows > 128) tile_product<P, 4, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
+            else if (rows > 64) tile_product<P, 2, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
+            else tile_product<P, 1, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
         }
-        if (!dw) tile -= tiles;
-        end = e;
+        slot_barrier<0>();                               // the loads past the end land before the LDS goes away
     }
-    const bool zeros = !dw && lo == hi;                    // rows past the last end
-    int row0 = 0, rows = a.N;
-    const uint16_t *A, *B;
-    int64_t lda, ldb;
-    int depth;
-    if (dw) {
-        row0 = (int)blockIdx.y * 32;
-        depth = hi - lo;
-        B = a.rows + (int64_t)lo * a.N;
-        A = a.other + (int64_t)lo * a.K;
-        ldb = a.N, lda = a.K;
-    } else {
-        row0 = zeros ? end + tile * 32 : lo + tile * 32;
-        rows = zeros ? a.M : hi;
-        depth = zeros ? 0 : PRODUCT == MXQ_PRODUCT_Y ? a.K : a.N;
-        B = a.rows;
-        A = a.other + (int64_t)g * a.N * a.K;
-        ldb = PRODUCT == MXQ_PRODUCT_Y ? a.K : a.N, lda = a.K;
+
+    if constexpr (!Shape<P>::kDw) {                      // rows past the last end: zeros, in every part
+        const int64_t per_row = (int64_t)Shape<P>::cols(a.N, a.K) * (F32OUT ? 4 : 2) / 16;
+        const int64_t total = (int64_t)(a.M - rows_end) * per_row;
+        for (int p = 0; p < a.split; ++p) {
+            uint4* y = (uint4*)a.out + ((int64_t)p * a.M + rows_end) * per_row;
+            for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads)
+                y[i] = make_uint4(0, 0, 0, 0);
+        }
     }
-    if (row0 >= rows) return;
-    v16f acc = {};
-    for (int k = 0; k < depth; k += 16) {
-        const v8u16 fa = operand<PRODUCT != MXQ_PRODUCT_Y>(A, lda, c0 + r, cols, k + 8 * h, depth);
-        const v8u16 fb = operand<dw>(B, ldb, row0 + r, rows, k + 8 * h, depth);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fa), __builtin_bit_cast(v8bf, fb), acc, 0, 0, 0);
+}
+
+// out = the sum of `parts` arrays of n4 float4, in order (and of what out holds).
+template <bool F32OUT>
+__global__ __launch_bounds__(kThreads)
+void join_parts_kernel(const float4* __restrict__ part, int parts, int64_t n4, void* out, int accumulate)
+{
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n4; i += (int64_t)gridDim.x * kThreads) {
+        float4 v = part[i];
+        for (int p = 1; p < parts; ++p) {
+            const float4 w = part[p * n4 + i];
+            v.x += w.x;
+            v.y += w.y;
+            v.z += w.z;
+            v.w += w.w;
+        }
+        if constexpr (F32OUT) {
+            float4* to = (float4*)out + i;
+            if (accumulate) {
+                const float4 w = *to;
+                v.x += w.x;
+                v.y += w.y;
+                v.z += w.z;
+                v.w += w.w;
+            }
+            *to = v;
+        } else {
+            ((uint2*)out)[i] = make_uint2(f32_pair_to_bf16(v.x, v.y), f32_pair_to_bf16(v.z, v.w));
+        }
     }
-    if (row0 + r >= rows) return;
-    const int64_t at = ((dw ? (int64_t)g * a.N : 0) + row0 + r) * cols;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int c = c0 + 8 * (i / 4) + 4 * h + i % 4;
-        if (c >= cols) continue;
-        if constexpr (F32OUT) ((float*)a.out)[at + c] = a.accumulate ? ((float*)a.out)[at + c] + acc[i] : acc[i];
-        else ((__bf16*)a.out)[at + c] = (__bf16)acc[i];
-    }
+}
+
+// How a product is cut: rows of a tile, parts of its sum, tiles at most (parts counted).
+struct Plan {
+    int rows, split;
+    int64_t items;
+};
+constexpr int kCus = 256;
+Plan plan_of(int product, int64_t M, int64_t N, int64_t K, int64_t G)
+{
+    const bool dw = product == MXQ_PRODUCT_DW;
+    const int64_t cols = ((product == MXQ_PRODUCT_Y ? N : K) + kCols - 1) / kCols;
+    const auto tiles = [&](int rows) {
+        return (dw ? G * ((N + rows - 1) / rows) : (M + rows - 1) / rows + (G < M ? G : M) - 1) * cols;
+    };
+    Plan p;
+    p.rows = tiles(256) >= kCus ? 256 : 128;
+    const int64_t n = tiles(p.rows);
+    // slots of an average sum; a part has four or more
+    const int64_t slots = ((dw ? M / G : product == MXQ_PRODUCT_Y ? K : N) + kSlotK - 1) / kSlotK;
+    int64_t split = n > 0 ? kCus / n : 1;
+    if (split > slots / 4) split = slots / 4;
+    if (split > kMaxSplit) split = kMaxSplit;
+    p.split = split < 1 ? 1 : (int)split;
+    p.items = n * p.split;
+    return p;
+}
+int64_t results_of(int product, int64_t M, int64_t N, int64_t K, int64_t G)
+{
+    return product == MXQ_PRODUCT_Y ? M * N : product == MXQ_PRODUCT_DX ? M * K : G * N * K;
 }
 
 }  // namespace
@@ -106,7 +737,7 @@ void bf16_mm_kernel(const MmArgs a)
 bool bf16_mm_sizes_ok(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 {
     constexpr int64_t kMaxSide = (int64_t)1 << 20;
-    if (M < 0 || M > ((int64_t)1 << 31) - 1024 || G < 1 || G > 4095) return false;
+    if (M < 0 || M > ((int64_t)1 << 31) - 1024 || G < 1 || G > kMaxGroups) return false;
     if (N < 8 || N > kMaxSide || N % 8 != 0 || K < 8 || K > kMaxSide || K % 8 != 0) return false;
     if (G * N * K > (int64_t)1 << 40) return false;
     const int64_t rows = product == MXQ_PRODUCT_DW ? G * ((N + 63) / 64) : M / 64 + G;
@@ -114,24 +745,52 @@ bool bf16_mm_sizes_ok(int product, int64_t M, int64_t N, int64_t K, int64_t G)
     return rows < ((int64_t)1 << 30) / cols;
 }
 
-size_t bf16_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int64_t G) { return 0; }
+size_t bf16_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int64_t G)
+{
+    if (M == 0) return 0;
+    const int split = plan_of(product, M, N, K, G).split;
+    return split > 1 ? (size_t)split * (size_t)results_of(product, M, N, K, G) * 4u : 0;
+}
 
 hipError_t launch_bf16_mm(int product, const void* rows, const void* other, const int32_t* offs, int M, int N, int K, int G,
                           void* out, bool f32_out, bool accumulate, void* workspace, hipStream_t stream)
 {
-    const MmArgs a = {(const uint16_t*)rows, (const uint16_t*)other, offs, out, M, N, K, G, accumulate};
-    const unsigned cols = (unsigned)(((product == MXQ_PRODUCT_Y ? N : K) + 31) / 32);
-    const dim3 grid = product == MXQ_PRODUCT_DW ? dim3(cols, (unsigned)((N + 31) / 32), (unsigned)G)
-                                                : dim3(cols, (unsigned)(M / 32 + G + 1));
-#define MXQ_LAUNCH(P)                                                                                     \
-    do {                                                                                                  \
-        if (f32_out) hipLaunchKernelGGL((bf16_mm_kernel<P, true>), grid, dim3(64), 0, stream, a);         \
-        else hipLaunchKernelGGL((bf16_mm_kernel<P, false>), grid, dim3(64), 0, stream, a);                \
-    } while (0)
-    if (product == MXQ_PRODUCT_Y) MXQ_LAUNCH(MXQ_PRODUCT_Y);
-    else if (product == MXQ_PRODUCT_DX) MXQ_LAUNCH(MXQ_PRODUCT_DX);
-    else MXQ_LAUNCH(MXQ_PRODUCT_DW);
+    int device = 0, cus = 0;
+    hipError_t e = hipGetDevice(&device);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+    if (e != hipSuccess) return e;
+    const Plan p = plan_of(product, M, N, K, G);
+    const bool joined = M > 0 && p.split > 1;
+    // One workgroup a CU, fewer when there are not that many tiles (their row parts counted),
+    // a multiple of it when a workgroup's list would not hold its tiles: it has at most
+    // (items + 8) / grid + 1.
+    const int64_t parts = p.items * (p.rows / 64);
+    int64_t grid = parts < cus ? (parts > 0 ? parts : 1) : cus;
+    grid *= (p.items + kXcds + grid * (kMaxEntries - 1) - 1) / (grid * (kMaxEntries - 1));
+    grid = (grid + kXcds - 1) / kXcds * kXcds;
+    const bool wide = f32_out || joined;
+    const MmArgs a = {(const uint16_t*)other, (const uint16_t*)rows, offs, joined ? workspace : out, M, N, K, G, p.rows,
+                      joined ? p.split : 1};
+#define MXQ_LAUNCH(P, F32, ADD) \
+    hipLaunchKernelGGL((bf16_mm_kernel<P, F32, ADD>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a)
+    if (product == MXQ_PRODUCT_DW && accumulate && !joined) MXQ_LAUNCH(MXQ_PRODUCT_DW, true, true);
+    else if (product == MXQ_PRODUCT_DW && wide) MXQ_LAUNCH(MXQ_PRODUCT_DW, true, false);
+    else if (product == MXQ_PRODUCT_DW) MXQ_LAUNCH(MXQ_PRODUCT_DW, false, false);
+    else if (product == MXQ_PRODUCT_DX && wide) MXQ_LAUNCH(MXQ_PRODUCT_DX, true, false);
+    else if (product == MXQ_PRODUCT_DX) MXQ_LAUNCH(MXQ_PRODUCT_DX, false, false);
+    else if (wide) MXQ_LAUNCH(MXQ_PRODUCT_Y, true, false);
+    else MXQ_LAUNCH(MXQ_PRODUCT_Y, false, false);
 #undef MXQ_LAUNCH
+    if (joined) {
+        const int64_t n4 = results_of(product, M, N, K, G) / 4;
+        const int64_t blocks = (n4 + kThreads - 1) / kThreads;
+        const dim3 g((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
+        if (f32_out)
+            hipLaunchKernelGGL(join_parts_kernel<true>, g, dim3(kThreads), 0, stream, (const float4*)workspace, p.split, n4, out,
+                               (int)accumulate);
+        else
+            hipLaunchKernelGGL(join_parts_kernel<false>, g, dim3(kThreads), 0, stream, (const float4*)workspace, p.split, n4, out, 0);
+    }
     return hipGetLastError();
 }
 
