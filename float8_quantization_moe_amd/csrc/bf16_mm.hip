@@ -46,6 +46,7 @@ constexpr int kMaxSplit = 16;
 static_assert((2 * (kMaxGroups + 2) + kThreads) * 4 <= (int)kLdsBytes, "the scan's arrays fit the ring");
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i* LdsV4i;
 typedef __attribute__((address_space(3))) v4s* LdsV4s;
@@ -218,9 +219,11 @@ __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_
 //
 // "Along": LDS rows of 128 bytes hold their eight 16-byte chunks at c ^ ((row >> 1) & 7): the
 // 16 lanes that a 128-bit LDS read serves at a time then meet 16 different bank groups.
-// "Across": LDS rows of 512 bytes hold their eight 64-byte parts at p ^ (row & 3): the four
-// rows of a transposing read then meet different banks.  The swizzles are applied to the
-// source offsets (the LDS side is linear in the lane).
+// "Across": LDS rows of 512 bytes hold their sixteen 32-byte parts at p ^ across_swizzle(row):
+// the four rows of a transposing read, and those eight rows on, then meet different banks.  The
+// swizzles are applied to the source offsets (the LDS side is linear in the lane).
+__device__ __forceinline__ uint32_t across_swizzle(uint32_t row) { return 2u * (row & 3u) + (row >> 3 & 1u); }
+
 template <bool ACROSS>
 struct Operand {
     v4i r;                                               // resource that starts at the next slot
@@ -234,8 +237,8 @@ struct Operand {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t row = (uint32_t)(16 * wave + 2 * i + (lane >> 5));
-                const uint32_t part = (((uint32_t)lane >> 2) & 7u) ^ (row & 3u);
-                off[i] = row * ld + 64u * part + 16u * ((uint32_t)lane & 3u);
+                const uint32_t part = (((uint32_t)lane >> 1) & 15u) ^ across_swizzle(row);
+                off[i] = row * ld + 32u * part + 16u * ((uint32_t)lane & 1u);
             }
         } else {
 #pragma unroll
@@ -288,7 +291,7 @@ struct Loader {
     Operand<S::kAcrossB> b;
     int entry, left;                                     // the tile's place in the list; its slots from the next one on
     uint32_t skip_a, skip_b;                             // bytes of a memory row before the tile ("across")
-    bool ends, masked;                                   // the tile's sum ends inside its last slot; the tail is masked now
+    int ends, masked;                                    // the tile's sum ends inside its last slot; the tail is masked now
     uint32_t lds_data;                                   // LDS address of the wave's part of ring slot 0
 
     __device__ __forceinline__ void set_lanes(const MmArgs& m, const uint8_t* lds, int wave, int lane)
@@ -296,7 +299,26 @@ struct Loader {
         a.set_lanes(S::lda(m.N, m.K), S::depth(m.N, m.K), wave, lane);
         b.set_lanes(S::ldb(m.N, m.K), S::depth(m.N, m.K), wave, lane);
         lds_data = (uint32_t)uniform((int)((uint32_t)(uintptr_t)(LdsPtr)lds + 8192u * (uint32_t)wave));
-        masked = false;
+        masked = ends = 0;
+    }
+
+    // The scalar state that a tile starts from, in scalar registers (after the divergent stores
+    // of the last one the compiler would keep it in vector registers).
+    __device__ __forceinline__ void make_uniform()
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            a.r[k] = uniform(a.r[k]);
+            b.r[k] = uniform(b.r[k]);
+        }
+        a.rows = uniform(a.rows);
+        b.rows = uniform(b.rows);
+        entry = uniform(entry);
+        left = uniform(left);
+        skip_a = (uint32_t)uniform((int)skip_a);
+        skip_b = (uint32_t)uniform((int)skip_b);
+        ends = uniform(ends);
+        masked = uniform(masked);
     }
 
     // The first slot of tile `entry` of the list; past the list's end, one that loads nothing.
@@ -330,7 +352,7 @@ struct Loader {
     __device__ __forceinline__ void mask()
     {
         if constexpr (!S::kDw) {
-            const bool want = ends && left == 1;
+            const int want = ends && left == 1;
             if (want != masked) {
                 a.toggle_tail();
                 b.toggle_tail();
@@ -370,245 +392,230 @@ struct Loader {
 };
 
 // --------------------------------------------------------------- products ---
-// In a 16-value step lane (r, h) = (lane % 32, lane / 32) holds the values 8h .. 8h + 7 of row
-// (or column) r of each 32-wide part.
-template <bool ACROSS, int T>
+// v_mfma_f32_16x16x32_bf16 and not 32x32x16: of the same rate, it moves half the accumulators a
+// flop, and the clock follows the power (loops of nothing else on random values: 1.94 against 1.71
+// PFLOP/s).  In a 32-value step lane (r, q) = (lane % 16, lane / 16) holds the values 8q .. 8q + 7
+// of row (or column) r of each 16-wide part.  A wave has 8 parts of A and TB of B.
+template <int T>
 struct Fragments {
     v4i v[T];
 };
 
 // A lane's LDS addresses of an operand in the ring slot that is read: "along", by the step, for
-// part 0 (part i is 32 rows on); "across", by the part, for step 0 and the first of its two
-// reads (step n is 16 rows on, the second read four).
+// part 0 (part i is 16 rows on); "across", by the part, for step 0 and the first of its two
+// reads (step n is 32 rows on, the second read four).
 template <bool ACROSS>
 struct Places {
-    uint32_t at[4];
-    // base: the operand's place in the slot; part: the wave's first 32-wide part.
+    static constexpr int kN = ACROSS ? 8 : 2;
+    uint32_t at[kN];
+    // base: the operand's place in the slot; part: the wave's first 16-wide part.
     __device__ __forceinline__ void set(uint32_t base, uint32_t part)
     {
-        const uint32_t lane = (uint32_t)lane_id();
+        const uint32_t lane = (uint32_t)lane_id(), q = lane >> 4;
 #pragma unroll
-        for (uint32_t n = 0; n < 4; ++n) {
-            if constexpr (ACROSS) {                      // row 8h + s, four columns of one half of a 64-byte part
-                const uint32_t s = (lane >> 2) & 3u;
-                at[n] = base + (8u * (lane >> 5) + s) * 512u + (((part + n) ^ s) << 6) + 32u * ((lane >> 4) & 1u) + 8u * (lane & 3u);
-            } else {                                     // row r, chunk 2n + h
-                at[n] = base + (32u * part + (lane & 31u)) * 128u + (((2u * n + (lane >> 5)) ^ ((lane >> 1) & 7u)) << 4);
+        for (uint32_t n = 0; n < kN; ++n) {
+            if constexpr (ACROSS) {                      // row 8q + s, four columns of a 32-byte part
+                const uint32_t s = (lane >> 2) & 3u, row = 8u * q + s;
+                at[n] = base + row * 512u + (((part + n) ^ across_swizzle(row)) << 5) + 8u * (lane & 3u);
+            } else {                                     // row r, chunk 4n + q
+                at[n] = base + (16u * part + (lane & 15u)) * 128u + (((4u * n + q) ^ ((lane >> 1) & 7u)) << 4);
             }
         }
     }
     __device__ __forceinline__ void other_slot()
     {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) at[n] ^= kSlotBytes;
+        for (int n = 0; n < kN; ++n) at[n] ^= kSlotBytes;
     }
 };
 
 // Piece Q of a step's operand (0 .. T - 1, twice that "across").
 template <bool ACROSS, int ST, int Q, int T>
-__device__ __forceinline__ void read_piece(Fragments<ACROSS, T>& f, const Places<ACROSS>& l)
+__device__ __forceinline__ void read_piece(Fragments<T>& f, const Places<ACROSS>& l)
 {
     if constexpr (ACROSS) {
         constexpr int i = Q / 2, half = Q % 2;
-        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)(l.at[i] + 8192u * ST + 2048u * half));
+        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)(l.at[i] + 16384u * ST + 2048u * half));
         const uint2 w = __builtin_bit_cast(uint2, v);
         f.v[i][2 * half] = (int)w.x;
         f.v[i][2 * half + 1] = (int)w.y;
     } else {
-        f.v[Q] = *(LdsV4i)(uintptr_t)(l.at[ST] + 4096u * Q);
+        f.v[Q] = *(LdsV4i)(uintptr_t)(l.at[ST] + 2048u * Q);
     }
 }
 template <int P>
 struct Lane {
-    uint32_t row, h;
+    uint32_t row, q;
     uint32_t wn, wm;                                     // the wave's place in the 2 x 2
     Places<Shape<P>::kAcrossA> a;
     Places<Shape<P>::kAcrossB> b;
 };
-template <int P, int TM>
+template <int TB>
 struct Operands {
-    Fragments<Shape<P>::kAcrossA, 4> a;
-    Fragments<Shape<P>::kAcrossB, TM> b;
+    Fragments<8> a;
+    Fragments<TB> b;
 };
-template <int P, int TM>
-constexpr int kPieces = 4 * (Shape<P>::kAcrossA ? 2 : 1) + TM * (Shape<P>::kAcrossB ? 2 : 1);
+template <int P, int TB>
+constexpr int kPieces = 8 * (Shape<P>::kAcrossA ? 2 : 1) + TB * (Shape<P>::kAcrossB ? 2 : 1);
 // Pieces Q .. END - 1 of step ST's operands.
-template <int P, int TM, int ST, int Q, int END>
-__device__ __forceinline__ void read_step(Operands<P, TM>& f, const Lane<P>& l)
+template <int P, int TB, int ST, int Q, int END>
+__device__ __forceinline__ void read_step(Operands<TB>& f, const Lane<P>& l)
 {
     if constexpr (Q < END) {
-        constexpr int na = 4 * (Shape<P>::kAcrossA ? 2 : 1);
+        constexpr int na = 8 * (Shape<P>::kAcrossA ? 2 : 1);
         if constexpr (Q < na) read_piece<Shape<P>::kAcrossA, ST, Q>(f.a, l.a);
         else read_piece<Shape<P>::kAcrossB, ST, Q - na>(f.b, l.b);
-        read_step<P, TM, ST, Q + 1, END>(f, l);
+        read_step<P, TB, ST, Q + 1, END>(f, l);
     }
 }
 
 // MFMAs I .. END - 1 of a step, each followed by its share of the other work of that stretch:
 // work(k, n) does part k of n.  ZERO: the sums start here.
-template <int P, int TM, bool ZERO, int I, int END, int K = 0, class Work>
-__device__ __forceinline__ void mfmas(v16f (&acc)[4][TM], const Operands<P, TM>& f, const Work& work)
+template <int TB, bool ZERO, int I, int END, int K = 0, class Work>
+__device__ __forceinline__ void mfmas(v4f (&acc)[8][TB], const Operands<TB>& f, const Work& work)
 {
     if constexpr (I < END) {
-        constexpr int i = I / TM, j = I % TM;
-        v16f c = acc[i][j];
-        if constexpr (ZERO) c = v16f{};
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, f.a.v[i]), __builtin_bit_cast(v8bf, f.b.v[j]),
+        constexpr int i = I / TB, j = I % TB;
+        v4f c = acc[i][j];
+        if constexpr (ZERO) c = v4f{};
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, f.a.v[i]), __builtin_bit_cast(v8bf, f.b.v[j]),
                                                             c, 0, 0, 0);
         work(Int<K>{}, Int<K + END - I>{});
         __builtin_amdgcn_sched_barrier(0);
-        mfmas<P, TM, ZERO, I + 1, END, K + 1>(acc, f, work);
+        mfmas<TB, ZERO, I + 1, END, K + 1>(acc, f, work);
     }
 }
 // The bounds of part k of n of a .. b.
 #define MXQ_PART(a, b) (a) + K.value * ((b) - (a)) / N.value, (a) + (K.value + 1) * ((b) - (a)) / N.value
 
-// The order of a slot's four steps in halves, what is loaded under each (16 loads a slot), and
-// the barriers between them ("read": all waves' LDS reads are done; "there": all waves' loads
-// have landed):
-//   step 0        slot + 1: 8 .. 13
-//   step 1        slot + 1: 14, 15
-//   step 2        (the slot is read)
-//     2nd half    slot + 2: 0, 1
-//   step 3        slot + 2: 2 .. 4
-//                 (slot + 1 is there)
-//     2nd half    slot + 2: 5 .. 7
-// A place in LDS is loaded anew from half a step after its last operands were asked for, and
-// waited for half a step before its first are used.
-constexpr int kLoads2 = 2, kLoads3 = 5, kLoads3b = 8, kLoads0 = 14;   // loads issued by the end of each stretch
+// The order of a slot's two steps of 8 TB MFMAs, in eighths; what is read and loaded under each
+// stretch (16 loads a slot), and the barriers between them ("read": all waves' LDS reads are
+// done; "there": all waves' loads have landed):
+//   step 0   0 .. 5   LDS: step 1
+//                     (the slot is read)
+//            5 .. 8   slot + 2: loads 0 .. 4
+//   step 1   0 .. 2   slot + 2: 5 .. 7
+//                     (slot + 1 is there)
+//            2 .. 8   slot + 2: 8 .. 15; LDS: step 0 of slot + 1
+// A load has thirteen eighths of a step to arrive, a step being 1024 cycles of MFMAs.
+constexpr int kLoads0 = 5, kLoads1 = 8;                  // loads issued by the end of each stretch
 
-template <int P, int TM, bool FIRST>
-__device__ __forceinline__ void steps01(v16f (&acc)[4][TM], Operands<P, TM> (&f)[2], Loader<P>& ld, const Lane<P>& l, uint32_t s)
+template <int P, int TB, bool FIRST>
+__device__ __forceinline__ void step0(v4f (&acc)[8][TB], Operands<TB> (&f)[2], Loader<P>& ld, Lane<P>& l, uint32_t s)
 {
-    constexpr int h = 2 * TM, n = 4 * TM, Q = kPieces<P, TM>;
+    constexpr int n = 8 * TB, Q = kPieces<P, TB>;
     __builtin_amdgcn_sched_barrier(0);
-    mfmas<P, TM, FIRST, 0, n>(acc, f[0], [&](auto K, auto N) {
-        read_step<P, TM, 1, MXQ_PART(0, Q)>(f[1], l);
-        ld.template issue_some<MXQ_PART(kLoads3b, kLoads0)>(s ^ 1u);
-    });
-    mfmas<P, TM, false, 0, h>(acc, f[1], [&](auto K, auto N) {
-        ld.template issue_some<MXQ_PART(kLoads0, 16)>(s ^ 1u);
-        read_step<P, TM, 2, MXQ_PART(0, Q / 2)>(f[0], l);
-    });
-    mfmas<P, TM, false, h, n>(acc, f[1], [&](auto K, auto N) { read_step<P, TM, 2, MXQ_PART(Q / 2, Q)>(f[0], l); });
-}
-
-// On exit f[0] holds the next slot's first step, unless this is the tile's LAST.
-template <int P, int TM, bool LAST>
-__device__ __forceinline__ void steps23(v16f (&acc)[4][TM], Operands<P, TM> (&f)[2], Loader<P>& ld, Lane<P>& l, uint32_t s)
-{
-    constexpr int h = 2 * TM, n = 4 * TM, Q = kPieces<P, TM>;
-    mfmas<P, TM, false, 0, h>(acc, f[0], [&](auto K, auto N) { read_step<P, TM, 3, MXQ_PART(0, Q)>(f[1], l); });
+    mfmas<TB, FIRST, 0, 5 * TB>(acc, f[0], [&](auto K, auto N) { read_step<P, TB, 1, MXQ_PART(0, Q)>(f[1], l); });
     l.a.other_slot();
     l.b.other_slot();
     slot_barrier<63>();
-    mfmas<P, TM, false, h, n>(acc, f[0], [&](auto K, auto N) { ld.template issue_some<MXQ_PART(0, kLoads2)>(s); });
-    mfmas<P, TM, false, 0, h>(acc, f[1], [&](auto K, auto N) { ld.template issue_some<MXQ_PART(kLoads2, kLoads3)>(s); });
-    slot_barrier<kLoads3>();                             // (newer: the slot after it)
-    mfmas<P, TM, false, h, n>(acc, f[1], [&](auto K, auto N) {
-        if constexpr (!LAST) read_step<P, TM, 0, MXQ_PART(0, Q)>(f[0], l);
-        ld.template issue_some<MXQ_PART(kLoads3, kLoads3b)>(s);
+    mfmas<TB, FIRST, 5 * TB, n>(acc, f[0], [&](auto K, auto N) { ld.template issue_some<MXQ_PART(0, kLoads0)>(s); });
+}
+// On exit f[0] holds the next slot's first step, unless this is the tile's LAST.
+template <int P, int TB, bool LAST>
+__device__ __forceinline__ void step1(v4f (&acc)[8][TB], Operands<TB> (&f)[2], Loader<P>& ld, Lane<P>& l, uint32_t s)
+{
+    constexpr int n = 8 * TB, Q = kPieces<P, TB>;
+    mfmas<TB, false, 0, 2 * TB>(acc, f[1], [&](auto K, auto N) { ld.template issue_some<MXQ_PART(kLoads0, kLoads1)>(s); });
+    slot_barrier<kLoads1>();                             // (newer: the slot after it)
+    mfmas<TB, false, 2 * TB, n>(acc, f[1], [&](auto K, auto N) {
+        if constexpr (!LAST) read_step<P, TB, 0, MXQ_PART(0, Q)>(f[0], l);
+        ld.template issue_some<MXQ_PART(kLoads1, 16)>(s);
     });
 }
 #undef MXQ_PART
 
 // The sums are needed here: without this the compiler moves MFMAs past the loads that are meant
 // to run under them, into the next basic block.
-template <int TM>
-__device__ __forceinline__ void pin(v16f (&acc)[4][TM])
+template <int TB>
+__device__ __forceinline__ void pin(v4f (&acc)[8][TB])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < TM; ++j) asm volatile("" : "+a"(acc[i][j]));
+        for (int j = 0; j < TB; ++j) asm volatile("" : "+a"(acc[i][j]));
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Stores: lane (r, h) holds, of row r of each 32 x 32 part, columns 8 q + 4 h .. + 3 for
-// q = 0 .. 3.  bf16: the halves of the wave exchange every other 4 columns, so that a lane
-// has 8 consecutive ones (16 bytes); then pieces change lanes so that stores cover whole lines.
-template <int P, int TM, bool F32OUT, bool ADD>
-__device__ __forceinline__ void store_tile(const v16f (&acc)[4][TM], const MmArgs& a, const Tile& t, const Lane<P>& l)
+// Stores: lane (r, q) holds, of row r of each 16 x 16 part, columns 4q .. 4q + 3.  fp32: 16 bytes
+// a lane, 64 of a row.  bf16: two parts side by side change lanes, so that those of even q have
+// eight columns of the first and those of odd q of the second: 16 bytes a lane, 64 of a row.
+template <int P, int TB, bool F32OUT, bool ADD>
+__device__ __forceinline__ void store_tile(v4f (&acc)[8][TB], const MmArgs& a, const Tile& t, const Lane<P>& l)
 {
     constexpr int kSize = F32OUT ? 4 : 2, kParts = F32OUT ? 1 : 2;
     const int cols = Shape<P>::cols(a.N, a.K);
     const int r1 = ADD && t.k0 == t.k1 ? t.r0 : t.r1;    // (nothing to add: nothing is touched)
     const int64_t rows_before = (int64_t)t.part * (Shape<P>::kDw ? (int64_t)a.G * a.N : a.M) + (Shape<P>::kDw ? (int64_t)t.g * a.N : 0);
     uint8_t* out = (uint8_t*)a.out + rows_before * cols * kSize;
-    const int n_lane = (int)(64u * (l.row >> 3 & 1u) + 32u * (l.row >> 4) + 16u * l.h) / kSize;
+    int r = (int)l.row, q = (int)l.q;
+    asm volatile("" : "+v"(r), "+v"(q));                 // (keeps the addresses from being made before the sums)
+    const int n_lane = F32OUT ? 4 * q : 16 * (q & 1) + 8 * (q >> 1);
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-        const int m = t.r0 + (int)(32u * TM * l.wm + 32u * j + (l.row & 7u));
+    for (int j = 0; j < TB; ++j) {
+        const int row = t.r0 + (int)(16u * TB * l.wm) + 16 * j + r;
+        uint8_t* to = out + ((int64_t)row * cols + t.c * kCols + (int)(128u * l.wn) + n_lane) * kSize;
 #pragma unroll
-        for (int i = 0; i < 4; i += kParts) {
-            __builtin_amdgcn_sched_barrier(0);           // (one block at a time in VGPRs)
-            v4i p[4];
+        for (int i = 0; i < 8; i += kParts) {
+            // one part at a time leaves the accumulators' registers
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) asm volatile("" : "+a"(acc[i + n][j]));
+            const v4f v = acc[i][j];
+            v4i p;
             if constexpr (F32OUT) {
-                const v16f& v = acc[i][j];
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) p[s][k] = __float_as_int(v[4 * s + k]);
+                for (int k = 0; k < 4; ++k) p[k] = __float_as_int(v[k]);
             } else {
+                const v4f w = acc[i + 1][j];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const v16f& v = acc[i + s / 2][j];
-                    const int q = 8 * (s % 2);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const auto w = __builtin_amdgcn_permlane32_swap(f32_pair_to_bf16(v[q + 2 * k], v[q + 2 * k + 1]),
-                                                                        f32_pair_to_bf16(v[q + 2 * k + 4], v[q + 2 * k + 5]), false, false);
-                        p[s][k] = (int)w[0];
-                        p[s][k + 2] = (int)w[1];
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    const auto x = __builtin_amdgcn_permlane16_swap(f32_pair_to_bf16(v[2 * k], v[2 * k + 1]),
+                                                                    f32_pair_to_bf16(w[2 * k], w[2 * k + 1]), false, false);
+                    p[k] = (int)x[0];
+                    p[k + 2] = (int)x[1];
                 }
             }
-            join_lines(p);
-            const int n = t.c * kCols + (int)(128u * l.wn) + 32 * i + n_lane;
+            if (row < r1 && t.c * kCols + (int)(128u * l.wn) + 16 * i + n_lane < cols) {
+                v4i* at = (v4i*)(to + 16 * i * kSize);
+                if constexpr (ADD) {
+                    const v4i old = *at;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int row = m + 16 * (s % 2) + 8 * (s / 2);
-                if (row < r1 && n < cols) {
-                    v4i* to = (v4i*)(out + ((int64_t)row * cols + n) * kSize);
-                    if constexpr (ADD) {
-                        const v4i old = *to;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) p[s][k] = __float_as_int(__int_as_float(old[k]) + __int_as_float(p[s][k]));
-                    }
-                    *to = p[s];
+                    for (int k = 0; k < 4; ++k) p[k] = __float_as_int(__int_as_float(old[k]) + __int_as_float(p[k]));
                 }
+                *at = p;
             }
         }
     }
 }
 
 // One tile: its slots are the next to come out of the stream, the first of them in ring slot s;
-// the loads are part way into the slot after it.
-template <int P, int TM, bool F32OUT, bool ADD>
+// the slot after it has been asked for.
+template <int P, int TB, bool F32OUT, bool ADD>
 __device__ __forceinline__ void tile_product(Loader<P>& ld, const MmArgs& a, const TileList& list, int count, const Tile& t,
                                              Lane<P>& l, uint32_t base, uint32_t& s)
 {
-    v16f acc[4][TM];
-    Operands<P, TM> f[2];
-    l.b.set(base + s * kSlotBytes + kOperandBytes, TM * l.wm);
+    v4f acc[8][TB];
+    Operands<TB> f[2];
+    l.b.set(base + s * kSlotBytes + kOperandBytes, TB * l.wm);
     const int nslots = uniform(slots_of(t));
-    s = (uint32_t)uniform((int)s);                       // (a scalar register's, which the loads' M0 needs)
-    read_step<P, TM, 0, 0, kPieces<P, TM>>(f[0], l);
-    steps01<P, TM, true>(acc, f, ld, l, s);
-    pin<TM>(acc);
-    ld.advance(a, list, count);
+    s = (uint32_t)uniform((int)s);
+    ld.make_uniform();
+    read_step<P, TB, 0, 0, kPieces<P, TB>>(f[0], l);
+    step0<P, TB, true>(acc, f, ld, l, s);
     for (int i = 1; i < nslots; ++i) {
-        steps23<P, TM, false>(acc, f, ld, l, s);
-        pin<TM>(acc);
-        s ^= 1u;
-        steps01<P, TM, false>(acc, f, ld, l, s);
-        pin<TM>(acc);
+        step1<P, TB, false>(acc, f, ld, l, s);
+        pin<TB>(acc);
         ld.advance(a, list, count);
+        s ^= 1u;
+        step0<P, TB, false>(acc, f, ld, l, s);
+        pin<TB>(acc);
     }
-    steps23<P, TM, true>(acc, f, ld, l, s);
-    pin<TM>(acc);
+    step1<P, TB, true>(acc, f, ld, l, s);
+    pin<TB>(acc);
+    ld.advance(a, list, count);
     s ^= 1u;
-    store_tile<P, TM, F32OUT, ADD>(acc, a, t, l);
+    store_tile<P, TB, F32OUT, ADD>(acc, a, t, l);
 }
 
 template <int P, bool F32OUT, bool ADD>
@@ -635,28 +642,29 @@ void bf16_mm_kernel(const MmArgs a)
 
     if (count > 0) {
         Lane<P> l;
-        l.row = (uint32_t)(lane & 31);
-        l.h = (uint32_t)(lane >> 5);
+        l.row = (uint32_t)(lane & 15);
+        l.q = (uint32_t)(lane >> 4);
         l.wn = (uint32_t)(wave >> 1);
         l.wm = (uint32_t)(wave & 1);
         const uint32_t base = (uint32_t)(uintptr_t)(LdsPtr)lds;
-        l.a.set(base, 4 * l.wn);
+        l.a.set(base, 8 * l.wn);
         Loader<P> ld;
         ld.set_lanes(a, lds, wave, lane);
         ld.entry = 0;
         ld.set_tile(a, list, count);
         ld.template issue_some<0, 16>(0);
         ld.advance(a, list, count);
-        ld.template issue_some<0, kLoads3b>(1);
-        slot_barrier<0>();
+        ld.template issue_some<0, 16>(1);
+        ld.advance(a, list, count);
+        slot_barrier<16>();
         uint32_t s = 0;
         for (int e = 0; e < count; ++e) {
             const Tile t = list.at(e);
             // a group's last tile runs at the smallest of three heights that holds its rows
             const int rows = t.r1 - t.r0;
-            if (rows > 128) tile_product<P, 4, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
-            else if (rows > 64) tile_product<P, 2, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
-            else tile_product<P, 1, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
+            if (rows > 128) tile_product<P, 8, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
+            else if (rows > 64) tile_product<P, 4, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
+            else tile_product<P, 2, F32OUT, ADD>(ld, a, list, count, t, l, base, s);
         }
         slot_barrier<0>();                               // the loads past the end land before the LDS goes away
     }
