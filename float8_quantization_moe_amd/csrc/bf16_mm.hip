@@ -39,11 +39,16 @@ constexpr uint32_t kOperandBytes = 32 * 1024;            // of one operand in on
 constexpr uint32_t kSlotBytes = 2 * kOperandBytes;
 constexpr uint32_t kLdsBytes = 2 * kSlotBytes;
 constexpr int kMaxEntries = 64;                          // tiles of one workgroup: one a lane
-constexpr int kColBlock = 4;                             // column tiles of a block of the tile order
+// Column tiles of a block of the tile order.  16 uniform groups of 1040 rows, Y / dX / dW: 4 1357 /
+// 1324 / 1413 us, 8 1367 / 1371 / 1369.
+template <int P>
+constexpr int kColBlock = P == MXQ_PRODUCT_DW ? 8 : 4;
 constexpr int kXcds = 8;
 constexpr int kMaxGroups = 4095;
 constexpr int kMaxSplit = 16;
-static_assert((2 * (kMaxGroups + 2) + kThreads) * 4 <= (int)kLdsBytes, "the scan's arrays fit the ring");
+constexpr int kListBytes = (3 * (kMaxGroups + 1) + kThreads) * 4 + kMaxEntries * 64;
+static_assert(kListBytes <= (int)kLdsBytes, "the list's arrays fit the ring");
+constexpr int kCostWhole = 16, kCostHalf = 10, kCostQuarter = 9;
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -106,21 +111,55 @@ __device__ __forceinline__ void part_of(Tile& t, int base, int n, int p, int S)
     t.k1 = base + (b < n ? b : n);
 }
 
-// Place `i` of a block-ordered grid of `rows` x `cols` tiles: kColBlock columns at a time, a
-// block's rows one after the other.
+// Place `i` of a grid of `rows` x `cols` tiles in blocks of B columns, a block's rows one after
+// the other.
+template <int B>
 __device__ __forceinline__ void place_in(int i, int rows, int cols, int* r, int* c)
 {
-    const int cb = i / (rows * kColBlock), rem = i - cb * rows * kColBlock;
-    const int width = cols - cb * kColBlock < kColBlock ? cols - cb * kColBlock : kColBlock;
+    const int cb = i / (rows * B), rem = i - cb * rows * B;
+    const int width = cols - cb * B < B ? cols - cb * B : B;
     *r = rem / width;
-    *c = cb * kColBlock + rem % width;
+    *c = cb * B + rem % width;
+}
+
+// What a tile of so many rows costs, in sixteenths of a whole one: its loads and barriers stay.
+__device__ __forceinline__ int tile_cost(int rows)
+{
+    return rows > 128 ? kCostWhole : rows > 64 ? kCostHalf : rows > 0 ? kCostQuarter : 0;
+}
+
+// The items of one round for an XCD's CUs, one a lane: cost[lane] of item `lane` (0: none), load:
+// CU `lane`'s work up to now, which grows.  Returns CU `lane`'s item: the costliest go to the CUs
+// with the least work.
+__device__ __forceinline__ int items_by_load(int cost, int& load, int cus)
+{
+    const int lane = lane_id();
+    const uint64_t whole = __ballot(cost == kCostWhole), half = __ballot(cost == kCostHalf),
+                   quarter = __ballot(cost == kCostQuarter), none = __ballot(cost == 0);
+    const auto below = [&](uint64_t m) { return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u)); };
+    const int n8 = __builtin_popcountll(whole), n4 = n8 + __builtin_popcountll(half), n2 = n4 + __builtin_popcountll(quarter);
+    const int place = cost == kCostWhole ? below(whole) : cost == kCostHalf ? n8 + below(half) : cost == kCostQuarter ? n4 + below(quarter) : n2 + below(none);
+    const int by_place = __builtin_amdgcn_ds_permute(4 * place, lane);      // the item at each place
+    int rank = 0;
+    for (int m = 0; m < cus; ++m) {
+        const int other = readlane(load, m);
+        rank += other < load || (other == load && m < lane);
+    }
+    const int item = __builtin_amdgcn_ds_bpermute(4 * (lane < cus ? rank : lane), by_place);
+    load += __builtin_amdgcn_ds_bpermute(4 * item, cost);
+    return item;
 }
 
 // Fills `list` with this workgroup's tiles and returns their number; *rows_end is the last
-// group's clamped end.  end_sh: the groups' clamped ends; first_sh: each group's first row tile.
+// group's clamped end.  sh: kListBytes of LDS.
 template <int P>
-__device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_sh, TileList& list, int* rows_end)
+__device__ int make_list(const MmArgs& a, uint8_t* sh, TileList& list, int* rows_end)
 {
+    int* end_sh = (int*)sh;                              // the groups' clamped ends
+    int* first_sh = end_sh + kMaxGroups + 1;             // each group's first row tile
+    int* work_sh = first_sh + kMaxGroups + 1;            // and the cost of those before it
+    int* scan_sh = work_sh + kMaxGroups + 1;
+    uint8_t* cost_sh = (uint8_t*)(scan_sh + kThreads);   // of the items of each round
     const int t = (int)threadIdx.x, R = a.rows, S = a.split;
     const int per = (a.G + kThreads - 1) / kThreads;
     const int ga = t * per < a.G ? t * per : a.G, gb = ga + per < a.G ? ga + per : a.G;
@@ -158,7 +197,7 @@ __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_
             tl.g = L / per_group;
             const int rem = L - tl.g * per_group;
             int r;
-            place_in(rem / S, NR, NC, &r, &tl.c);
+            place_in<kColBlock<P>>(rem / S, NR, NC, &r, &tl.c);
             tl.r0 = r * R;
             tl.r1 = tl.r0 + R < a.N ? tl.r0 + R : a.N;
             const int start = tl.g ? end_sh[tl.g - 1] : 0;
@@ -168,48 +207,87 @@ __device__ int make_list(const MmArgs& a, int* end_sh, int* first_sh, int* scan_
         return count < kMaxEntries ? count : kMaxEntries;
     }
 
-    int tiles = 0;
+    int tiles = 0, work = 0;
     for (int g = ga, start = base; g < gb; ++g) {
-        tiles += (end_sh[g] - start + R - 1) / R;
+        const int m = end_sh[g] - start;
+        tiles += (m + R - 1) / R;
+        work += m / R * tile_cost(R) + tile_cost(m % R);
         start = end_sh[g];
     }
     int first = block_scan<false>(tiles, scan_sh) - tiles;
+    int before_work = block_scan<false>(work, scan_sh) - work;
     for (int g = ga, start = base; g < gb; ++g) {
+        const int m = end_sh[g] - start;
         first_sh[g] = first;
-        first += (end_sh[g] - start + R - 1) / R;
+        work_sh[g] = before_work;
+        first += (m + R - 1) / R;
+        before_work += m / R * tile_cost(R) + tile_cost(m % R);
         start = end_sh[g];
     }
-    if (t == kThreads - 1) first_sh[a.G] = first;
+    if (t == kThreads - 1) {
+        first_sh[a.G] = first;
+        work_sh[a.G] = before_work;
+    }
     __syncthreads();
 
-    // Each XCD walks one contiguous stretch, its CUs side by side; the tiles left after the
-    // last full round are cut in row parts of 64 or more while that gives no more than one for
-    // each CU.
-    const int V = first_sh[a.G] * NC * S;
-    const int lo = (int)((int64_t)V * x / kXcds), n = (int)((int64_t)V * (x + 1) / kXcds) - lo;
-    const int full = n / cus, over = n - full * cus;
-    const int parts = 4 * over <= cus && R == 256 ? 4 : 2 * over <= cus ? 2 : 1;
-    const int count = full + (cu < over * parts);
-    if (j < count) {
-        const int L = lo + j * cus + (j < full ? (cu + 6 * j) % cus : cu / parts);
-        const int V2 = L / S;
-        int p = 0, r = a.G - 1;                          // the last group whose tiles start at or before V2
+    // Each XCD walks one stretch of the tiles, about an eighth of the work, its CUs side by
+    // side; the tiles left after the last full round are cut in row parts of 64 or more while
+    // that gives no more than one for each CU.
+    const int V = first_sh[a.G] * NC * S, W = work_sh[a.G];
+    const auto last_at = [&](const int* sh_, int v, int mul) {               // the last group that starts at or before v
+        int p = 0, r = a.G - 1;
         while (p < r) {
             const int mid = (p + r + 1) >> 1;
-            if (first_sh[mid] * NC <= V2) p = mid;
+            if (sh_[mid] * mul <= v) p = mid;
             else r = mid - 1;
         }
+        return p;
+    };
+    const auto cut = [&](int i) {
+        if (i == kXcds) return V;
+        const int w = (int)((int64_t)W * i / kXcds), p = last_at(work_sh, w, 1);
+        const int64_t n = (int64_t)(first_sh[p + 1] - first_sh[p]) * NC * S;
+        return (int)(first_sh[p] * NC * S + (n > 0 ? (w - work_sh[p]) * n / (work_sh[p + 1] - work_sh[p]) : 0));
+    };
+    const int lo = cut(x), n = cut(x + 1) - lo;
+    const int full = n / cus, over = n - full * cus;
+    const int parts = 4 * over <= cus && R == 256 ? 4 : 2 * over <= cus ? 2 : 1;
+    // Item i of round e: its tile, whole or (in the last round) a part of it.
+    const auto tile_of = [&](int e, int i) {
+        const int L = lo + e * cus + (e < full ? i : i / parts), V2 = L / S;
+        const int p = last_at(first_sh, V2, NC);
         int rt;
         Tile tl;
-        place_in(V2 - first_sh[p] * NC, first_sh[p + 1] - first_sh[p], NC, &rt, &tl.c);
-        const int height = j < full ? R : R / parts, part = j < full ? 0 : cu % parts;
+        place_in<kColBlock<P>>(V2 - first_sh[p] * NC, first_sh[p + 1] - first_sh[p], NC, &rt, &tl.c);
+        const int height = e < full ? R : R / parts, part = e < full ? 0 : i % parts;
         tl.g = p;
         tl.r0 = (p ? end_sh[p - 1] : 0) + rt * R + part * height;
         tl.r1 = tl.r0 + height < end_sh[p] ? tl.r0 + height : end_sh[p];
         if (tl.r1 < tl.r0) tl.r1 = tl.r0;                // a part past the group's rows
         part_of(tl, 0, Shape<P>::depth(a.N, a.K), L % S, S);
-        list.mine = tl;
+        return tl;
+    };
+    const int rounds = full + (over > 0);
+    const auto items = [&](int e) { return e < full ? cus : over * parts; };
+    int mine = cu;                                       // this CU's item of round `lane`
+    if (rounds > 1 && cus <= 64) {
+        for (int e = t >> 6; e < rounds && e < kMaxEntries; e += kThreads / 64) {
+            const Tile tl = j < items(e) ? tile_of(e, j) : Tile{0, 0, 0, 0, 0, 0, 0};
+            cost_sh[e * 64 + j] = (uint8_t)tile_cost(tl.r1 - tl.r0);
+        }
+        __syncthreads();
+        int load = 0;
+        for (int e = 0; e < rounds && e < kMaxEntries; ++e) {
+            const int cost = cost_sh[e * 64 + j], one = readlane(cost, 0);
+            int item = j;
+            if (__ballot(j < cus && cost != one)) item = items_by_load(cost, load, cus);
+            else load += cost;
+            item = readlane(item, cu);
+            if (j == e) mine = item;
+        }
     }
+    const int count = full + (rounds > full && readlane(mine, full < 63 ? full : 63) < items(full));
+    if (j < count) list.mine = tile_of(j, mine);
     return count < kMaxEntries ? count : kMaxEntries;
 }
 
@@ -540,52 +618,56 @@ __device__ __forceinline__ void pin(v4f (&acc)[8][TB])
 // Stores: lane (r, q) holds, of row r of each 16 x 16 part, columns 4q .. 4q + 3.  fp32: 16 bytes
 // a lane, 64 of a row.  bf16: two parts side by side change lanes, so that those of even q have
 // eight columns of the first and those of odd q of the second: 16 bytes a lane, 64 of a row.
+// Through a buffer resource that ends with the tile's last row; a lane past the last column
+// leaves it too.  (Nothing else stands between the stores: with 64-bit addresses and branches
+// around each, 16640 x 8192 x 5120 over 16 groups, dW in fp32, took 1364 us.)
 template <int P, int TB, bool F32OUT, bool ADD>
 __device__ __forceinline__ void store_tile(v4f (&acc)[8][TB], const MmArgs& a, const Tile& t, const Lane<P>& l)
 {
     constexpr int kSize = F32OUT ? 4 : 2, kParts = F32OUT ? 1 : 2;
-    const int cols = Shape<P>::cols(a.N, a.K);
-    const int r1 = ADD && t.k0 == t.k1 ? t.r0 : t.r1;    // (nothing to add: nothing is touched)
+    const int cols = Shape<P>::cols(a.N, a.K), c0 = t.c * kCols;
     const int64_t rows_before = (int64_t)t.part * (Shape<P>::kDw ? (int64_t)a.G * a.N : a.M) + (Shape<P>::kDw ? (int64_t)t.g * a.N : 0);
-    uint8_t* out = (uint8_t*)a.out + rows_before * cols * kSize;
+    const int rows = ADD && t.k0 == t.k1 ? 0 : t.r1 - t.r0;                 // (nothing to add: nothing is touched)
+    const int ld = cols * kSize;
+    const auto out = __builtin_amdgcn_make_buffer_rsrc((uint8_t*)a.out + ((rows_before + t.r0) * cols + c0) * kSize, 0,
+                                                       rows > 0 ? rows * ld - c0 * kSize : 0, 0x00020000);
     int r = (int)l.row, q = (int)l.q;
     asm volatile("" : "+v"(r), "+v"(q));                 // (keeps the addresses from being made before the sums)
-    const int n_lane = F32OUT ? 4 * q : 16 * (q & 1) + 8 * (q >> 1);
+    const int n = (int)(128u * l.wn) + (F32OUT ? 4 * q : 16 * (q & 1) + 8 * (q >> 1));
+    int at = ((int)(16u * TB * l.wm) + r) * ld + n * kSize;
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
-        const int row = t.r0 + (int)(16u * TB * l.wm) + 16 * j + r;
-        uint8_t* to = out + ((int64_t)row * cols + t.c * kCols + (int)(128u * l.wn) + n_lane) * kSize;
+        const auto place = [&](int i) { return c0 + n + 16 * i < cols ? at + 16 * i * kSize : (int)0x80000000; };
+        v4f old[8];
+        if constexpr (ADD) {                             // (a row of parts asked for together)
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) old[i] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(out, place(i), 0, 0));
+        }
 #pragma unroll
         for (int i = 0; i < 8; i += kParts) {
             // one part at a time leaves the accumulators' registers
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int n = 0; n < kParts; ++n) asm volatile("" : "+a"(acc[i + n][j]));
+            for (int k = 0; k < kParts; ++k) asm volatile("" : "+a"(acc[i + k][j]));
             const v4f v = acc[i][j];
-            v4i p;
+            u32x4 p;
             if constexpr (F32OUT) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) p[k] = __float_as_int(v[k]);
+                p = __builtin_bit_cast(u32x4, v);
             } else {
                 const v4f w = acc[i + 1][j];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const auto x = __builtin_amdgcn_permlane16_swap(f32_pair_to_bf16(v[2 * k], v[2 * k + 1]),
                                                                     f32_pair_to_bf16(w[2 * k], w[2 * k + 1]), false, false);
-                    p[k] = (int)x[0];
-                    p[k + 2] = (int)x[1];
+                    p[k] = x[0];
+                    p[k + 2] = x[1];
                 }
             }
-            if (row < r1 && t.c * kCols + (int)(128u * l.wn) + 16 * i + n_lane < cols) {
-                v4i* at = (v4i*)(to + 16 * i * kSize);
-                if constexpr (ADD) {
-                    const v4i old = *at;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) p[k] = __float_as_int(__int_as_float(old[k]) + __int_as_float(p[k]));
-                }
-                *at = p;
-            }
+            if constexpr (ADD) p = __builtin_bit_cast(u32x4, old[i] + v);
+            __builtin_amdgcn_raw_buffer_store_b128(p, out, place(i), 0, 0);
         }
+        at += 16 * ld;
     }
 }
 
@@ -628,10 +710,7 @@ void bf16_mm_kernel(const MmArgs a)
     int rows_end;
     int count;
     {
-        int* end_sh = (int*)lds;
-        int* first_sh = end_sh + kMaxGroups + 1;
-        int* scan_sh = first_sh + kMaxGroups + 1;
-        count = uniform(make_list<P>(a, end_sh, first_sh, scan_sh, list, &rows_end));
+        count = uniform(make_list<P>(a, lds, list, &rows_end));
         rows_end = uniform(rows_end);
     }
     __syncthreads();                                     // the scan's arrays are free
@@ -769,12 +848,14 @@ hipError_t launch_bf16_mm(int product, const void* rows, const void* other, cons
     if (e != hipSuccess) return e;
     const Plan p = plan_of(product, M, N, K, G);
     const bool joined = M > 0 && p.split > 1;
-    // One workgroup a CU, fewer when there are not that many tiles (their row parts counted),
-    // a multiple of it when a workgroup's list would not hold its tiles: it has at most
-    // (items + 8) / grid + 1.
-    const int64_t parts = p.items * (p.rows / 64);
+    // One workgroup a CU, fewer when there are not that many tiles (their row parts counted), a
+    // multiple of it when a workgroup's list would not hold its tiles: an XCD's stretch of the
+    // work has at most kCostWhole / kCostQuarter times an eighth of the tiles and two, a
+    // workgroup of grid / 8 its part of them and one.
+    const int64_t parts = p.items * (p.rows / 64), most =
+        (product == MXQ_PRODUCT_DW ? p.items : p.items * kCostWhole / kCostQuarter) + 2 * kXcds + 1;
     int64_t grid = parts < cus ? (parts > 0 ? parts : 1) : cus;
-    grid *= (p.items + kXcds + grid * (kMaxEntries - 1) - 1) / (grid * (kMaxEntries - 1));
+    grid *= (most + grid * (kMaxEntries - 1) - 1) / (grid * (kMaxEntries - 1));
     grid = (grid + kXcds - 1) / kXcds * kXcds;
     const bool wide = f32_out || joined;
     const MmArgs a = {(const uint16_t*)other, (const uint16_t*)rows, offs, joined ? workspace : out, M, N, K, G, p.rows,
