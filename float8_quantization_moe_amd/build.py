@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["api.hip", "mx_codec.hip", "mx_dim0.hip", "dispatch.hip", "group_scale.hip", "group_split.hip", "transpose.hip",
            "grouped_mm.hip", "norm.hip", "route.hip", "mxfp4_codec.hip", "mxfp4_mm.hip",
-           "mxfp4_mm_tile.hip", "layernorm.hip", "rows.hip", "bf16_mm.hip"]
+           "mxfp4_mm_tile.hip", "layernorm.hip", "rows.hip", "bf16_mm.hip", "bf16_mm_few.hip"]
 ARCH = "gfx950"
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON_FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra",

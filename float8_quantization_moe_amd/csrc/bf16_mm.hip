@@ -805,14 +805,28 @@ Plan plan_of(int product, int64_t M, int64_t N, int64_t K, int64_t G)
     Plan p;
     p.rows = tiles(256) >= kCus ? 256 : 128;
     const int64_t n = tiles(p.rows);
-    // slots of an average sum; a part has four or more
+    // Slots of an average sum; a part has four or more.  A short sum is not worth the second
+    // launch (8192 rows x 512 x 512, 8 slots: 28 us in two parts, 16 in one).
     const int64_t slots = ((dw ? M / G : product == MXQ_PRODUCT_Y ? K : N) + kSlotK - 1) / kSlotK;
     int64_t split = n > 0 ? kCus / n : 1;
     if (split > slots / 4) split = slots / 4;
+    if (slots < 16) split = 1;
     if (split > kMaxSplit) split = kMaxSplit;
     p.split = split < 1 ? 1 : (int)split;
     p.items = n * p.split;
     return p;
+}
+// Few rows go to launch_bf16_mm_few (Y / dX, few against tiles, us): 16 experts of 8192 x 5120, 8 rows
+// 84 / 103 against 100 / 142, 256 rows 255 / 305 against 290 / 312, 512 rows 309 / 359 against 295 /
+// 309; one expert, 256 rows 40 / 63 against 51 / 57.  More rows too while the whole product is
+// small: one expert of 512 x 512, 4096 rows 12 / 12 against 24 / 24, 8192 rows 24 / 24 against 28 /
+// 28, 16384 rows 43 / 43 against 18 / 18; 8 of 256 x 128, 16384 rows 19 / 14 against 12 / 13; 2 of
+// 1736 x 1408, 1024 rows 16 / 21 against 29 / 25; 8 of 2048 x 768, 1024 rows 18 / 15 against 24 /
+// 23, 2048 rows 28 / 25 against 19 / 27.
+bool few_rows(int product, int64_t M, int64_t N, int64_t K)
+{
+    return product != MXQ_PRODUCT_DW && M > 0 &&
+           (M <= 256 || (M <= 1024 && M * N * K <= (int64_t)1 << 31) || (M <= 16384 && M * N * K <= (int64_t)1 << 30));
 }
 int64_t results_of(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 {
@@ -834,7 +848,7 @@ bool bf16_mm_sizes_ok(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 
 size_t bf16_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 {
-    if (M == 0) return 0;
+    if (M == 0 || few_rows(product, M, N, K)) return 0;
     const int split = plan_of(product, M, N, K, G).split;
     return split > 1 ? (size_t)split * (size_t)results_of(product, M, N, K, G) * 4u : 0;
 }
@@ -842,6 +856,8 @@ size_t bf16_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int
 hipError_t launch_bf16_mm(int product, const void* rows, const void* other, const int32_t* offs, int M, int N, int K, int G,
                           void* out, bool f32_out, bool accumulate, void* workspace, hipStream_t stream)
 {
+    if (few_rows(product, M, N, K))
+        return launch_bf16_mm_few(rows, other, product == MXQ_PRODUCT_DX, offs, M, N, K, G, out, f32_out, stream);
     int device = 0, cus = 0;
     hipError_t e = hipGetDevice(&device);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);

@@ -1,0 +1,242 @@
+// bf16_mm_few.hip -- the products Y and dX of bf16_mm.hip for few token rows.
+//
+// The weights' bytes are the cost and each is used once or a few times, so nothing is shared
+// between waves: a workgroup takes 64 columns of results by 16 TB rows of one group, its four
+// waves a quarter of the sum each.  A wave has a ring of two steps of its own in LDS (64 values of
+// the sum: 8 KB of weights, 2 KB a 16 rows of tokens), filled by buffer-load-to-LDS in whole
+// 128-byte lines, and waits for its own loads only.  The waves' sums are added in LDS in order:
+// one launch, no workspace.
+//
+// Weights whose memory rows run along the sum (Y) are read 16 bytes a lane, those that run across
+// it (dX) with the transposing LDS read; MFMA operands as in bf16_mm.hip.
+#include "device_common.hpp"
+#include "internal.hpp"
+#include "mm_tile.hpp"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kThreads = kTileThreads;
+constexpr int kWaves = kThreads / 64;
+constexpr int kCols = 64;                                // columns of a workgroup
+constexpr int kStepK = 64;
+constexpr uint32_t kABytes = 8192;                       // weights of one step
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i* LdsV4i;
+typedef __attribute__((address_space(3))) v4f* LdsV4f;
+typedef __attribute__((address_space(3))) v4s* LdsV4s;
+
+struct FewArgs {
+    const uint16_t *w, *rows;
+    const int32_t* offs;
+    void* out;
+    int M, N, K, G;
+};
+
+// Rows of one workgroup.
+struct Chunk {
+    int g, r0, r1;                                       // g < 0: none
+    int rows_end;                                        // the last group's clamped end
+};
+
+// Chunk `want` of the groups' rows, `height` rows at most each, in the groups' order.  By one wave.
+__device__ __forceinline__ Chunk find_chunk(const FewArgs& a, int want, int height)
+{
+    const int lane = lane_id();
+    Chunk c = {-1, 0, 0, 0};
+    int seen = 0;
+    for (int base = 0; base < a.G; base += 64) {
+        int e = base + lane < a.G ? a.offs[base + lane] : 0;
+        e = wave_incl_max_dpp(e > 0 ? e : 0);
+        e = e > c.rows_end ? e : c.rows_end;
+        e = e < a.M ? e : a.M;
+        const int up = __shfl_up(e, 1, 64), start = lane ? up : c.rows_end;
+        const int n = (e - start + height - 1) / height, upto = wave_incl_sum(n) + seen;
+        const uint64_t hit = __ballot(upto > want);
+        if (c.g < 0 && hit) {
+            const int l = __builtin_ctzll(hit);
+            c.g = base + l;
+            c.r0 = readlane(start, l) + (want - readlane(upto - n, l)) * height;
+            c.r1 = readlane(e, l);
+            c.r1 = c.r0 + height < c.r1 ? c.r0 + height : c.r1;
+        }
+        c.rows_end = readlane(e, 63);
+        seen = readlane(upto, 63);
+    }
+    return c;
+}
+
+// The wave's loads and all before them but the last N have landed.
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void wait_reads()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// ACROSS: the weights' rows run across the sum (dX).  TB: 16-row parts.
+template <bool ACROSS, int TB, bool F32OUT>
+__global__ __launch_bounds__(kThreads)
+void bf16_mm_few_kernel(const FewArgs a)
+{
+    constexpr int kLoads = 8 + 2 * TB;                   // of a step
+    constexpr uint32_t kStepBytes = kABytes + 2048u * TB;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * 2 * kStepBytes];
+    const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
+    const Chunk c = find_chunk(a, (int)blockIdx.y, 16 * TB);
+    const int cols = ACROSS ? a.K : a.N, depth = ACROSS ? a.N : a.K;
+    const int c0 = (int)blockIdx.x * kCols;
+
+    if (blockIdx.y == 0) {                               // rows past the last end: zeros
+        constexpr int kPer = F32OUT ? 4 : 8;             // values of 16 bytes
+        const int width = (cols - c0 < kCols ? cols - c0 : kCols) / kPer;
+        for (int i = (int)threadIdx.x; i < (a.M - c.rows_end) * width; i += kThreads)
+            ((uint4*)a.out)[((int64_t)(c.rows_end + i / width) * cols + c0) / kPer + i % width] = make_uint4(0, 0, 0, 0);
+    }
+    if (c.g < 0) return;
+
+    // this wave's steps of the sum, and the resources at the first
+    const int steps = (depth + kStepK - 1) / kStepK;
+    const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
+    const uint32_t lda = 2u * (uint32_t)a.K, ldb = 2u * (uint32_t)depth;
+    const int rows = c.r1 - c.r0, width = cols - c0 < kCols ? cols - c0 : kCols;
+    const uint16_t* wbase = a.w + ((int64_t)c.g * a.N + (ACROSS ? 0 : c0)) * a.K + (ACROSS ? c0 : 0);
+    const uint16_t* rbase = a.rows + (int64_t)c.r0 * depth;
+
+    // Lane offsets.  LDS rows of 128 bytes: "along" and the tokens', their 16-byte chunks at
+    // c ^ ((row >> 1) & 7); "across", their 32-byte parts at p ^ (row & 3).  Load i is rows
+    // 8i .. 8i + 7, so both swizzles repeat every second load.
+    uint32_t along[2], tail[2], part[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t row = 8u * i + ((uint32_t)lane >> 3);
+        const uint32_t chunk = ((uint32_t)lane & 7u) ^ ((row >> 1) & 7u);
+        along[i] = 16u * chunk;
+        tail[i] = depth % kStepK != 0 && chunk >= (uint32_t)(depth % kStepK) / 8u ? 0x80000000u : 0u;
+        part[i] = 32u * ((((uint32_t)lane >> 1) & 3u) ^ (row & 3u)) + 16u * ((uint32_t)lane & 1u);
+    }
+    const uint32_t my = (uint32_t)uniform((int)((uint32_t)(uintptr_t)(LdsPtr)lds + (uint32_t)wave * 2u * kStepBytes));
+    // A step into ring slot s & 1; past the wave's last one it loads nothing.
+    const auto issue = [&](int s) {
+        const uint32_t to = my + (uint32_t)((s - s0) & 1) * kStepBytes;
+        const bool some = s < s1, last = s == steps - 1;
+        const int k = s * kStepK;
+        const int n = depth - k < kStepK ? depth - k : kStepK;
+        const v4i ra = resource(ACROSS ? wbase + (int64_t)k * a.K : wbase + k,
+                                !some ? 0u : ACROSS ? (uint32_t)n * lda - 2u * (uint32_t)c0 : (uint32_t)width * lda - 2u * (uint32_t)k);
+        const v4i rb = resource(rbase + k, some ? (uint32_t)rows * ldb - 2u * (uint32_t)k : 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t off = (8u * i + ((uint32_t)lane >> 3)) * lda;
+            load_to_lds<3>(ra, to + 1024u * i, ACROSS ? off + part[i & 1] : (off + along[i & 1]) | (last ? tail[i & 1] : 0u));
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * TB; ++i)
+            load_to_lds<3>(rb, to + kABytes + 1024u * i,
+                           ((8u * i + ((uint32_t)lane >> 3)) * ldb + along[i & 1]) | (last ? tail[i & 1] : 0u));
+    };
+
+    v4f acc[4][TB];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) acc[i][j] = v4f{};
+    const uint32_t r = (uint32_t)lane & 15u, q = (uint32_t)lane >> 4, sub = (r >> 2) & 3u;
+    if (s0 < s1) {
+        issue(s0);
+        issue(s0 + 1);
+    }
+    for (int s = s0; s < s1; ++s) {
+        const uint32_t slot = my + (uint32_t)((s - s0) & 1) * kStepBytes;
+        wait_loads<kLoads>();                            // (newer: the next step)
+        v4i fa[2][4], fb[2][TB];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {                    // 32 values of the sum
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (ACROSS) {                  // rows 32h + 8q + sub and four on, columns 16i + 4 (r % 4) ..
+                    const uint32_t at = slot + (32u * h + 8u * q + sub) * 128u + (((uint32_t)i ^ sub) << 5) + 8u * (r & 3u);
+                    const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)at));
+                    const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)(at + 512u)));
+                    fa[h][i] = v4i{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+                } else {
+                    fa[h][i] = *(LdsV4i)(uintptr_t)(slot + (16u * i + r) * 128u + (((4u * h + q) ^ ((r >> 1) & 7u)) << 4));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+                fb[h][j] = *(LdsV4i)(uintptr_t)(slot + kABytes + (16u * j + r) * 128u + (((4u * h + q) ^ ((r >> 1) & 7u)) << 4));
+        }
+        wait_reads();
+        issue(s + 2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < TB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, fa[h][i]),
+                                                                        __builtin_bit_cast(v8bf, fb[h][j]), acc[i][j], 0, 0, 0);
+    }
+    wait_loads<0>();                                     // (the loads past the end, before the ring is used again)
+
+    // the waves' sums: wave i adds part i of all of them
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) *(LdsV4f)(uintptr_t)(my + (uint32_t)(i * TB + j) * 1024u + 16u * (uint32_t)lane) = acc[i][j];
+    __syncthreads();
+    const uint32_t base = (uint32_t)(uintptr_t)(LdsPtr)lds;
+    const int col = c0 + 16 * wave + 4 * (int)q;
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+        v4f sum = {};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            sum += *(LdsV4f)(uintptr_t)(base + (uint32_t)w * 2u * kStepBytes + (uint32_t)(wave * TB + j) * 1024u + 16u * (uint32_t)lane);
+        const int row = c.r0 + 16 * j + (int)r;
+        if (row < c.r1 && col < cols) {
+            const int64_t at = (int64_t)row * cols + col;
+            if constexpr (F32OUT) *(v4f*)((float*)a.out + at) = sum;
+            else *(uint2*)((uint16_t*)a.out + at) = make_uint2(f32_pair_to_bf16(sum[0], sum[1]), f32_pair_to_bf16(sum[2], sum[3]));
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_bf16_mm_few(const void* rows, const void* w, bool across, const int32_t* offs, int M, int N, int K, int G,
+                              void* out, bool f32_out, hipStream_t stream)
+{
+    const FewArgs a = {(const uint16_t*)w, (const uint16_t*)rows, offs, out, M, N, K, G};
+    const int groups = G < M ? G : M;
+    const int parts = M <= 16 ? 1 : M <= 32 * groups ? 2 : 4;
+    const int cols = across ? K : N, height = 16 * parts;
+    const dim3 grid((unsigned)((cols + kCols - 1) / kCols), (unsigned)((M + height - 1) / height + (G < M ? G : M) - 1));
+#define MXQ_LAUNCH(T, F)                                                                                                \
+    do {                                                                                                                \
+        if (across) hipLaunchKernelGGL((bf16_mm_few_kernel<true, T, F>), grid, dim3(kThreads), 0, stream, a);           \
+        else hipLaunchKernelGGL((bf16_mm_few_kernel<false, T, F>), grid, dim3(kThreads), 0, stream, a);                 \
+    } while (0)
+    if (parts == 1 && f32_out) MXQ_LAUNCH(1, true);
+    else if (parts == 1) MXQ_LAUNCH(1, false);
+    else if (parts == 2 && f32_out) MXQ_LAUNCH(2, true);
+    else if (parts == 2) MXQ_LAUNCH(2, false);
+    else if (f32_out) MXQ_LAUNCH(4, true);
+    else MXQ_LAUNCH(4, false);
+#undef MXQ_LAUNCH
+    return hipGetLastError();
+}
+
+}  // namespace mxq

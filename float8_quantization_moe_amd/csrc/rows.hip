@@ -27,6 +27,12 @@ __device__ __forceinline__ int64_t row_of(const int32_t* pair_row, int64_t p, in
     const int64_t r = pair_row[p];
     return r >= 0 && r < R ? r : -1;
 }
+// A wave's number in the launch, in a scalar register: what depends on it alone (a token, its
+// rows and weights) is then loaded once a wave.
+__device__ __forceinline__ int64_t wave_number()
+{
+    return (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
 
 // A wave takes 64 chunks of 16 bytes of a token.
 __global__ __launch_bounds__(kThreads)
@@ -36,7 +42,7 @@ void dispatch_rows_kernel(const uint4* __restrict__ x, int64_t chunks, int64_t M
     const int64_t slices = (chunks + 63) / 64, P = M * topk;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < P; i += (int64_t)gridDim.x * kThreads)
         if (i >= group_end[E - 1]) src_pair[i] = -1;      // past the last row
-    for (int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); u < M * slices; u += (int64_t)gridDim.x * kWaves) {
+    for (int64_t u = wave_number(); u < M * slices; u += (int64_t)gridDim.x * kWaves) {
         const int64_t t = u / slices, c = (u - t * slices) * 64 + lane_id();
         if (c >= chunks) continue;
         const uint4 v = x[t * chunks + c];
@@ -69,18 +75,31 @@ void combine_rows_kernel(const uint8_t* __restrict__ rows, int64_t R, int64_t K,
                          int topk, const float* __restrict__ weights, uint8_t* __restrict__ out)
 {
     const int64_t chunks = K / 8, slices = (chunks + 63) / 64, row_bytes = K * T::kBytes;
-    for (int64_t u = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); u < M * slices; u += (int64_t)gridDim.x * kWaves) {
+    for (int64_t u = wave_number(); u < M * slices; u += (int64_t)gridDim.x * kWaves) {
         const int64_t t = u / slices, c = (u - t * slices) * 64 + lane_id();
         if (c >= chunks) continue;
         float acc[8] = {};
-        for (int j = 0; j < topk; ++j) {
-            const int64_t r = row_of(pair_row, t * topk + j, R);
-            if (r < 0) continue;
-            const float w = weights ? weights[t * topk + j] : 1.0f;
-            float v[8];
-            T::unpack(T::load8(rows + r * row_bytes, c), v);
+        for (int j0 = 0; j0 < topk; j0 += kBatch) {
+            typename T::Raw v[kBatch];
+            float w[kBatch];
+            bool some[kBatch];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t p = t * topk + j0 + j, r = j0 + j < topk ? row_of(pair_row, p, R) : -1;
+                some[j] = r >= 0;
+                if (some[j]) {
+                    v[j] = T::load8(rows + r * row_bytes, c);
+                    w[j] = weights ? weights[p] : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (some[j]) {
+                    float f[8];
+                    T::unpack(v[j], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j], f[e], acc[e]);
+                }
         }
         T::store8(out + t * row_bytes, c, T::pack(acc));
     }

@@ -83,13 +83,19 @@ def add_layernorm(x: torch.Tensor, residual, weight: torch.Tensor, bias, eps: fl
     if x.dim() != 2:
         raise ValueError("x must be 2-D (M, K)")
     M, K = x.shape
+    code, dt = mxq._float_code(x, "x"), x.dtype
+    px, pr = mxq._dev(x, "x"), mxq._opt(residual, "residual", dt, M * K)
+    pw, pb = mxq._dev(weight, "weight", dt, K), mxq._opt(bias, "bias", dt, K)
+    # (outputs made here need no checks: a token's norm is host time)
     h = x if residual is None else torch.empty_like(x)
     y = torch.empty_like(x)
     q = torch.empty_like(x, dtype=torch.uint8)
     s = x.new_empty((M, K // 32), dtype=torch.uint8)
     mean = x.new_empty(M, dtype=torch.float32)
     rstd = x.new_empty(M, dtype=torch.float32)
-    mxq.mxq_add_layernorm(x, residual, weight, bias, eps, None if residual is None else h, y, q, s, mean, rstd)
+    mxq._check(mxq.lib().mxq_add_layernorm(px, pr, pw, pb, code, M, K, eps, 0 if residual is None else h.data_ptr(),
+                                           y.data_ptr(), q.data_ptr(), s.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                           mxq._stream(None)), "mxq_add_layernorm")
     return h, y, q, s, mean, rstd
 
 

@@ -104,6 +104,14 @@ CASES = [
     (700, 2048, 8, [699]),
     (130, 8200, 24, [65, 130]),
     (64, 24, 8200, [10, 64]),
+    # rows enough for tiles (the smaller ones above go to the kernel for few rows)
+    (600, 264, 16392, [120, 250]),                         # few tiles, a long sum: in parts
+    (600, 16392, 264, [3, 290, 290]),
+    (1100, 1032, 1288, [300, 300, 301, 560, 577, 1099]),
+    (1100, 1288, 1032, [64, 129, 1000]),
+    (5000, 520, 456, [1300, 1300, 2600, 2601, 4990]),
+    (20000, 264, 264, [300 * i for i in range(1, 66)]),    # 65 groups, their last tiles of 44 rows
+    (300, 2696, 2696, [0, 300]),
 ]
 
 
@@ -118,7 +126,7 @@ def test_integers_are_exact(M, N, K, ends, product, out):
 
 
 @pytest.mark.parametrize("product", ["y", "dx", "dw"])
-@pytest.mark.parametrize("M,N,K,ends", [c for c in CASES if c[0] in (8, 200, 257, 777, 2000, 4100)],
+@pytest.mark.parametrize("M,N,K,ends", [c for c in CASES if c[0] in (8, 200, 257, 600, 777, 1100, 2000, 4100)],
                          ids=lambda v: str(v) if isinstance(v, int) else f"g{len(v)}")
 def test_real_values(M, N, K, ends, product):
     def make(shape, g):
