@@ -20,6 +20,14 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBatch = 8;                                 // rows of a token in flight at once
 constexpr int kMaxGrid = 1 << 22;
+// What does not fit the 256 MB last-level cache is read as a stream (8192 tokens x 8 rows x 5120,
+// combine 136 -> 126 us, its gradients 288 -> 270; 16640 tokens to 2 rows each 93 -> 87); less may be
+// there, where its writer left it.
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
+template <bool NT>
+__device__ __forceinline__ uint4 load16(const uint4* p) { return NT ? load_nt(p) : *p; }
+template <class T, bool NT>
+__device__ __forceinline__ typename T::Raw load8(const void* row, int64_t i) { return NT ? T::load8_nt(row, i) : T::load8(row, i); }
 
 // Row of pair p, -1 for none.
 __device__ __forceinline__ int64_t row_of(const int32_t* pair_row, int64_t p, int64_t R)
@@ -35,6 +43,7 @@ __device__ __forceinline__ int64_t wave_number()
 }
 
 // A wave takes 64 chunks of 16 bytes of a token.
+template <bool NT>
 __global__ __launch_bounds__(kThreads)
 void dispatch_rows_kernel(const uint4* __restrict__ x, int64_t chunks, int64_t M, int topk, const int32_t* __restrict__ pair_row,
                           const int32_t* __restrict__ group_end, int E, uint4* __restrict__ rows, int32_t* __restrict__ src_pair)
@@ -45,7 +54,7 @@ void dispatch_rows_kernel(const uint4* __restrict__ x, int64_t chunks, int64_t M
     for (int64_t u = wave_number(); u < M * slices; u += (int64_t)gridDim.x * kWaves) {
         const int64_t t = u / slices, c = (u - t * slices) * 64 + lane_id();
         if (c >= chunks) continue;
-        const uint4 v = x[t * chunks + c];
+        const uint4 v = load16<NT>(x + t * chunks + c);
         for (int j = 0; j < topk; ++j) {
             const int64_t r = row_of(pair_row, t * topk + j, P);
             if (r >= 0) rows[r * chunks + c] = v;
@@ -69,7 +78,7 @@ void pair_rows_kernel(const int32_t* __restrict__ src_pair, int64_t n, int32_t* 
 }
 
 // A wave takes 64 chunks of 8 values of a token.
-template <class T>
+template <class T, bool NT>
 __global__ __launch_bounds__(kThreads)
 void combine_rows_kernel(const uint8_t* __restrict__ rows, int64_t R, int64_t K, const int32_t* __restrict__ pair_row, int64_t M,
                          int topk, const float* __restrict__ weights, uint8_t* __restrict__ out)
@@ -88,7 +97,7 @@ void combine_rows_kernel(const uint8_t* __restrict__ rows, int64_t R, int64_t K,
                 const int64_t p = t * topk + j0 + j, r = j0 + j < topk ? row_of(pair_row, p, R) : -1;
                 some[j] = r >= 0;
                 if (some[j]) {
-                    v[j] = T::load8(rows + r * row_bytes, c);
+                    v[j] = load8<T, NT>(rows + r * row_bytes, c);
                     w[j] = weights ? weights[p] : 1.0f;
                 }
             }
@@ -105,8 +114,9 @@ void combine_rows_kernel(const uint8_t* __restrict__ rows, int64_t R, int64_t K,
     }
 }
 
-// A workgroup takes a token and kBatch of its slots.  dweights null: only drows.
-template <class T>
+// A workgroup takes a token and kBatch of its slots.  dweights null: only drows.  A chunk of all
+// the rows is read before any is written (drows may be rows).
+template <class T, bool NT>
 __global__ __launch_bounds__(kThreads)
 void combine_rows_bwd_kernel(const uint8_t* __restrict__ dout, const uint8_t* rows, int64_t R, int64_t K,
                              const int32_t* __restrict__ pair_row, int64_t M, int topk, const float* __restrict__ weights,
@@ -121,24 +131,30 @@ void combine_rows_bwd_kernel(const uint8_t* __restrict__ dout, const uint8_t* ro
         const int64_t p0 = t * topk + j0;
         float dot[kBatch] = {};
         for (int64_t c = threadIdx.x; c < chunks; c += kThreads) {
-            float d[8];
-            T::unpack(T::load8(dout + t * row_bytes, c), d);
+            const typename T::Raw dr = T::load8(dout + t * row_bytes, c);
+            typename T::Raw v[kBatch];
+            int64_t row[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                if (j >= n) continue;
-                const int64_t r = row_of(pair_row, p0 + j, R);
-                if (r < 0) continue;
-                if (dweights) {
-                    float v[8];
-                    T::unpack(T::load8(rows + r * row_bytes, c), v);
+                row[j] = j < n ? row_of(pair_row, p0 + j, R) : -1;
+                if (dweights && row[j] >= 0) v[j] = load8<T, NT>(rows + row[j] * row_bytes, c);
+            }
+            float d[8];
+            T::unpack(dr, d);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], v[e], dot[j]);
+            for (int j = 0; j < kBatch; ++j) {
+                if (row[j] < 0) continue;
+                if (dweights) {
+                    float f[8];
+                    T::unpack(v[j], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
                 }
                 const float w = weights ? weights[p0 + j] : 1.0f;
                 float o[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o[e] = w * d[e];
-                T::store8(drows + r * row_bytes, c, T::pack(o));
+                T::store8(drows + row[j] * row_bytes, c, T::pack(o));
             }
         }
         if (!dweights) continue;
@@ -165,8 +181,13 @@ hipError_t launch_dispatch_rows(const void* x, int64_t row_bytes, int64_t M, int
                                 const int32_t* group_end, int E, void* rows, int32_t* src_pair, hipStream_t stream)
 {
     const int64_t chunks = row_bytes / 16, waves = M * ((chunks + 63) / 64);
-    hipLaunchKernelGGL(dispatch_rows_kernel, dim3(capped((waves + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream,
-                       (const uint4*)x, chunks, M, topk, pair_row, group_end, E, (uint4*)rows, src_pair);
+    const dim3 grid(capped((waves + kWaves - 1) / kWaves));
+    if (M * row_bytes * (1 + topk) > kCacheBytes)
+        hipLaunchKernelGGL(dispatch_rows_kernel<true>, grid, dim3(kThreads), 0, stream, (const uint4*)x, chunks, M, topk, pair_row,
+                           group_end, E, (uint4*)rows, src_pair);
+    else
+        hipLaunchKernelGGL(dispatch_rows_kernel<false>, grid, dim3(kThreads), 0, stream, (const uint4*)x, chunks, M, topk, pair_row,
+                           group_end, E, (uint4*)rows, src_pair);
     return hipGetLastError();
 }
 
@@ -178,31 +199,40 @@ hipError_t launch_pair_rows(const int32_t* src_pair, int64_t pairs, int32_t* pai
     return hipGetLastError();
 }
 
+#define MXQ_TYPES(CALL)                          \
+    do {                                         \
+        const bool nt = bytes > kCacheBytes;     \
+        if (f32 && nt) CALL(F32, true);          \
+        else if (f32) CALL(F32, false);          \
+        else if (nt) CALL(Bf16, true);           \
+        else CALL(Bf16, false);                  \
+    } while (0)
+
 hipError_t launch_combine_rows(const void* rows, bool f32, int64_t R, int64_t K, const int32_t* pair_row, int64_t M, int topk,
                                const float* weights, void* out, hipStream_t stream)
 {
-    const int64_t waves = M * ((K / 8 + 63) / 64);
+    const int64_t waves = M * ((K / 8 + 63) / 64), bytes = M * topk * K * (f32 ? 4 : 2);
     const dim3 grid(capped((waves + kWaves - 1) / kWaves));
-    if (f32)
-        hipLaunchKernelGGL(combine_rows_kernel<F32>, grid, dim3(kThreads), 0, stream, (const uint8_t*)rows, R, K, pair_row, M,
-                           topk, weights, (uint8_t*)out);
-    else
-        hipLaunchKernelGGL(combine_rows_kernel<Bf16>, grid, dim3(kThreads), 0, stream, (const uint8_t*)rows, R, K, pair_row, M,
-                           topk, weights, (uint8_t*)out);
+#define MXQ_CALL(T, NT)                                                                                                      \
+    hipLaunchKernelGGL((combine_rows_kernel<T, NT>), grid, dim3(kThreads), 0, stream, (const uint8_t*)rows, R, K, pair_row, M, \
+                       topk, weights, (uint8_t*)out)
+    MXQ_TYPES(MXQ_CALL);
+#undef MXQ_CALL
     return hipGetLastError();
 }
 
 hipError_t launch_combine_rows_bwd(const void* dout, const void* rows, bool f32, int64_t R, int64_t K, const int32_t* pair_row,
                                    int64_t M, int topk, const float* weights, void* drows, float* dweights, hipStream_t stream)
 {
+    const int64_t bytes = M * topk * K * (f32 ? 4 : 2) * 2;
     const dim3 grid(capped(M * ((topk + kBatch - 1) / kBatch)));
-    if (f32)
-        hipLaunchKernelGGL(combine_rows_bwd_kernel<F32>, grid, dim3(kThreads), 0, stream, (const uint8_t*)dout,
-                           (const uint8_t*)rows, R, K, pair_row, M, topk, weights, (uint8_t*)drows, dweights);
-    else
-        hipLaunchKernelGGL(combine_rows_bwd_kernel<Bf16>, grid, dim3(kThreads), 0, stream, (const uint8_t*)dout,
-                           (const uint8_t*)rows, R, K, pair_row, M, topk, weights, (uint8_t*)drows, dweights);
+#define MXQ_CALL(T, NT)                                                                                            \
+    hipLaunchKernelGGL((combine_rows_bwd_kernel<T, NT>), grid, dim3(kThreads), 0, stream, (const uint8_t*)dout,    \
+                       (const uint8_t*)rows, R, K, pair_row, M, topk, weights, (uint8_t*)drows, dweights)
+    MXQ_TYPES(MXQ_CALL);
+#undef MXQ_CALL
     return hipGetLastError();
 }
+#undef MXQ_TYPES
 
 }  // namespace mxq
