@@ -8,9 +8,9 @@
 //   y = (h - m) * rstd * w + b      rounded once to the stored type;
 //   q, s = the MXFP8 encoding of y rounded to bf16.
 // The row is in registers, so the squares are those of the differences from a mean that is
-// already known (mean(h^2) - m^2 loses everything when m^2 is large next to v).  The sum of
-// those differences, which rounding of the mean leaves above zero, is taken in the same
-// pass: m gets its mean added, v its mean's square taken off.
+// already known (mean(h^2) - m^2 loses everything when m^2 is large next to v).  That mean is
+// cut to 16 bits; what it lacks is the mean of those differences, taken in the same pass: m
+// gets it added, v its square taken off.
 //
 // Backward, with n = (h - m) * rstd and g = dy * w:
 //   dx = rstd * (g - mean(g) - n * mean(g * n)) + dh      (the gradient of x and of r alike)
@@ -110,7 +110,9 @@ void add_layernorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __r
                 for (int e = 0; e < 8; ++e) t[e] += a[e];
             }
         }
-        const float m0 = row_sums<LANES>(sum8(t), 0.0f, sh, 0).x / (float)K;
+        // (cut to 16 bits, so that the differences of bf16 values from it are exact: their roundings
+        // are alike over a row, and the mean lacked half a unit of them)
+        const float m0 = __uint_as_float(__float_as_uint(row_sums<LANES>(sum8(t), 0.0f, sh, 0).x / (float)K) & 0xFFFFFF00u);
         float d1[8] = {}, d2[8] = {};
 #pragma unroll
         for (int c = 0; c < C; ++c) {

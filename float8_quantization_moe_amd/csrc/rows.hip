@@ -21,8 +21,8 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kBatch = 8;                                 // rows of a token in flight at once
 constexpr int kMaxGrid = 1 << 22;
 // What does not fit the 256 MB last-level cache is read as a stream (8192 tokens x 8 rows x 5120,
-// combine 136 -> 126 us, its gradients 288 -> 270; 16640 tokens to 2 rows each 93 -> 87); less may be
-// there, where its writer left it.
+// combine 136 -> 126 us, its gradients 288 -> 270), and dispatched rows written as one (16640 tokens to
+// 2 rows each 101 -> 93); less may be there, where its writer left it.
 constexpr int64_t kCacheBytes = (int64_t)256 << 20;
 template <bool NT>
 __device__ __forceinline__ uint4 load16(const uint4* p) { return NT ? load_nt(p) : *p; }
@@ -57,7 +57,9 @@ void dispatch_rows_kernel(const uint4* __restrict__ x, int64_t chunks, int64_t M
         const uint4 v = load16<NT>(x + t * chunks + c);
         for (int j = 0; j < topk; ++j) {
             const int64_t r = row_of(pair_row, t * topk + j, P);
-            if (r >= 0) rows[r * chunks + c] = v;
+            if (r < 0) continue;
+            if constexpr (NT) store_nt(v, rows + r * chunks + c);
+            else rows[r * chunks + c] = v;
         }
     }
 }

@@ -18,24 +18,42 @@ def _on(stream, t: torch.Tensor):
     return torch.cuda.stream(mxq._stream_of(stream, t))
 
 
-def _workspace(like: torch.Tensor, size: int):
-    """Scratch of `size` bytes on like's device; None for none."""
-    return like.new_empty(size, dtype=torch.uint8) if size else None
+def _scratch(like: torch.Tensor, size: int):
+    """(tensor to keep, address, bytes) of a workspace on like's device."""
+    if size == 0:
+        return None, 0, 0
+    t = like.new_empty(size, dtype=torch.uint8)
+    return t, t.data_ptr(), size
 
+
+# (Outputs and workspaces made here need no checks, so the helpers call the library themselves:
+# a small call is host time.)
 
 # ------------------------------------------------------------- products ---
+def _out_code(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return mxq.MXQ_OUT_BF16
+    if dtype == torch.float32:
+        return mxq.MXQ_OUT_F32
+    raise TypeError(f"out_dtype must be bfloat16 or float32, got {dtype}")
+
+
 def bf16_grouped_mm(x: torch.Tensor, w: torch.Tensor, group_end_offs: torch.Tensor, out_dtype=torch.bfloat16,
                     stream=None) -> torch.Tensor:
     """y (M, N) = each row of x (M, K) times its group's w (G, N, K) transposed."""
     if stream is not None:
         with _on(stream, x):
             return bf16_grouped_mm(x, w, group_end_offs, out_dtype)
-    if x.dim() != 2 or w.dim() != 3:
+    if x.dim() != 2 or w.dim() != 3 or x.shape[1] != w.shape[2]:
         raise ValueError("x must be (M, K) and w (G, N, K)")
     M, (G, N, K) = x.shape[0], w.shape
+    code, L = _out_code(out_dtype), mxq.lib()
+    px, pw = mxq._dev(x, "x", torch.bfloat16), mxq._dev(w, "w", torch.bfloat16)
+    po = mxq._dev(group_end_offs, "group_end_offs", torch.int32, G)
     y = x.new_empty((M, N), dtype=out_dtype)
-    ws = _workspace(x, mxq.mxq_bf16_grouped_mm_workspace_bytes(mxq.MXQ_PRODUCT_Y, M, N, K, G))
-    mxq.mxq_bf16_grouped_mm(x, w, group_end_offs, y, ws)
+    ws, at, size = _scratch(x, L.mxq_bf16_grouped_mm_workspace_bytes(mxq.MXQ_PRODUCT_Y, M, N, K, G))
+    mxq._check(L.mxq_bf16_grouped_mm(px, pw, po, M, N, K, G, code, y.data_ptr(), at, size, mxq._stream(None)),
+               "mxq_bf16_grouped_mm")
     return y
 
 
@@ -45,12 +63,16 @@ def bf16_grouped_mm_dx(dy: torch.Tensor, w: torch.Tensor, group_end_offs: torch.
     if stream is not None:
         with _on(stream, dy):
             return bf16_grouped_mm_dx(dy, w, group_end_offs, out_dtype)
-    if dy.dim() != 2 or w.dim() != 3:
+    if dy.dim() != 2 or w.dim() != 3 or dy.shape[1] != w.shape[1]:
         raise ValueError("dy must be (M, N) and w (G, N, K)")
     M, (G, N, K) = dy.shape[0], w.shape
+    code, L = _out_code(out_dtype), mxq.lib()
+    pd, pw = mxq._dev(dy, "dy", torch.bfloat16), mxq._dev(w, "w", torch.bfloat16)
+    po = mxq._dev(group_end_offs, "group_end_offs", torch.int32, G)
     dx = dy.new_empty((M, K), dtype=out_dtype)
-    ws = _workspace(dy, mxq.mxq_bf16_grouped_mm_workspace_bytes(mxq.MXQ_PRODUCT_DX, M, N, K, G))
-    mxq.mxq_bf16_grouped_mm_dx(dy, w, group_end_offs, dx, ws)
+    ws, at, size = _scratch(dy, L.mxq_bf16_grouped_mm_workspace_bytes(mxq.MXQ_PRODUCT_DX, M, N, K, G))
+    mxq._check(L.mxq_bf16_grouped_mm_dx(pd, pw, po, M, N, K, G, code, dx.data_ptr(), at, size, mxq._stream(None)),
+               "mxq_bf16_grouped_mm_dx")
     return dx
 
 
@@ -61,16 +83,23 @@ def bf16_grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, group_end_offs: torch.
     if stream is not None:
         with _on(stream, dy):
             return bf16_grouped_mm_dw(dy, x, group_end_offs, out_dtype, dw)
-    if dy.dim() != 2 or x.dim() != 2:
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
         raise ValueError("dy must be (M, N) and x (M, K)")
     (M, N), K, G = dy.shape, x.shape[1], group_end_offs.numel()
     add = dw is not None
     if add and tuple(dw.shape) != (G, N, K):
         raise ValueError("dw must be (G, N, K)")
-    if not add:
-        dw = dy.new_empty((G, N, K), dtype=out_dtype)
-    ws = _workspace(dy, mxq.mxq_bf16_grouped_mm_workspace_bytes(mxq.MXQ_PRODUCT_DW, M, N, K, G))
-    mxq.mxq_bf16_grouped_mm_dw(dy, x, group_end_offs, dw, add, ws)
+    L = mxq.lib()
+    pd, px = mxq._dev(dy, "dy", torch.bfloat16), mxq._dev(x, "x", torch.bfloat16)
+    po = mxq._dev(group_end_offs, "group_end_offs", torch.int32)
+    if add:
+        code, pw = mxq._float_code(dw, "dw"), mxq._dev(dw, "dw")
+    else:
+        code, dw = _out_code(out_dtype), dy.new_empty((G, N, K), dtype=out_dtype)
+        pw = dw.data_ptr()
+    ws, at, size = _scratch(dy, L.mxq_bf16_grouped_mm_workspace_bytes(mxq.MXQ_PRODUCT_DW, M, N, K, G))
+    mxq._check(L.mxq_bf16_grouped_mm_dw(pd, px, po, M, N, K, G, code, int(add), pw, at, size, mxq._stream(None)),
+               "mxq_bf16_grouped_mm_dw")
     return dw
 
 
@@ -86,7 +115,6 @@ def add_layernorm(x: torch.Tensor, residual, weight: torch.Tensor, bias, eps: fl
     code, dt = mxq._float_code(x, "x"), x.dtype
     px, pr = mxq._dev(x, "x"), mxq._opt(residual, "residual", dt, M * K)
     pw, pb = mxq._dev(weight, "weight", dt, K), mxq._opt(bias, "bias", dt, K)
-    # (outputs made here need no checks: a token's norm is host time)
     h = x if residual is None else torch.empty_like(x)
     y = torch.empty_like(x)
     q = torch.empty_like(x, dtype=torch.uint8)
@@ -108,11 +136,16 @@ def add_layernorm_bwd(h: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
     if h.dim() != 2:
         raise ValueError("h must be 2-D (M, K)")
     M, K = h.shape
+    code, dt, n, L = mxq._float_code(h, "h"), h.dtype, M * K, mxq.lib()
+    ph, pw = mxq._dev(h, "h"), mxq._dev(weight, "weight", dt, K)
+    pm, pr = mxq._dev(mean, "mean", torch.float32, M), mxq._dev(rstd, "rstd", torch.float32, M)
+    pg, pd = mxq._dev(dy, "dy", dt, n), mxq._opt(dh, "dh", dt, n)
     dx = torch.empty_like(h)
     dweight = h.new_empty(K, dtype=torch.float32)
     dbias = h.new_empty(K, dtype=torch.float32)
-    ws = h.new_empty(max(mxq.mxq_add_layernorm_bwd_workspace_bytes(M, K), 16), dtype=torch.uint8)
-    mxq.mxq_add_layernorm_bwd(h, weight, mean, rstd, dy, dh, dx, dweight, dbias, ws)
+    ws, at, size = _scratch(h, L.mxq_add_layernorm_bwd_workspace_bytes(M, K))
+    mxq._check(L.mxq_add_layernorm_bwd(ph, pw, pm, pr, pg, pd, code, M, K, dx.data_ptr(), dweight.data_ptr(),
+                                       dbias.data_ptr(), at, size, mxq._stream(None)), "mxq_add_layernorm_bwd")
     return dx, dweight, dbias
 
 
@@ -122,15 +155,18 @@ def dispatch_rows(x: torch.Tensor, expert_ids: torch.Tensor, E: int, stream=None
     if stream is not None:
         with _on(stream, x):
             return dispatch_rows(x, expert_ids, E)
-    if x.dim() != 2 or expert_ids.dim() != 2:
+    if x.dim() != 2 or expert_ids.dim() != 2 or x.shape[0] != expert_ids.shape[0]:
         raise ValueError("x must be (M, K) and expert_ids (M, topk)")
-    K, (M, topk) = x.shape[1], expert_ids.shape
+    K, (M, topk), E = x.shape[1], expert_ids.shape, int(E)
+    code, L = mxq._float_code(x, "x"), mxq.lib()
+    px, pi = mxq._dev(x, "x"), mxq._dev(expert_ids, "expert_ids", torch.int32)
     rows = x.new_empty((M * topk, K))
-    ends = x.new_empty(int(E), dtype=torch.int32)
+    ends = x.new_empty(E, dtype=torch.int32)
     src = x.new_empty(M * topk, dtype=torch.int32)
     place = x.new_empty((M, topk), dtype=torch.int32)
-    ws = x.new_empty(max(mxq.mxq_dispatch_rows_workspace_bytes(M, topk, E), 16), dtype=torch.uint8)
-    mxq.mxq_dispatch_rows(x, expert_ids, E, rows, ends, src, place, ws)
+    ws, at, size = _scratch(x, L.mxq_dispatch_rows_workspace_bytes(M, topk, E))
+    mxq._check(L.mxq_dispatch_rows(px, code, M, K, pi, topk, E, rows.data_ptr(), ends.data_ptr(), src.data_ptr(),
+                                   place.data_ptr(), at, size, mxq._stream(None)), "mxq_dispatch_rows")
     return rows, ends, src, place
 
 
@@ -151,8 +187,12 @@ def combine_rows(rows: torch.Tensor, pair_row: torch.Tensor, weights=None, strea
             return combine_rows(rows, pair_row, weights)
     if rows.dim() != 2 or pair_row.dim() != 2:
         raise ValueError("rows must be (R, K) and pair_row (M, topk)")
-    out = rows.new_empty((pair_row.shape[0], rows.shape[1]))
-    mxq.mxq_combine_rows(rows, pair_row, weights, out)
+    (R, K), (M, topk) = rows.shape, pair_row.shape
+    code, pr = mxq._float_code(rows, "rows"), mxq._dev(rows, "rows")
+    pp, pw = mxq._dev(pair_row, "pair_row", torch.int32), mxq._opt(weights, "weights", torch.float32, M * topk)
+    out = rows.new_empty((M, K))
+    mxq._check(mxq.lib().mxq_combine_rows(pr, code, R, K, pp, M, topk, pw, out.data_ptr(), mxq._stream(None)),
+               "mxq_combine_rows")
     return out
 
 
@@ -161,9 +201,13 @@ def combine_rows_bwd(dout: torch.Tensor, rows: torch.Tensor, pair_row: torch.Ten
     if stream is not None:
         with _on(stream, dout):
             return combine_rows_bwd(dout, rows, pair_row, weights)
-    if rows.dim() != 2 or pair_row.dim() != 2:
-        raise ValueError("rows must be (R, K) and pair_row (M, topk)")
+    if dout.dim() != 2 or rows.dim() != 2 or pair_row.dim() != 2:
+        raise ValueError("dout must be (M, K), rows (R, K) and pair_row (M, topk)")
+    (R, K), (M, topk), dt = rows.shape, pair_row.shape, dout.dtype
+    code, pd, pr = mxq._float_code(dout, "dout"), mxq._dev(dout, "dout", dt, M * K), mxq._dev(rows, "rows", dt)
+    pp, pw = mxq._dev(pair_row, "pair_row", torch.int32), mxq._opt(weights, "weights", torch.float32, M * topk)
     drows = torch.empty_like(rows)
-    dweights = dout.new_empty(pair_row.shape, dtype=torch.float32)
-    mxq.mxq_combine_rows_bwd(dout, rows, pair_row, weights, drows, dweights)
+    dweights = dout.new_empty((M, topk), dtype=torch.float32)
+    mxq._check(mxq.lib().mxq_combine_rows_bwd(pd, pr, code, R, K, pp, M, topk, pw, drows.data_ptr(), dweights.data_ptr(),
+                                              mxq._stream(None)), "mxq_combine_rows_bwd")
     return drows, dweights
