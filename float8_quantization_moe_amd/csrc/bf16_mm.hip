@@ -846,24 +846,49 @@ bool bf16_mm_sizes_ok(int product, int64_t M, int64_t N, int64_t K, int64_t G)
     return rows < ((int64_t)1 << 30) / cols;
 }
 
+// Parts of a product's sums.
+static int split_of(int product, int64_t M, int64_t N, int64_t K, int64_t G)
+{
+    if (M == 0) return 1;
+    if (few_rows(product, M, N, K)) return bf16_mm_few_split(product == MXQ_PRODUCT_DX, (int)M, (int)N, (int)K, (int)G);
+    return plan_of(product, M, N, K, G).split;
+}
+
 size_t bf16_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 {
-    if (M == 0 || few_rows(product, M, N, K)) return 0;
-    const int split = plan_of(product, M, N, K, G).split;
+    const int split = split_of(product, M, N, K, G);
     return split > 1 ? (size_t)split * (size_t)results_of(product, M, N, K, G) * 4u : 0;
+}
+
+static hipError_t join_parts(const void* parts, int split, int64_t results, void* out, bool f32_out, bool accumulate,
+                             hipStream_t stream)
+{
+    const int64_t n4 = results / 4, blocks = (n4 + kThreads - 1) / kThreads;
+    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
+    if (f32_out)
+        hipLaunchKernelGGL(join_parts_kernel<true>, grid, dim3(kThreads), 0, stream, (const float4*)parts, split, n4, out,
+                           (int)accumulate);
+    else
+        hipLaunchKernelGGL(join_parts_kernel<false>, grid, dim3(kThreads), 0, stream, (const float4*)parts, split, n4, out, 0);
+    return hipGetLastError();
 }
 
 hipError_t launch_bf16_mm(int product, const void* rows, const void* other, const int32_t* offs, int M, int N, int K, int G,
                           void* out, bool f32_out, bool accumulate, void* workspace, hipStream_t stream)
 {
-    if (few_rows(product, M, N, K))
-        return launch_bf16_mm_few(rows, other, product == MXQ_PRODUCT_DX, offs, M, N, K, G, out, f32_out, stream);
+    const int split = split_of(product, M, N, K, G);
+    const bool joined = split > 1;
+    if (few_rows(product, M, N, K)) {
+        const hipError_t e = launch_bf16_mm_few(rows, other, product == MXQ_PRODUCT_DX, offs, M, N, K, G, split,
+                                                joined ? workspace : out, f32_out || joined, stream);
+        if (e != hipSuccess || !joined) return e;
+        return join_parts(workspace, split, results_of(product, M, N, K, G), out, f32_out, false, stream);
+    }
     int device = 0, cus = 0;
     hipError_t e = hipGetDevice(&device);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
     if (e != hipSuccess) return e;
     const Plan p = plan_of(product, M, N, K, G);
-    const bool joined = M > 0 && p.split > 1;
     // One workgroup a CU, fewer when there are not that many tiles (their row parts counted), a
     // multiple of it when a workgroup's list would not hold its tiles: an XCD's stretch of the
     // work has at most kCostWhole / kCostQuarter times an eighth of the tiles and two, a
@@ -875,7 +900,7 @@ hipError_t launch_bf16_mm(int product, const void* rows, const void* other, cons
     grid = (grid + kXcds - 1) / kXcds * kXcds;
     const bool wide = f32_out || joined;
     const MmArgs a = {(const uint16_t*)other, (const uint16_t*)rows, offs, joined ? workspace : out, M, N, K, G, p.rows,
-                      joined ? p.split : 1};
+                      split};
 #define MXQ_LAUNCH(P, F32, ADD) \
     hipLaunchKernelGGL((bf16_mm_kernel<P, F32, ADD>), dim3((unsigned)grid), dim3(kThreads), 0, stream, a)
     if (product == MXQ_PRODUCT_DW && accumulate && !joined) MXQ_LAUNCH(MXQ_PRODUCT_DW, true, true);
@@ -886,17 +911,8 @@ hipError_t launch_bf16_mm(int product, const void* rows, const void* other, cons
     else if (wide) MXQ_LAUNCH(MXQ_PRODUCT_Y, true, false);
     else MXQ_LAUNCH(MXQ_PRODUCT_Y, false, false);
 #undef MXQ_LAUNCH
-    if (joined) {
-        const int64_t n4 = results_of(product, M, N, K, G) / 4;
-        const int64_t blocks = (n4 + kThreads - 1) / kThreads;
-        const dim3 g((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
-        if (f32_out)
-            hipLaunchKernelGGL(join_parts_kernel<true>, g, dim3(kThreads), 0, stream, (const float4*)workspace, p.split, n4, out,
-                               (int)accumulate);
-        else
-            hipLaunchKernelGGL(join_parts_kernel<false>, g, dim3(kThreads), 0, stream, (const float4*)workspace, p.split, n4, out, 0);
-    }
-    return hipGetLastError();
+    if (!joined) return hipGetLastError();
+    return join_parts(workspace, split, results_of(product, M, N, K, G), out, f32_out, accumulate, stream);
 }
 
 }  // namespace mxq

@@ -33,8 +33,9 @@ typedef __attribute__((address_space(3))) v4s* LdsV4s;
 struct FewArgs {
     const uint16_t *w, *rows;
     const int32_t* offs;
-    void* out;
+    void* out;                                           // split > 1: the parts, fp32
     int M, N, K, G;
+    int split;                                           // workgroups that share a sum
 };
 
 // Rows of one workgroup.
@@ -96,19 +97,27 @@ void bf16_mm_few_kernel(const FewArgs a)
     const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
     const Chunk c = find_chunk(a, (int)blockIdx.y, 16 * TB);
     const int cols = ACROSS ? a.K : a.N, depth = ACROSS ? a.N : a.K;
-    const int c0 = (int)blockIdx.x * kCols;
+    // "Across", a memory row's 128 bytes may end inside a line, and the next ones are the next
+    // workgroup's: four neighbours share an XCD (workgroup index mod 8).  16 experts of 8192 x 5120, 16
+    // rows: 141 -> 127 us; 7 of 3168 x 3160: 28 -> 23; 4 of 4096 x 4096: 18.6 -> 19.4.
+    constexpr int kNear = 4, kRound = 8 * kNear;
+    const int at = (int)blockIdx.x % kRound, round = (int)blockIdx.x - at;
+    const int c0 = (ACROSS && round + kRound <= (int)gridDim.x ? round + at % 8 * kNear + at / 8 : (int)blockIdx.x) * kCols;
+
+    uint8_t* out = (uint8_t*)a.out + (int64_t)blockIdx.z * a.M * cols * (F32OUT ? 4 : 2);
 
     if (blockIdx.y == 0) {                               // rows past the last end: zeros
         constexpr int kPer = F32OUT ? 4 : 8;             // values of 16 bytes
         const int width = (cols - c0 < kCols ? cols - c0 : kCols) / kPer;
         for (int i = (int)threadIdx.x; i < (a.M - c.rows_end) * width; i += kThreads)
-            ((uint4*)a.out)[((int64_t)(c.rows_end + i / width) * cols + c0) / kPer + i % width] = make_uint4(0, 0, 0, 0);
+            ((uint4*)out)[((int64_t)(c.rows_end + i / width) * cols + c0) / kPer + i % width] = make_uint4(0, 0, 0, 0);
     }
     if (c.g < 0) return;
 
     // this wave's steps of the sum, and the resources at the first
     const int steps = (depth + kStepK - 1) / kStepK;
-    const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
+    const int pieces = kWaves * a.split, piece = kWaves * (int)blockIdx.z + wave;
+    const int s0 = (int)((int64_t)steps * piece / pieces), s1 = (int)((int64_t)steps * (piece + 1) / pieces);
     const uint32_t lda = 2u * (uint32_t)a.K, ldb = 2u * (uint32_t)depth;
     const int rows = c.r1 - c.r0, width = cols - c0 < kCols ? cols - c0 : kCols;
     const uint16_t* wbase = a.w + ((int64_t)c.g * a.N + (ACROSS ? 0 : c0)) * a.K + (ACROSS ? c0 : 0);
@@ -208,22 +217,47 @@ void bf16_mm_few_kernel(const FewArgs a)
         const int row = c.r0 + 16 * j + (int)r;
         if (row < c.r1 && col < cols) {
             const int64_t at = (int64_t)row * cols + col;
-            if constexpr (F32OUT) *(v4f*)((float*)a.out + at) = sum;
-            else *(uint2*)((uint16_t*)a.out + at) = make_uint2(f32_pair_to_bf16(sum[0], sum[1]), f32_pair_to_bf16(sum[2], sum[3]));
+            if constexpr (F32OUT) *(v4f*)((float*)out + at) = sum;
+            else *(uint2*)((uint16_t*)out + at) = make_uint2(f32_pair_to_bf16(sum[0], sum[1]), f32_pair_to_bf16(sum[2], sum[3]));
         }
     }
 }
 
 }  // namespace
 
-hipError_t launch_bf16_mm_few(const void* rows, const void* w, bool across, const int32_t* offs, int M, int N, int K, int G,
-                              void* out, bool f32_out, hipStream_t stream)
+// 16-row parts of a workgroup.
+static int few_parts(int M, int G)
 {
-    const FewArgs a = {(const uint16_t*)w, (const uint16_t*)rows, offs, out, M, N, K, G};
     const int groups = G < M ? G : M;
-    const int parts = M <= 16 ? 1 : M <= 32 * groups ? 2 : 4;
-    const int cols = across ? K : N, height = 16 * parts;
-    const dim3 grid((unsigned)((cols + kCols - 1) / kCols), (unsigned)((M + height - 1) / height + (G < M ? G : M) - 1));
+    return M <= 16 ? 1 : M <= 32 * groups ? 2 : 4;
+}
+static dim3 few_grid(bool across, int M, int N, int K, int G)
+{
+    const int cols = across ? K : N, height = 16 * few_parts(M, G);
+    return dim3((unsigned)((cols + kCols - 1) / kCols), (unsigned)((M + height - 1) / height + (G < M ? G : M) - 1));
+}
+
+// Workgroups that share a sum, and then a second launch that adds the parts: where there are few and
+// their waves' sums are long (142 rows x 6416 x 552, dX 33 -> 15 us; one row 13 -> 9; 142 rows x 512 x
+// 4096 over 8 experts, Y, sums of 64 steps, 12 -> 15).
+int bf16_mm_few_split(bool across, int M, int N, int K, int G)
+{
+    const dim3 grid = few_grid(across, M, N, K, G);
+    const int64_t groups = (int64_t)grid.x * grid.y;
+    const int steps = ((across ? N : K) + kStepK - 1) / kStepK;
+    if (groups > 128 || steps < 20 * kWaves) return 1;
+    int64_t split = 512 / groups;
+    if (split > steps / (3 * kWaves)) split = steps / (3 * kWaves);
+    return (int)(split < 16 ? split : 16);
+}
+
+hipError_t launch_bf16_mm_few(const void* rows, const void* w, bool across, const int32_t* offs, int M, int N, int K, int G,
+                              int split, void* out, bool f32_out, hipStream_t stream)
+{
+    const FewArgs a = {(const uint16_t*)w, (const uint16_t*)rows, offs, out, M, N, K, G, split};
+    const int parts = few_parts(M, G);
+    dim3 grid = few_grid(across, M, N, K, G);
+    grid.z = (unsigned)split;
 #define MXQ_LAUNCH(T, F)                                                                                                \
     do {                                                                                                                \
         if (across) hipLaunchKernelGGL((bf16_mm_few_kernel<true, T, F>), grid, dim3(kThreads), 0, stream, a);           \

@@ -104,6 +104,8 @@ CASES = [
     (700, 2048, 8, [699]),
     (130, 8200, 24, [65, 130]),
     (64, 24, 8200, [10, 64]),
+    (40, 136, 8200, [9, 33]),                              # few workgroups, long sums: in parts
+    (70, 8200, 72, [70]),
     # rows enough for tiles (the smaller ones above go to the kernel for few rows)
     (600, 264, 16392, [120, 250]),                         # few tiles, a long sum: in parts
     (600, 16392, 264, [3, 290, 290]),
