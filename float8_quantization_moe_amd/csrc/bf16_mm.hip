@@ -822,10 +822,14 @@ Plan plan_of(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 // small: one expert of 512 x 512, 4096 rows 12 / 12 against 24 / 24, 8192 rows 24 / 24 against 28 /
 // 28, 16384 rows 43 / 43 against 18 / 18; 8 of 256 x 128, 16384 rows 19 / 14 against 12 / 13; 2 of
 // 1736 x 1408, 1024 rows 16 / 21 against 29 / 25; 8 of 2048 x 768, 1024 rows 18 / 15 against 24 /
-// 23, 2048 rows 28 / 25 against 19 / 27.
-bool few_rows(int product, int64_t M, int64_t N, int64_t K)
+// 23, 2048 rows 28 / 25 against 19 / 27.  dW of few results and sums that are not long: 4000 rows, 8
+// experts of 512 x 512, 15 against 27; 10 of 208 x 152, 9 against 22, 16000 rows 31 against 22; one of
+// 240 x 600, 1000 rows 8 against 13, 4000 rows 23 against 19; 16 of 1024 x 1024, 1000 rows, 56 against 20.
+bool few_rows(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 {
-    return product != MXQ_PRODUCT_DW && M > 0 &&
+    if (product == MXQ_PRODUCT_DW)
+        return M > 0 && M <= 8192 && M <= 2048 * G && G * ((N + 63) / 64) * ((K + 63) / 64) <= 512 && M * N * K <= (int64_t)1 << 30;
+    return M > 0 &&
            (M <= 256 || (M <= 1024 && M * N * K <= (int64_t)1 << 31) || (M <= 16384 && M * N * K <= (int64_t)1 << 30));
 }
 int64_t results_of(int product, int64_t M, int64_t N, int64_t K, int64_t G)
@@ -850,7 +854,7 @@ bool bf16_mm_sizes_ok(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 static int split_of(int product, int64_t M, int64_t N, int64_t K, int64_t G)
 {
     if (M == 0) return 1;
-    if (few_rows(product, M, N, K)) return bf16_mm_few_split(product == MXQ_PRODUCT_DX, (int)M, (int)N, (int)K, (int)G);
+    if (few_rows(product, M, N, K, G)) return bf16_mm_few_split(product, (int)M, (int)N, (int)K, (int)G);
     return plan_of(product, M, N, K, G).split;
 }
 
@@ -878,11 +882,11 @@ hipError_t launch_bf16_mm(int product, const void* rows, const void* other, cons
 {
     const int split = split_of(product, M, N, K, G);
     const bool joined = split > 1;
-    if (few_rows(product, M, N, K)) {
-        const hipError_t e = launch_bf16_mm_few(rows, other, product == MXQ_PRODUCT_DX, offs, M, N, K, G, split,
-                                                joined ? workspace : out, f32_out || joined, stream);
+    if (few_rows(product, M, N, K, G)) {
+        const hipError_t e = launch_bf16_mm_few(product, rows, other, offs, M, N, K, G, split, joined ? workspace : out,
+                                                f32_out || joined, accumulate && !joined, stream);
         if (e != hipSuccess || !joined) return e;
-        return join_parts(workspace, split, results_of(product, M, N, K, G), out, f32_out, false, stream);
+        return join_parts(workspace, split, results_of(product, M, N, K, G), out, f32_out, accumulate, stream);
     }
     int device = 0, cus = 0;
     hipError_t e = hipGetDevice(&device);

@@ -1,5 +1,6 @@
-// bf16_mm_few.hip -- the products Y and dX of bf16_mm.hip for few token rows.
+// bf16_mm_few.hip -- the products of bf16_mm.hip for few token rows and for small results.
 //
+// Y and dX, few rows.
 // The weights' bytes are the cost and each is used once or a few times, so nothing is shared
 // between waves: a workgroup takes 64 columns of results by 16 TB rows of one group, its four
 // waves a quarter of the sum each.  A wave has a ring of two steps of its own in LDS (64 values of
@@ -7,11 +8,16 @@
 // 128-byte lines, and waits for its own loads only.  The waves' sums are added in LDS in order:
 // one launch, no workspace.
 //
+// dW, small results.  The same with 64 x 64 results a workgroup, whose sum runs over the group's
+// rows: both operands run across it.
+//
 // Weights whose memory rows run along the sum (Y) are read 16 bytes a lane, those that run across
 // it (dX) with the transposing LDS read; MFMA operands as in bf16_mm.hip.
 #include "device_common.hpp"
 #include "internal.hpp"
 #include "mm_tile.hpp"
+
+#include "../../include/mxq.h"
 
 namespace mxq {
 
@@ -31,11 +37,12 @@ typedef __attribute__((address_space(3))) v4f* LdsV4f;
 typedef __attribute__((address_space(3))) v4s* LdsV4s;
 
 struct FewArgs {
-    const uint16_t *w, *rows;
+    const uint16_t *w, *rows;                            // W or X; X or dY
     const int32_t* offs;
     void* out;                                           // split > 1: the parts, fp32
     int M, N, K, G;
     int split;                                           // workgroups that share a sum
+    int add;                                             // dW: added to what out holds
 };
 
 // Rows of one workgroup.
@@ -71,6 +78,25 @@ __device__ __forceinline__ Chunk find_chunk(const FewArgs& a, int want, int heig
     return c;
 }
 
+// Rows [r0, r1) of group g.  By one wave.
+__device__ __forceinline__ Chunk rows_of_group(const FewArgs& a, int g)
+{
+    const int lane = lane_id();
+    Chunk c = {g, 0, 0, 0};
+    for (int base = 0; base <= g; base += 64) {
+        int e = base + lane < a.G ? a.offs[base + lane] : 0;
+        e = wave_incl_max_dpp(e > 0 ? e : 0);
+        e = e > c.rows_end ? e : c.rows_end;
+        e = e < a.M ? e : a.M;
+        if (g < base + 64) {
+            c.r0 = g > base ? readlane(e, g - base - 1) : c.rows_end;
+            c.r1 = readlane(e, g - base);
+        }
+        c.rows_end = readlane(e, 63);
+    }
+    return c;
+}
+
 // The wave's loads and all before them but the last N have landed.
 template <int N>
 __device__ __forceinline__ void wait_loads()
@@ -86,17 +112,19 @@ __device__ __forceinline__ void wait_reads()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// ACROSS: the weights' rows run across the sum (dX).  TB: 16-row parts.
-template <bool ACROSS, int TB, bool F32OUT>
+// P: an mxq_product.  TB: 16-row parts (dW: 4, of 64 columns of dY).
+template <int P, int TB, bool F32OUT>
 __global__ __launch_bounds__(kThreads)
 void bf16_mm_few_kernel(const FewArgs a)
 {
+    constexpr bool ACROSS = P != MXQ_PRODUCT_Y, DW = P == MXQ_PRODUCT_DW;   // the operands that run across the sum
     constexpr int kLoads = 8 + 2 * TB;                   // of a step
     constexpr uint32_t kStepBytes = kABytes + 2048u * TB;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * 2 * kStepBytes];
     const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
-    const Chunk c = find_chunk(a, (int)blockIdx.y, 16 * TB);
-    const int cols = ACROSS ? a.K : a.N, depth = ACROSS ? a.N : a.K;
+    const int ntiles = (a.N + 16 * TB - 1) / (16 * TB);  // (dW's)
+    const Chunk c = DW ? rows_of_group(a, (int)blockIdx.y / ntiles) : find_chunk(a, (int)blockIdx.y, 16 * TB);
+    const int cols = ACROSS ? a.K : a.N, depth = DW ? c.r1 - c.r0 : ACROSS ? a.N : a.K;
     // "Across", a memory row's 128 bytes may end inside a line, and the next ones are the next
     // workgroup's: four neighbours share an XCD (workgroup index mod 8).  16 experts of 8192 x 5120, 16
     // rows: 141 -> 127 us; 7 of 3168 x 3160: 28 -> 23; 4 of 4096 x 4096: 18.6 -> 19.4.
@@ -104,9 +132,14 @@ void bf16_mm_few_kernel(const FewArgs a)
     const int at = (int)blockIdx.x % kRound, round = (int)blockIdx.x - at;
     const int c0 = (ACROSS && round + kRound <= (int)gridDim.x ? round + at % 8 * kNear + at / 8 : (int)blockIdx.x) * kCols;
 
-    uint8_t* out = (uint8_t*)a.out + (int64_t)blockIdx.z * a.M * cols * (F32OUT ? 4 : 2);
+    // the result's rows: those of this workgroup from `first`, `rows` of them
+    const int64_t first = DW ? (int64_t)c.g * a.N + (int)blockIdx.y % ntiles * 16 * TB : c.r0;
+    const int n0 = DW ? (int)blockIdx.y % ntiles * 16 * TB : 0;
+    const int rows = !DW ? c.r1 - c.r0 : a.N - n0 < 16 * TB ? a.N - n0 : 16 * TB;
+    uint8_t* out = (uint8_t*)a.out + (int64_t)blockIdx.z * (DW ? (int64_t)a.G * a.N : a.M) * cols * (F32OUT ? 4 : 2);
+    if (DW && a.add && depth == 0) return;               // nothing to add: nothing is touched
 
-    if (blockIdx.y == 0) {                               // rows past the last end: zeros
+    if (!DW && blockIdx.y == 0) {                        // rows past the last end: zeros
         constexpr int kPer = F32OUT ? 4 : 8;             // values of 16 bytes
         const int width = (cols - c0 < kCols ? cols - c0 : kCols) / kPer;
         for (int i = (int)threadIdx.x; i < (a.M - c.rows_end) * width; i += kThreads)
@@ -118,10 +151,10 @@ void bf16_mm_few_kernel(const FewArgs a)
     const int steps = (depth + kStepK - 1) / kStepK;
     const int pieces = kWaves * a.split, piece = kWaves * (int)blockIdx.z + wave;
     const int s0 = (int)((int64_t)steps * piece / pieces), s1 = (int)((int64_t)steps * (piece + 1) / pieces);
-    const uint32_t lda = 2u * (uint32_t)a.K, ldb = 2u * (uint32_t)depth;
-    const int rows = c.r1 - c.r0, width = cols - c0 < kCols ? cols - c0 : kCols;
-    const uint16_t* wbase = a.w + ((int64_t)c.g * a.N + (ACROSS ? 0 : c0)) * a.K + (ACROSS ? c0 : 0);
-    const uint16_t* rbase = a.rows + (int64_t)c.r0 * depth;
+    const uint32_t lda = 2u * (uint32_t)a.K, ldb = 2u * (uint32_t)(DW ? a.N : depth);
+    const int width = cols - c0 < kCols ? cols - c0 : kCols;
+    const uint16_t* wbase = a.w + (DW ? (int64_t)c.r0 : (int64_t)c.g * a.N + (ACROSS ? 0 : c0)) * a.K + (ACROSS ? c0 : 0);
+    const uint16_t* rbase = a.rows + (int64_t)c.r0 * (DW ? a.N : depth) + n0;
 
     // Lane offsets.  LDS rows of 128 bytes: "along" and the tokens', their 16-byte chunks at
     // c ^ ((row >> 1) & 7); "across", their 32-byte parts at p ^ (row & 3).  Load i is rows
@@ -144,7 +177,8 @@ void bf16_mm_few_kernel(const FewArgs a)
         const int n = depth - k < kStepK ? depth - k : kStepK;
         const v4i ra = resource(ACROSS ? wbase + (int64_t)k * a.K : wbase + k,
                                 !some ? 0u : ACROSS ? (uint32_t)n * lda - 2u * (uint32_t)c0 : (uint32_t)width * lda - 2u * (uint32_t)k);
-        const v4i rb = resource(rbase + k, some ? (uint32_t)rows * ldb - 2u * (uint32_t)k : 0u);
+        const v4i rb = resource(DW ? rbase + (int64_t)k * a.N : rbase + k,
+                                !some ? 0u : DW ? (uint32_t)n * ldb - 2u * (uint32_t)n0 : (uint32_t)rows * ldb - 2u * (uint32_t)k);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t off = (8u * i + ((uint32_t)lane >> 3)) * lda;
@@ -152,8 +186,10 @@ void bf16_mm_few_kernel(const FewArgs a)
         }
 #pragma unroll
         for (int i = 0; i < 2 * TB; ++i)
-            load_to_lds<3>(rb, to + kABytes + 1024u * i,
-                           ((8u * i + ((uint32_t)lane >> 3)) * ldb + along[i & 1]) | (last ? tail[i & 1] : 0u));
+        {
+            const uint32_t off = (8u * i + ((uint32_t)lane >> 3)) * ldb;
+            load_to_lds<3>(rb, to + kABytes + 1024u * i, DW ? off + part[i & 1] : (off + along[i & 1]) | (last ? tail[i & 1] : 0u));
+        }
     };
 
     v4f acc[4][TB];
@@ -170,22 +206,21 @@ void bf16_mm_few_kernel(const FewArgs a)
         const uint32_t slot = my + (uint32_t)((s - s0) & 1) * kStepBytes;
         wait_loads<kLoads>();                            // (newer: the next step)
         v4i fa[2][4], fb[2][TB];
+        // Part i of an operand at `base`, half h of the step: "across", rows 32h + 8q + sub and four on,
+        // columns 16i + 4 (r % 4) ..
+        const auto read = [&](uint32_t base, bool across, int h, int i) {
+            if (!across) return *(LdsV4i)(uintptr_t)(base + (16u * i + r) * 128u + (((4u * h + q) ^ ((r >> 1) & 7u)) << 4));
+            const uint32_t at = base + (32u * h + 8u * q + sub) * 128u + (((uint32_t)i ^ sub) << 5) + 8u * (r & 3u);
+            const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)at));
+            const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)(at + 512u)));
+            return v4i{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+        };
 #pragma unroll
         for (int h = 0; h < 2; ++h) {                    // 32 values of the sum
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (ACROSS) {                  // rows 32h + 8q + sub and four on, columns 16i + 4 (r % 4) ..
-                    const uint32_t at = slot + (32u * h + 8u * q + sub) * 128u + (((uint32_t)i ^ sub) << 5) + 8u * (r & 3u);
-                    const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)at));
-                    const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsV4s)(uintptr_t)(at + 512u)));
-                    fa[h][i] = v4i{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
-                } else {
-                    fa[h][i] = *(LdsV4i)(uintptr_t)(slot + (16u * i + r) * 128u + (((4u * h + q) ^ ((r >> 1) & 7u)) << 4));
-                }
-            }
+            for (int i = 0; i < 4; ++i) fa[h][i] = read(slot, ACROSS, h, i);
 #pragma unroll
-            for (int j = 0; j < TB; ++j)
-                fb[h][j] = *(LdsV4i)(uintptr_t)(slot + kABytes + (16u * j + r) * 128u + (((4u * h + q) ^ ((r >> 1) & 7u)) << 4));
+            for (int j = 0; j < TB; ++j) fb[h][j] = read(slot + kABytes, DW, h, j);
         }
         wait_reads();
         issue(s + 2);
@@ -214,10 +249,13 @@ void bf16_mm_few_kernel(const FewArgs a)
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
             sum += *(LdsV4f)(uintptr_t)(base + (uint32_t)w * 2u * kStepBytes + (uint32_t)(wave * TB + j) * 1024u + 16u * (uint32_t)lane);
-        const int row = c.r0 + 16 * j + (int)r;
-        if (row < c.r1 && col < cols) {
-            const int64_t at = (int64_t)row * cols + col;
-            if constexpr (F32OUT) *(v4f*)((float*)out + at) = sum;
+        const int row = 16 * j + (int)r;
+        if (row < rows && col < cols) {
+            const int64_t at = (first + row) * cols + col;
+            if constexpr (F32OUT) {
+                if (DW && a.add) sum = *(const v4f*)((float*)out + at) + sum;
+                *(v4f*)((float*)out + at) = sum;
+            }
             else *(uint2*)((uint16_t*)out + at) = make_uint2(f32_pair_to_bf16(sum[0], sum[1]), f32_pair_to_bf16(sum[2], sum[3]));
         }
     }
@@ -226,49 +264,54 @@ void bf16_mm_few_kernel(const FewArgs a)
 }  // namespace
 
 // 16-row parts of a workgroup.
-static int few_parts(int M, int G)
+static int few_parts(int product, int M, int G)
 {
     const int groups = G < M ? G : M;
-    return M <= 16 ? 1 : M <= 32 * groups ? 2 : 4;
+    return product == MXQ_PRODUCT_DW ? 4 : M <= 16 ? 1 : M <= 32 * groups ? 2 : 4;
 }
-static dim3 few_grid(bool across, int M, int N, int K, int G)
+static int64_t few_groups(int product, int64_t M, int64_t N, int64_t K, int64_t G, dim3* grid)
 {
-    const int cols = across ? K : N, height = 16 * few_parts(M, G);
-    return dim3((unsigned)((cols + kCols - 1) / kCols), (unsigned)((M + height - 1) / height + (G < M ? G : M) - 1));
+    const int64_t height = 16 * few_parts(product, (int)M, (int)G);
+    const int64_t x = ((product == MXQ_PRODUCT_Y ? N : K) + kCols - 1) / kCols;
+    const int64_t y = product == MXQ_PRODUCT_DW ? G * ((N + height - 1) / height) : (M + height - 1) / height + (G < M ? G : M) - 1;
+    *grid = dim3((unsigned)x, (unsigned)y);
+    return x * y;
 }
 
 // Workgroups that share a sum, and then a second launch that adds the parts: where there are few and
 // their waves' sums are long (142 rows x 6416 x 552, dX 33 -> 15 us; one row 13 -> 9; 142 rows x 512 x
 // 4096 over 8 experts, Y, sums of 64 steps, 12 -> 15).
-int bf16_mm_few_split(bool across, int M, int N, int K, int G)
+int bf16_mm_few_split(int product, int M, int N, int K, int G)
 {
-    const dim3 grid = few_grid(across, M, N, K, G);
-    const int64_t groups = (int64_t)grid.x * grid.y;
-    const int steps = ((across ? N : K) + kStepK - 1) / kStepK;
+    dim3 grid;
+    const int64_t groups = few_groups(product, M, N, K, G, &grid);
+    const int sum = product == MXQ_PRODUCT_DW ? M / G : product == MXQ_PRODUCT_DX ? N : K, steps = (sum + kStepK - 1) / kStepK;
     if (groups > 128 || steps < 20 * kWaves) return 1;
     int64_t split = 512 / groups;
     if (split > steps / (3 * kWaves)) split = steps / (3 * kWaves);
     return (int)(split < 16 ? split : 16);
 }
 
-hipError_t launch_bf16_mm_few(const void* rows, const void* w, bool across, const int32_t* offs, int M, int N, int K, int G,
-                              int split, void* out, bool f32_out, hipStream_t stream)
+hipError_t launch_bf16_mm_few(int product, const void* rows, const void* w, const int32_t* offs, int M, int N, int K, int G,
+                              int split, void* out, bool f32_out, bool add, hipStream_t stream)
 {
-    const FewArgs a = {(const uint16_t*)w, (const uint16_t*)rows, offs, out, M, N, K, G, split};
-    const int parts = few_parts(M, G);
-    dim3 grid = few_grid(across, M, N, K, G);
+    const FewArgs a = {(const uint16_t*)w, (const uint16_t*)rows, offs, out, M, N, K, G, split, add};
+    const int parts = few_parts(product, M, G);
+    dim3 grid;
+    few_groups(product, M, N, K, G, &grid);
     grid.z = (unsigned)split;
-#define MXQ_LAUNCH(T, F)                                                                                                \
-    do {                                                                                                                \
-        if (across) hipLaunchKernelGGL((bf16_mm_few_kernel<true, T, F>), grid, dim3(kThreads), 0, stream, a);           \
-        else hipLaunchKernelGGL((bf16_mm_few_kernel<false, T, F>), grid, dim3(kThreads), 0, stream, a);                 \
+#define MXQ_LAUNCH(P, T)                                                                                               \
+    do {                                                                                                               \
+        if (f32_out) hipLaunchKernelGGL((bf16_mm_few_kernel<P, T, true>), grid, dim3(kThreads), 0, stream, a);         \
+        else hipLaunchKernelGGL((bf16_mm_few_kernel<P, T, false>), grid, dim3(kThreads), 0, stream, a);                \
     } while (0)
-    if (parts == 1 && f32_out) MXQ_LAUNCH(1, true);
-    else if (parts == 1) MXQ_LAUNCH(1, false);
-    else if (parts == 2 && f32_out) MXQ_LAUNCH(2, true);
-    else if (parts == 2) MXQ_LAUNCH(2, false);
-    else if (f32_out) MXQ_LAUNCH(4, true);
-    else MXQ_LAUNCH(4, false);
+    if (product == MXQ_PRODUCT_DW) MXQ_LAUNCH(MXQ_PRODUCT_DW, 4);
+    else if (product == MXQ_PRODUCT_DX && parts == 1) MXQ_LAUNCH(MXQ_PRODUCT_DX, 1);
+    else if (product == MXQ_PRODUCT_DX && parts == 2) MXQ_LAUNCH(MXQ_PRODUCT_DX, 2);
+    else if (product == MXQ_PRODUCT_DX) MXQ_LAUNCH(MXQ_PRODUCT_DX, 4);
+    else if (parts == 1) MXQ_LAUNCH(MXQ_PRODUCT_Y, 1);
+    else if (parts == 2) MXQ_LAUNCH(MXQ_PRODUCT_Y, 2);
+    else MXQ_LAUNCH(MXQ_PRODUCT_Y, 4);
 #undef MXQ_LAUNCH
     return hipGetLastError();
 }

@@ -100,10 +100,10 @@ size_t bf16_mm_workspace_bytes(int product, int64_t M, int64_t N, int64_t K, int
 hipError_t launch_bf16_mm(int product, const void* rows, const void* other, const int32_t* offs, int M, int N, int K, int G,
                           void* out, bool f32_out, bool accumulate, void* workspace, hipStream_t stream);
 
-// Their part for few rows: Y, or dX (across).  With a split above 1 out takes that many fp32 arrays of results, to be added.
-int bf16_mm_few_split(bool across, int M, int N, int K, int G);
-hipError_t launch_bf16_mm_few(const void* rows, const void* w, bool across, const int32_t* offs, int M, int N, int K, int G,
-                              int split, void* out, bool f32_out, hipStream_t stream);
+// Their part for few rows and small results.  With a split above 1 out takes that many fp32 arrays of results, to be added.
+int bf16_mm_few_split(int product, int M, int N, int K, int G);
+hipError_t launch_bf16_mm_few(int product, const void* rows, const void* other, const int32_t* offs, int M, int N, int K, int G,
+                              int split, void* out, bool f32_out, bool add, hipStream_t stream);
 
 // Routing.
 int route_max_experts();

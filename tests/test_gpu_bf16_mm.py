@@ -106,6 +106,8 @@ CASES = [
     (64, 24, 8200, [10, 64]),
     (40, 136, 8200, [9, 33]),                              # few workgroups, long sums: in parts
     (70, 8200, 72, [70]),
+    (7000, 72, 200, [700 * i for i in range(1, 8)] + [5000, 7000]),   # dW: few results
+    (1500, 200, 328, [0, 1400, 1400, 1490]),
     # rows enough for tiles (the smaller ones above go to the kernel for few rows)
     (600, 264, 16392, [120, 250]),                         # few tiles, a long sum: in parts
     (600, 16392, 264, [3, 290, 290]),
@@ -144,7 +146,8 @@ def test_real_values(M, N, K, ends, product):
         assert torch.equal(got, run(product, t, ends, out, M))         # the same bits again
 
 
-@pytest.mark.parametrize("M,N,K,ends", [(300, 264, 200, [100, 100, 250]), (4100, 32, 48, [4000]), (5, 512, 520, [5])])
+@pytest.mark.parametrize("M,N,K,ends", [(300, 264, 200, [100, 100, 250]), (4100, 32, 48, [4000]), (5, 512, 520, [5]), (900, 1032, 1160, [300, 300, 890]),
+                                         (20000, 264, 264, [20000])])
 def test_gradient_added_to_what_is_there(M, N, K, ends):
     t = operands(M, N, K, len(ends), 3)
     want, _ = want_of("dw", t, ends, M)
