@@ -18,18 +18,26 @@
 //
 // Both are HBM bound: the row is read once and held in registers between its reductions and
 // its use, LANES threads a row with C chunks of 8 values each.  Sums go in a fixed order.
-// 65536 x 5120 bf16 with every output: 515 us, 5.9 TB/s; backward of 16640 x 5120 with dh: 120 us,
+// 65536 x 5120 bf16 with every output: 528 us, 5.7 TB/s; backward of 16640 x 5120 with dh: 120 us,
 // 5.7 TB/s.  The backward pass is near its VALU's bound too: with the differences and dy * w
 // made again after the sums it took 136 us, with the next row's loads ahead of that 142.
 #include "device_common.hpp"
 #include "internal.hpp"
 #include "mx_block.hpp"
 
+#include <type_traits>
+
 namespace mxq {
 
 namespace {
 
 constexpr int kWaves = 8;                                 // of a workgroup, at most
+// y is rounded to bf16 (itself or for its codes) from fp32 arithmetic that is good to two units of
+// 2^-24 or so; where the fp32 value is within this many of the middle between two bf16, the chunk is
+// computed again in doubles.  Of 3.4e8 values 1300 then differ from the exact ones' roundings and of
+// 10^7 blocks' scales none; 3800 and one or two without it; 13000 and one in steps of fp32 throughout
+// (65536 x 5120: 528 us; 515 with sums in fp32, 593 all in doubles).
+constexpr uint32_t kNear = 4;
 
 // Sums of two values over the LANES threads of a row, in all of them: a wave alone, else
 // through LDS (alternated by `turn`, so that one barrier is enough).
@@ -52,33 +60,73 @@ __device__ __forceinline__ float2 row_sums(float a, float b, float2 (*sh)[kWaves
     return make_float2(a, b);
 }
 
+// Over the wave, by moves of the halves as lanes_sum.
+__device__ __forceinline__ double wave_sum(double v)
+{
+    const auto moved = [](double x, auto ctrl) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const uint64_t lo = dpp_move<decltype(ctrl)::value>((uint32_t)b), hi = dpp_move<decltype(ctrl)::value>((uint32_t)(b >> 32));
+        return __builtin_bit_cast(double, hi << 32 | lo);
+    };
+    const auto lane = [](double x, int l) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);
+        const uint64_t lo = (uint32_t)readlane((int)(uint32_t)b, l), hi = (uint32_t)readlane((int)(uint32_t)(b >> 32), l);
+        return __builtin_bit_cast(double, hi << 32 | lo);
+    };
+    v += moved(v, std::integral_constant<int, kDppXor1>{});
+    v += moved(v, std::integral_constant<int, kDppXor2>{});
+    v += moved(v, std::integral_constant<int, kDppHalfMirror>{});
+    v += moved(v, std::integral_constant<int, kDppMirror>{});
+    return (lane(v, 0) + lane(v, 16)) + (lane(v, 32) + lane(v, 48));
+}
+// Sums of two doubles over the LANES threads of a row, in all of them.
+template <int LANES>
+__device__ __forceinline__ double2 row_sums(double a, double b, double2 (&sh)[kWaves])
+{
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (LANES > 64) {
+        constexpr int W = LANES / 64;
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = make_double2(a, b);
+        __syncthreads();
+        a = b = 0.0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            a += sh[w].x;
+            b += sh[w].y;
+        }
+    }
+    return make_double2(a, b);
+}
+
 __device__ __forceinline__ float sum8(const float (&v)[8])
 {
     return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
 template <class T, int LANES, int C, bool NT>
-__global__ __launch_bounds__(LANES < 256 ? 256 : LANES)
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES, T::kBytes * C <= (NT ? 6 : 4) ? 3 : 2)
 void add_layernorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __restrict__ w, const uint8_t* __restrict__ b,
                           int64_t M, int K, float eps, uint8_t* h, uint8_t* y, uint8_t* __restrict__ q,
                           uint8_t* __restrict__ s, float* __restrict__ mean, float* __restrict__ rstd)
 {
     constexpr int kRows = LANES < 256 ? 256 / LANES : 1;      // rows of a workgroup
     __shared__ float2 sh[2][kWaves];
+    __shared__ double2 shd[kWaves];
     const int lane = (int)threadIdx.x % LANES;
     const int K8 = K / 8;
     const int64_t row_bytes = (int64_t)K * T::kBytes;
+    constexpr bool kHold = LANES < 512;                   // (w and b anew from the cache where registers are short)
     typename T::Raw wr[C], br[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = lane + c * LANES;
         br[c] = {};
-        if (i < K8) {
+        if (kHold && i < K8) {
             wr[c] = T::load8(w, i);
             if (b) br[c] = T::load8(b, i);
         }
     }
-    const float inv_k = 1.0f / (float)K;
     for (int64_t m = (int64_t)blockIdx.x * kRows + (int)threadIdx.x / LANES; m < M; m += (int64_t)gridDim.x * kRows) {
         const int64_t at = m * row_bytes;
         typename T::Raw xr[C], rr[C];
@@ -113,7 +161,7 @@ void add_layernorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __r
         // (cut to 16 bits, so that the differences of bf16 values from it are exact: their roundings
         // are alike over a row, and the mean lacked half a unit of them)
         const float m0 = __uint_as_float(__float_as_uint(row_sums<LANES>(sum8(t), 0.0f, sh, 0).x / (float)K) & 0xFFFFFF00u);
-        float d1[8] = {}, d2[8] = {};
+        double d1 = 0.0, d2 = 0.0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = lane + c * LANES;
@@ -122,36 +170,45 @@ void add_layernorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __r
                 T::unpack(xr[c], a);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float d = a[e] - m0;
-                    d1[e] += d;
-                    d2[e] += d * d;
+                    const double d = a[e] - m0;
+                    d1 += d;
+                    d2 = fma(d, d, d2);
                 }
             }
         }
-        const float2 sums = row_sums<LANES>(sum8(d1), sum8(d2), sh, 1);
-        const float left = sums.x * inv_k;                // what the mean lacks
-        const double var = (double)sums.y / K - (double)left * left;
-        const float rs = (float)(1.0 / sqrt((var < 0.0 ? 0.0 : var) + (double)eps));
-        const float mu = m0 + left;
+        const double2 sums = row_sums<LANES>(d1, d2, shd);
+        const double left = sums.x / K;                   // what the mean lacks
+        const double var = sums.y / K - left * left;
+        const double rstd64 = 1.0 / sqrt((var < 0.0 ? 0.0 : var) + (double)eps), mean64 = (double)m0 + left;
+        const float rs = (float)rstd64, l0 = (float)left;
         if (lane == 0) {
-            if (mean) mean[m] = mu;
+            if (mean) mean[m] = (float)mean64;
             if (rstd) rstd[m] = rs;
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = lane + c * LANES;
             if (i < K8) {
-                float a[8], f[8], g[8];
+                float a[8], f[8], g[8], o[8];
                 T::unpack(xr[c], a);
-                T::unpack(wr[c], f);
-                T::unpack(br[c], g);
+                T::unpack(kHold ? wr[c] : T::load8(w, i), f);
+                T::unpack(kHold || !b ? br[c] : T::load8(b, i), g);
+                uint32_t least = ~0u;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] = fmaf((a[e] - m0 - left) * rs, f[e], g[e]);
-                const typename T::Raw o = T::pack(a);
-                if (y) T::store8(y + at, i, o);
+                for (int e = 0; e < 8; ++e) {
+                    o[e] = fmaf((a[e] - m0 - l0) * rs, f[e], g[e]);
+                    const uint32_t from = (__float_as_uint(o[e]) - (0x8000u - kNear)) << 16;
+                    least = from < least ? from : least;
+                }
+                if (least <= (2u * kNear) << 16) {        // near the middle of two bf16: again in doubles
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = (float)fma(((double)a[e] - mean64) * rstd64, (double)f[e], (double)g[e]);
+                }
+                const typename T::Raw p = T::pack(o);
+                if (y) T::store8(y + at, i, p);
                 if (q) {                                  // whole quads are in or out (K % 32 == 0)
                     uint32_t code;
-                    const uint2 e8 = quantize_chunk<false>(T::bf16_bits(o), &code);
+                    const uint2 e8 = quantize_chunk<false>(T::bf16_bits(p), &code);
                     store_nt(e8, (uint2*)(q + m * K) + i);
                     if ((lane & 3) == 0) s[m * (K / 32) + (i >> 2)] = (uint8_t)code;
                 }
@@ -340,7 +397,7 @@ void columns_kernel(const float* __restrict__ part, int rows, int K, float* __re
 
 constexpr int kMaxGrid = 1 << 22;
 // Inputs that do not fit the 256 MB last-level cache are read as streams (65536 x 5120 with a
-// residual 539 -> 515 us; backward 16640 x 5120 with dh 137 -> 135); smaller ones may be there.
+// residual 4 % less; backward 16640 x 5120 with dh 137 -> 135); smaller ones may be there.
 constexpr int64_t kCacheBytes = (int64_t)256 << 20;
 // Workgroups of the backward pass at most, and so parts: two a CU, which are resident together
 // (16640 x 5120: 512 / 768 119 / 141 us).
