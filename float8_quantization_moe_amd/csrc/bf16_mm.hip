@@ -500,6 +500,7 @@ struct Places {
             }
         }
     }
+    // (The ring is the kernel's only LDS and so starts at 0: a slot's address is a bit.)
     __device__ __forceinline__ void other_slot()
     {
 #pragma unroll

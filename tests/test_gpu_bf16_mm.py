@@ -116,6 +116,9 @@ CASES = [
     (5000, 520, 456, [1300, 1300, 2600, 2601, 4990]),
     (20000, 264, 264, [300 * i for i in range(1, 66)]),    # 65 groups, their last tiles of 44 rows
     (300, 2696, 2696, [0, 300]),
+    (1100, 1032, 1288, [0, 0, -5]),                        # no group has rows, nor is the matrix small
+    (20000, 264, 264, [5 * i for i in range(4094)] + [19999]),        # 4095 groups of 5 rows, -1 empty
+    (66000, 8192, 72, [1000 * i for i in range(1, 65)] + [66000]),    # two workgroups' lists a CU
 ]
 
 
@@ -162,7 +165,7 @@ def test_gradient_added_to_what_is_there(M, N, K, ends):
     assert torch.equal(dw, before)
 
 
-@pytest.mark.parametrize("M,N,K,ends", [(200, 264, 200, [64, 130, 130, 190]), (40, 72, 136, [17, 39])])
+@pytest.mark.parametrize("M,N,K,ends", [(200, 264, 200, [64, 130, 130, 190]), (40, 72, 136, [17, 39]), (1100, 1032, 1288, [300, 600, 1090])])
 def test_nan_and_infinity_reach_their_own_sums_only(M, N, K, ends):
     base = operands(M, N, K, len(ends), 1)
     e = torch.tensor(ends, dtype=torch.int32, device="cuda")
