@@ -9,8 +9,10 @@
 //
 // Persistent workgroups (one a CU, 4 waves in 2 x 2 of 128 x 128 results) walk over tiles.  The
 // sum advances 64 values a slot through a 2-slot LDS ring of 32 KB of each operand, filled by
-// buffer-load-to-LDS in whole 128-byte lines.  A slot is four MFMA steps of 16; a step's
-// operands are read from LDS during the step before it.  An "along" operand is 256 rows of 128
+// buffer-load-to-LDS in whole 128-byte lines.  A slot is two MFMA steps of 32 (16 x 16
+// results an instruction; 32 x 32 by 16 has half the LDS reads' addresses but leaves a lower clock:
+// 1277 / 1276 / 1451 us for Y / dX / dW below, against 1199 / 1221 / 1438); a step's operands are
+// read from LDS during the step before it.  An "along" operand is 256 rows of 128
 // bytes in LDS, read 16 bytes a lane; an "across" one 64 rows of 512 bytes, read with the
 // transposing LDS read, which gives a lane four consecutive values of its own column.  With one
 // wave a SIMD nothing issues while a load or an LDS read waits for its pipe, so both are spread
@@ -22,6 +24,12 @@
 // Every workgroup finds its own tiles from the group offsets (a scan in LDS), so no launch comes
 // before.  Where there are fewer tiles than CUs, the sum is split: the parts go to the workspace
 // in fp32 and a second launch adds them in order.
+//
+// 16640 x 8192 x 5120 over 16 ragged groups (1.4 TFLOP): Y 1196 us, dX 1230, dW in fp32 1395; one group
+// of 16384 rows 993, 1003, 1044 (1.39, 1.37, 1.32 PFLOP/s; nothing but these MFMAs on random values
+// runs at 1.94).  Bound by the MFMAs at the clock their power leaves and by the loads' path from L2 (a copy
+// without loads 821 / 749 / 846 us); dW also by its stores, whose time adds to the products' (2.7 GB:
+// 480 us with next to nothing to sum).
 #include "device_common.hpp"
 #include "internal.hpp"
 #include "mm_tile.hpp"
@@ -48,6 +56,10 @@ constexpr int kMaxGroups = 4095;
 constexpr int kMaxSplit = 16;
 constexpr int kListBytes = (3 * (kMaxGroups + 1) + kThreads) * 4 + kMaxEntries * 64;
 static_assert(kListBytes <= (int)kLdsBytes, "the list's arrays fit the ring");
+// What a tile of 129 to 256 rows, of 65 to 128 and of up to 64 costs next to the others in a full round,
+// where the columns' operand is most of it: a round of 256-, 128- and 64-row tiles after others at
+// K = 5120 was measured as 1, 0.72 and 0.6 in the sum of a call (0.82, 0.8 and 0.73 alone); lists dealt by
+// 16 / 10 / 9 took Y / dX of 16 groups of 1040 rows from 1357 / 1324 us to 1309 / 1293.
 constexpr int kCostWhole = 16, kCostHalf = 10, kCostQuarter = 9;
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -620,8 +632,7 @@ __device__ __forceinline__ void pin(v4f (&acc)[8][TB])
 // a lane, 64 of a row.  bf16: two parts side by side change lanes, so that those of even q have
 // eight columns of the first and those of odd q of the second: 16 bytes a lane, 64 of a row.
 // Through a buffer resource that ends with the tile's last row; a lane past the last column
-// leaves it too.  (Nothing else stands between the stores: with 64-bit addresses and branches
-// around each, 16640 x 8192 x 5120 over 16 groups, dW in fp32, took 1364 us.)
+// leaves it too, so that no branch stands between the stores.
 template <int P, int TB, bool F32OUT, bool ADD>
 __device__ __forceinline__ void store_tile(v4f (&acc)[8][TB], const MmArgs& a, const Tile& t, const Lane<P>& l)
 {

@@ -1,7 +1,6 @@
 // bf16_mm_few.hip -- the products of bf16_mm.hip for few token rows and for small results.
 //
-// Y and dX, few rows.
-// The weights' bytes are the cost and each is used once or a few times, so nothing is shared
+// Y and dX, few rows.  The weights' bytes are the cost and each is used once or a few times, so nothing is shared
 // between waves: a workgroup takes 64 columns of results by 16 TB rows of one group, its four
 // waves a quarter of the sum each.  A wave has a ring of two steps of its own in LDS (64 values of
 // the sum: 8 KB of weights, 2 KB a 16 rows of tokens), filled by buffer-load-to-LDS in whole
@@ -13,6 +12,9 @@
 //
 // Weights whose memory rows run along the sum (Y) are read 16 bytes a lane, those that run across
 // it (dX) with the transposing LDS read; MFMA operands as in bf16_mm.hip.
+//
+// 8 rows over 16 experts of 8192 x 5120, six of them with rows: 84 us for 503 MB, 6.0 TB/s (a ring
+// shared by the four waves and its barriers 99).  Against the tile kernel: few_rows() in bf16_mm.hip.
 #include "device_common.hpp"
 #include "internal.hpp"
 #include "mm_tile.hpp"

@@ -8,7 +8,9 @@
 //
 // All walk over tokens, not rows: a token's own row (x, out, dout) is then read or written
 // once, its topk rows once each, which is every byte once.  Sums are fp32, over j in order,
-// and over k in an order fixed by K.  HBM bound.
+// and over k in an order fixed by K.  HBM bound: 8192 tokens x 8 rows x 5120, combine 126 us (6.0 TB/s),
+// its gradients 264 us (5.4 TB/s); dispatch of 16640 tokens x 2 rows x 5120 93 us (5.5 TB/s), 5 + 5 us of
+// it the two launches that find the rows.
 #include "device_common.hpp"
 #include "internal.hpp"
 

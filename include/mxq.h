@@ -648,10 +648,10 @@ mxq_status mxq_bf16_grouped_mm_dw(const void* dy, const void* x, const int32_t* 
  *   mean     (M) fp32 output, the row mean of h; or NULL.
  *   rstd     (M) fp32 output 1 / sqrt(mean((h - mean)^2) + eps); or NULL.
  *   y        (M, K) output (h - mean) * rstd * weight + bias, rounded once; or NULL (with q).
- * Everything else as mxq_add_rmsnorm, errors included.  The mean is taken first and
- * the squares are those of the differences from it, in fp32.  A NaN or an infinity in h
- * makes its whole row NaN (scales 0xFF), as do values whose sum, or squares whose sum,
- * pass the largest fp32 value; with eps = 0 a row of equal values comes out as NaN.
+ * Everything else as mxq_add_rmsnorm, errors included.  A first mean is taken in
+ * fp32; the differences from it, their squares and both sums are in doubles.  A NaN or an
+ * infinity in h makes its whole row NaN (scales 0xFF), as do values whose sum passes the
+ * largest fp32 value; with eps = 0 the y of a row of equal values is unspecified.
  */
 mxq_status mxq_add_layernorm(const void* x, const void* residual, const void* weight, const void* bias, int dtype,
                              int64_t M, int64_t K, float eps, void* h, void* y, void* q_e4m3, void* s_e8m0,
