@@ -256,57 +256,61 @@ void add_layernorm_bwd_kernel(const uint8_t* __restrict__ h, const uint8_t* __re
             }
         }
         const float mu = mean[m], rs = rstd[m];
-        // d = h - m and u = g = dy * w; held in fp32 between the passes where registers allow it
+        // n = (h - m) * rstd and u = dy * w; held in fp32 between the passes where registers allow it
         constexpr bool kHold = C <= 3;
-        float hd[kHold ? C : 1][8], hu[kHold ? C : 1][8];
-        const auto differences = [&](int c, int i, float (&d)[8], float (&u)[8], float (&g)[8]) {
+        float hn[kHold ? C : 1][8], hu[kHold ? C : 1][8];
+        // n is left as h - m, whose product with rstd comes where it is used (with it here one variant spills)
+        const auto differences = [&](int c, int i, float (&n)[8], float (&u)[8], float (&g)[8]) {
             float f[8];
-            T::unpack(hr[c], d);
+            T::unpack(hr[c], n);
             T::unpack(gr[c], g);
             T::unpack(kHoldW ? wr[c] : T::load8(w, i), f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                d[e] -= mu;
+                n[e] -= mu;
                 u[e] = g[e] * f[e];
             }
         };
-        float s1 = 0.0f, s2 = 0.0f;                       // sums of u and of u * n, n = d * rstd
+        float s1 = 0.0f, s2 = 0.0f;                       // sums of u and of u * n
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = lane + c * LANES;
             if (i < K8) {
-                float d[8], u[8], g[8];
-                differences(c, i, d, u, g);
+                float n[8], u[8], g[8];
+                differences(c, i, n, u, g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float n = d[e] * rs;
+                    n[e] *= rs;
                     s1 += u[e];
-                    s2 = fmaf(u[e], n, s2);
-                    aw[c][e] = fmaf(g[e], n, aw[c][e]);
+                    s2 = fmaf(u[e], n[e], s2);
+                    aw[c][e] = fmaf(g[e], n[e], aw[c][e]);
                     ab[c][e] += g[e];
                     if constexpr (kHold) {
-                        hd[c][e] = d[e];
+                        hn[c][e] = n[e];
                         hu[c][e] = u[e];
                     }
                 }
             }
         }
         const float2 sums = row_sums<LANES>(s1, s2, sh, turn);
-        // dx = rstd u - rstd mean(u) - d rstd^2 mean(u n)
-        const float k1 = -rs * (sums.x / (float)K), k2 = -(rs * rs) * (sums.y / (float)K);
+        // dx = rstd u - rstd mean(u) - n rstd mean(u n); not with (h - m) and rstd^2, which leaves
+        // fp32's range at spreads of 1e19 and 1e-19 already
+        const float k1 = -rs * (sums.x / (float)K), k2 = -rs * (sums.y / (float)K);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int i = lane + c * LANES;
             if (i < K8) {
-                float d[8], u[8], g[8], o[8];
-                if constexpr (!kHold) differences(c, i, d, u, g);
+                float n[8], u[8], g[8], o[8];
+                if constexpr (!kHold) differences(c, i, n, u, g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     if constexpr (kHold) {
-                        d[e] = hd[c][e];
+                        n[e] = hn[c][e];
                         u[e] = hu[c][e];
+                    } else {
+                        n[e] *= rs;
                     }
-                    o[e] = fmaf(d[e], k2, fmaf(u[e], rs, k1));
+                    o[e] = fmaf(n[e], k2, fmaf(u[e], rs, k1));
                 }
                 if (dh) {
                     float r[8];
