@@ -896,9 +896,9 @@ hipError_t launch_bf16_mm(int product, const void* rows, const void* other, cons
     const bool joined = split > 1;
     if (few_rows(product, M, N, K, G)) {
         const hipError_t e = launch_bf16_mm_few(product, rows, other, offs, M, N, K, G, split, joined ? workspace : out,
-                                                f32_out || joined, accumulate && !joined, stream);
+                                                f32_out || joined, accumulate, stream);
         if (e != hipSuccess || !joined) return e;
-        return join_parts(workspace, split, results_of(product, M, N, K, G), out, f32_out, accumulate, stream);
+        return join_parts(workspace, split, results_of(product, M, N, K, G), out, f32_out, false, stream);   // (not dW)
     }
     int device = 0, cus = 0;
     hipError_t e = hipGetDevice(&device);

@@ -43,7 +43,7 @@ struct FewArgs {
     const int32_t* offs;
     void* out;                                           // split > 1: the parts, fp32
     int M, N, K, G;
-    int split;                                           // workgroups that share a sum
+    int split;                                           // workgroups that share a sum (dW: 1)
     int add;                                             // dW: added to what out holds
 };
 
@@ -138,7 +138,7 @@ void bf16_mm_few_kernel(const FewArgs a)
     const int64_t first = DW ? (int64_t)c.g * a.N + (int)blockIdx.y % ntiles * 16 * TB : c.r0;
     const int n0 = DW ? (int)blockIdx.y % ntiles * 16 * TB : 0;
     const int rows = !DW ? c.r1 - c.r0 : a.N - n0 < 16 * TB ? a.N - n0 : 16 * TB;
-    uint8_t* out = (uint8_t*)a.out + (int64_t)blockIdx.z * (DW ? (int64_t)a.G * a.N : a.M) * cols * (F32OUT ? 4 : 2);
+    uint8_t* out = (uint8_t*)a.out + (DW ? 0 : (int64_t)blockIdx.z * a.M * cols * (F32OUT ? 4 : 2));
     if (DW && a.add && depth == 0) return;               // nothing to add: nothing is touched
 
     if (!DW && blockIdx.y == 0) {                        // rows past the last end: zeros
@@ -151,7 +151,7 @@ void bf16_mm_few_kernel(const FewArgs a)
 
     // this wave's steps of the sum, and the resources at the first
     const int steps = (depth + kStepK - 1) / kStepK;
-    const int pieces = kWaves * a.split, piece = kWaves * (int)blockIdx.z + wave;
+    const int pieces = DW ? kWaves : kWaves * a.split, piece = DW ? wave : kWaves * (int)blockIdx.z + wave;
     const int s0 = (int)((int64_t)steps * piece / pieces), s1 = (int)((int64_t)steps * (piece + 1) / pieces);
     const uint32_t lda = 2u * (uint32_t)a.K, ldb = 2u * (uint32_t)(DW ? a.N : depth);
     const int width = cols - c0 < kCols ? cols - c0 : kCols;
@@ -282,12 +282,14 @@ static int64_t few_groups(int product, int64_t M, int64_t N, int64_t K, int64_t 
 
 // Workgroups that share a sum, and then a second launch that adds the parts: where there are few and
 // their waves' sums are long (142 rows x 6416 x 552, dX 33 -> 15 us; one row 13 -> 9; 142 rows x 512 x
-// 4096 over 8 experts, Y, sums of 64 steps, 12 -> 15).
+// 4096 over 8 experts, Y, sums of 64 steps, 12 -> 15).  dW's sums are not long here: 2048 rows a group
+// on average, see few_rows().
 int bf16_mm_few_split(int product, int M, int N, int K, int G)
 {
+    if (product == MXQ_PRODUCT_DW) return 1;
     dim3 grid;
     const int64_t groups = few_groups(product, M, N, K, G, &grid);
-    const int sum = product == MXQ_PRODUCT_DW ? M / G : product == MXQ_PRODUCT_DX ? N : K, steps = (sum + kStepK - 1) / kStepK;
+    const int steps = ((product == MXQ_PRODUCT_DX ? N : K) + kStepK - 1) / kStepK;
     if (groups > 128 || steps < 20 * kWaves) return 1;
     int64_t split = 512 / groups;
     if (split > steps / (3 * kWaves)) split = steps / (3 * kWaves);
