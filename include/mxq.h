@@ -61,9 +61,9 @@ typedef enum mxq_status {
     MXQ_ERR_HIP = 6,         /* a HIP runtime call failed (launch, device query)    */
     MXQ_ERR_NOT_IMPLEMENTED = 7,
     MXQ_ERR_DTYPE = 8,       /* unknown mxq_out_dtype or mxq_format value           */
-    MXQ_ERR_RULE = 9         /* unknown mxq_scale_rule, mxq_score or mxq_product
-                                value, unknown flag, or an eps that is negative or
-                                NaN                                                 */
+    MXQ_ERR_RULE = 9         /* unknown mxq_scale_rule or mxq_score value, unknown
+                                flag, an accumulate that is neither 0 nor 1, or an
+                                eps that is negative or NaN                         */
 } mxq_status;
 
 typedef enum mxq_layout {
@@ -616,7 +616,8 @@ mxq_status mxq_mxfp4_grouped_mm_packed(const void* packed, const void* wq_e2m1, 
  *           added to what dw holds, in fp32 (a group without rows keeps its own); needs
  *           MXQ_OUT_F32 (MXQ_ERR_DTYPE otherwise), any other value: MXQ_ERR_RULE.
  *   workspace   DEVICE scratch of mxq_bf16_grouped_mm_workspace_bytes(product, M, N,
- *           K, G) bytes, for either out_dtype; where that is 0 it may be NULL.  It
+ *           K, G) bytes, for either out_dtype; where that is 0 it may be NULL (sizes
+ *           that the call refuses, and values that are no mxq_product, give 0).  It
  *           holds parts of sums that are split over several workgroups; it needs no
  *           initialisation, and two calls in flight must not share it.
  *
@@ -648,10 +649,11 @@ mxq_status mxq_bf16_grouped_mm_dw(const void* dy, const void* x, const int32_t* 
  *   mean     (M) fp32 output, the row mean of h; or NULL.
  *   rstd     (M) fp32 output 1 / sqrt(mean((h - mean)^2) + eps); or NULL.
  *   y        (M, K) output (h - mean) * rstd * weight + bias, rounded once; or NULL (with q).
- * Everything else as mxq_add_rmsnorm, errors included.  A first mean is taken in
- * fp32; the differences from it, their squares and both sums are in doubles.  A NaN or an
- * infinity in h makes its whole row NaN (scales 0xFF), as do values whose sum passes the
- * largest fp32 value; with eps = 0 the y of a row of equal values is unspecified.
+ * Everything else as mxq_add_rmsnorm, errors included.  A first mean and the differences
+ * from it are taken in fp32; their squares and both sums are in doubles.  y's value in fp32
+ * is what is rounded to bf16.  A NaN or an infinity in h makes its whole row NaN (scales
+ * 0xFF), as do values whose sum passes the largest fp32 value; with eps = 0 the y of a row
+ * of equal values, or of any whose rstd passes that value, is unspecified.
  */
 mxq_status mxq_add_layernorm(const void* x, const void* residual, const void* weight, const void* bias, int dtype,
                              int64_t M, int64_t K, float eps, void* h, void* y, void* q_e4m3, void* s_e8m0,
