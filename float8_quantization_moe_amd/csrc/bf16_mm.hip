@@ -588,7 +588,8 @@ __device__ __forceinline__ void mfmas(v4f (&acc)[8][TB], const Operands<TB>& f, 
 //   step 1   0 .. 2   slot + 2: 5 .. 7
 //                     (slot + 1 is there)
 //            2 .. 8   slot + 2: 8 .. 15; LDS: step 0 of slot + 1
-// A load has thirteen eighths of a step to arrive, a step being 1024 cycles of MFMAs.
+// A load has twenty-one (the first) to ten eighths (the last) of a step to arrive, a step being 1024 cycles of
+// MFMAs.
 constexpr int kLoads0 = 5, kLoads1 = 8;                  // loads issued by the end of each stretch
 
 template <int P, int TB, bool FIRST>

@@ -18,9 +18,9 @@
 //
 // Both are HBM bound: the row is read once and held in registers between its reductions and
 // its use, LANES threads a row with C chunks of 8 values each.  Sums go in a fixed order.
-// 65536 x 5120 bf16 with every output: 528 us, 5.7 TB/s; backward of 16640 x 5120 with dh: 120 us,
-// 5.7 TB/s.  The backward pass is near its VALU's bound too: with the differences and dy * w
-// made again after the sums it took 136 us, with the next row's loads ahead of that 142.
+// 65536 x 5120 bf16 with every output: 525 us, 5.8 TB/s; backward of 16640 x 5120 with dh: 122 us,
+// 5.6 TB/s.  The backward pass is near its VALU's bound too: with n and dy * w made again after
+// the sums it took 136 us, with the next row's loads ahead of that 142.
 #include "device_common.hpp"
 #include "internal.hpp"
 #include "mx_block.hpp"
@@ -34,9 +34,12 @@ namespace {
 constexpr int kWaves = 8;                                 // of a workgroup, at most
 // y is rounded to bf16 (itself or for its codes) from fp32 arithmetic that is good to two units of
 // 2^-24 or so; where the fp32 value is within this many of the middle between two bf16, the chunk is
-// computed again in doubles.  Of 3.4e8 values 1300 then differ from the exact ones' roundings and of
-// 10^7 blocks' scales none; 3800 and one or two without it; 13000 and one in steps of fp32 throughout
-// (65536 x 5120: 528 us; 515 with sums in fp32, 593 all in doubles).
+// computed again in doubles, rounded to fp32 first.  Of 3.4e8 values 1300 then differ from the exact
+// ones' roundings by way of fp32 and of 10^7 blocks' scales none; 3800 and one or two without it; 13000
+// and one in steps of fp32 throughout (65536 x 5120: 528 us; 515 with sums in fp32, 593 all in doubles).
+// Against the bf16 nearest to the exact values themselves it is 3900 and at times one: some 2600 of
+// 3.4e8 roundings to fp32 land on a middle from the wrong side.  fp32 rows take this path too, so that
+// their y is the same with and without codes.
 constexpr uint32_t kNear = 4;
 
 // Sums of two values over the LANES threads of a row, in all of them: a wave alone, else
@@ -158,8 +161,8 @@ void add_layernorm_kernel(const uint8_t* x, const uint8_t* r, const uint8_t* __r
                 for (int e = 0; e < 8; ++e) t[e] += a[e];
             }
         }
-        // (cut to 16 bits, so that the differences of bf16 values from it are exact: their roundings
-        // are alike over a row, and the mean lacked half a unit of them)
+        // (cut to 16 bits, so that the differences of bf16 values of its size from it are exact: their
+        // roundings are alike over a row, and the mean lacked half a unit of them)
         const float m0 = __uint_as_float(__float_as_uint(row_sums<LANES>(sum8(t), 0.0f, sh, 0).x / (float)K) & 0xFFFFFF00u);
         double d1 = 0.0, d2 = 0.0;
 #pragma unroll
@@ -471,7 +474,7 @@ hipError_t launch_add_layernorm_bwd(const void* h, const void* w, const float* m
     float* part_w = grid == 1 ? dw : part;
     float* part_b = grid == 1 || !db ? db : part + K;
     if (grid > 0) {
-    const bool nt = M * K * (f32 ? 4 : 2) * (dh ? 3 : 2) > kCacheBytes;
+        const bool nt = M * K * (f32 ? 4 : 2) * (dh ? 3 : 2) > kCacheBytes;
 #define MXQ_LAUNCH(T, L, C, NT)                                                                                        \
     hipLaunchKernelGGL((add_layernorm_bwd_kernel<T, L, C, NT>), dim3((unsigned)grid), dim3((L) < 256 ? 256 : (L)), 0, stream, \
                        (const uint8_t*)h, (const uint8_t*)w, mean, rstd, (const uint8_t*)dy, (const uint8_t*)dh, M,     \

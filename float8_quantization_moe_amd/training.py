@@ -105,7 +105,8 @@ def bf16_grouped_mm_dw(dy: torch.Tensor, x: torch.Tensor, group_end_offs: torch.
 
 # ----------------------------------------------------------- layer norm ---
 def add_layernorm(x: torch.Tensor, residual, weight: torch.Tensor, bias, eps: float, stream=None):
-    """(h, y, q, s, mean, rstd) of mxq_add_layernorm; h is x itself when there is no residual."""
+    """(h, y, q, s, mean, rstd) of mxq_add_layernorm; h is x itself when there is no residual.  The codes need K % 32 == 0:
+    other widths, and rows without codes, go to mxq.mxq_add_layernorm."""
     if stream is not None:
         with _on(stream, x):
             return add_layernorm(x, residual, weight, bias, eps)
@@ -197,7 +198,8 @@ def combine_rows(rows: torch.Tensor, pair_row: torch.Tensor, weights=None, strea
 
 
 def combine_rows_bwd(dout: torch.Tensor, rows: torch.Tensor, pair_row: torch.Tensor, weights=None, stream=None):
-    """(drows, dweights) of mxq_combine_rows_bwd; rows that no pair names are left as allocated."""
+    """(drows, dweights) of mxq_combine_rows_bwd; rows that no pair names are left as allocated.  drows alone, without reading
+    rows: mxq.mxq_combine_rows_bwd."""
     if stream is not None:
         with _on(stream, dout):
             return combine_rows_bwd(dout, rows, pair_row, weights)
