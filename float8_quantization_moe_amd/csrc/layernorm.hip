@@ -18,7 +18,7 @@
 //
 // Both are HBM bound: the row is read once and held in registers between its reductions and
 // its use, LANES threads a row with C chunks of 8 values each.  Sums go in a fixed order.
-// 65536 x 5120 bf16 with every output: 525 us, 5.8 TB/s; backward of 16640 x 5120 with dh: 122 us,
+// 65536 x 5120 bf16 with every output: 528 us, 5.7 TB/s; backward of 16640 x 5120 with dh: 122 us,
 // 5.6 TB/s.  The backward pass is near its VALU's bound too: with n and dy * w made again after
 // the sums it took 136 us, with the next row's loads ahead of that 142.
 #include "device_common.hpp"
